@@ -15,7 +15,9 @@ LIB = os.path.join(PKG, "libconvfwd.so")
 PROBE_SRC = "probe_ceilings.hip"
 PROBE_LIB = os.path.join(PKG, "libconvprobe.so")
 
-SOURCES = ["conv_plan.cpp", "pool_plan.cpp", "conv_host.cpp", "k_pool.hip", "k_convint.hip", "k_convint_rs.hip", "k_winograd.hip", "k_igemm.hip", "k_direct.hip", "k_halo.hip", "k_rowshift.hip", "k_pointwise.hip", "k_rowband.hip", "k_grouped.hip", "k_pointwise32.hip"]
+SOURCES = ["conv_plan.cpp", "pool_plan.cpp", "conv_host.cpp", "k_pool.hip", "k_convint.hip", "k_convint_rs.hip", "k_winograd.hip", "k_igemm.hip", "k_direct.hip", "k_halo.hip", "k_rowshift.hip", "k_pointwise.hip", "k_rowband.hip", "k_grouped.hip", "k_pointwise32.hip",
+           "linear_plan.cpp", "grad_clip_plan.cpp", "k_linear.hip", "k_linear_f16.hip", "k_linear_bf16.hip",
+           "k_linear_f32.hip", "k_linear_stream.hip", "k_linear_grad.hip", "k_grad_clip.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

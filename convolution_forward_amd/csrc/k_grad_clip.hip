@@ -1,0 +1,272 @@
+// Global gradient norm over many tensors and clipping (include/grad_clip.h).
+//
+// Pass 1 reads every gradient once: the tensors are cut into chunks (a power of
+// two of elements, never across tensors), dealt to at most 1024 workgroups in
+// turn, each of which sums |g|^p of its chunks in float64 and writes one partial.
+// Pass 2 reads and scales: every workgroup first adds the partials itself, in
+// one fixed order (1024 float64 from L2, cheaper than a launch between), so all
+// hold the same norm and coefficient, then scales its chunks.  Clipping in place
+// with a coefficient of 1 leaves memory alone.  Bound by memory: two reads and a
+// write of every element (the norm must be known before the first element can be
+// scaled), the second read from the last-level cache where the tensors fit it.
+// More than 112 tensors go in several launches, whose partials one workgroup joins.
+#include <math.h>
+
+#include <algorithm>
+
+#include "epilogue.h"
+#include "grad_clip_plan.h"
+
+namespace convfwd {
+
+namespace {
+
+struct ClipEntry {
+  const void* g;
+  void* out;
+  long long elems;
+  int dtype;
+  int first;  // its first chunk in this launch
+};
+
+struct ClipArgs {
+  double* partials;
+  float* norm;        // written by workgroup 0 where not null
+  long long count;    // partials to add (pass 2)
+  int n;              // tensors
+  int chunks;         // of all of them
+  int shift;          // log2 of the chunk
+  int kind;
+  float max_norm, eps;
+  ClipEntry t[kClipTable];
+};
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+
+template <typename E> struct VecOf;
+template <> struct VecOf<float> { typedef f32x4_t type; static constexpr int N = 4; };
+template <> struct VecOf<_Float16> { typedef f16x8_t type; static constexpr int N = 8; };
+template <> struct VecOf<__bf16> { typedef bf16x8_t type; static constexpr int N = 8; };
+
+// max that keeps NaN
+__device__ __forceinline__ double nan_max(double a, double b) {
+  return a != a ? a : (b > a || b != b) ? b : a;
+}
+
+// |g|^p joined into s.  A float32's square is exact in float64.
+__device__ __forceinline__ void add_power(double& s, float v, int kind) {
+  if (kind == GRAD_NORM_2) {
+    const double d = v;
+    s = fma(d, d, s);
+  } else if (kind == GRAD_NORM_1) {
+    s += (double)fabsf(v);
+  } else {
+    s = nan_max(s, (double)fabsf(v));
+  }
+}
+
+__device__ __forceinline__ double combine(double a, double b, int kind) {
+  return kind == GRAD_NORM_INF ? nan_max(a, b) : a + b;
+}
+
+// Sum over a workgroup of 256 threads in a fixed order; every thread gets it.
+__device__ __forceinline__ double reduce256(double s, int kind, double* lds) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s = combine(s, __shfl_xor(s, d), kind);
+  const int wave = threadIdx.x >> 6;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[wave] = s;
+  __syncthreads();
+  return combine(combine(lds[0], lds[1], kind), combine(lds[2], lds[3], kind), kind);
+}
+
+__device__ __forceinline__ int entry_of(const ClipArgs& a, int chunk) {
+  int lo = 0, hi = a.n - 1;  // the last entry whose first chunk is <= chunk
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.t[mid].first <= chunk) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// f(vector index) over whole vectors of [0, n), 4 loads in flight; then scalars.
+template <typename E, int KIND>
+__device__ __forceinline__ void chunk_power(const E* g, int n, double (&s)[4]) {
+  using V = VecOf<E>;
+  int done = 0;
+  if (reinterpret_cast<unsigned long long>(g) % 16 == 0) {
+    const typename V::type* v = reinterpret_cast<const typename V::type*>(g);
+    const int nv = n / V::N;
+    done = nv * V::N;
+    int i = threadIdx.x;
+    for (; i + 768 < nv; i += 1024) {
+      typename V::type q[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) q[u] = v[i + 256 * u];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) add_power(s[u], (float)q[u][e], KIND);
+    }
+    for (; i < nv; i += 256) {
+      const typename V::type q = v[i];
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) add_power(s[0], (float)q[e], KIND);
+    }
+  }
+  for (int i = done + threadIdx.x; i < n; i += 256) add_power(s[0], (float)g[i], KIND);
+}
+
+template <int KIND>
+__global__ __launch_bounds__(256) void clip_norm_kernel(const ClipArgs a) {
+  __shared__ double lds[4];
+  double s[4] = {0, 0, 0, 0};
+  for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+    const ClipEntry& t = a.t[entry_of(a, c)];
+    const long long at = (long long)(c - t.first) << a.shift;
+    const int n = (int)min((long long)1 << a.shift, t.elems - at);
+    if (t.dtype == CONV_F32) chunk_power<float, KIND>(static_cast<const float*>(t.g) + at, n, s);
+    else if (t.dtype == CONV_F16) chunk_power<_Float16, KIND>(static_cast<const _Float16*>(t.g) + at, n, s);
+    else chunk_power<__bf16, KIND>(static_cast<const __bf16*>(t.g) + at, n, s);
+  }
+  const double v = reduce256(combine(combine(s[0], s[1], KIND), combine(s[2], s[3], KIND), KIND),
+                             KIND, lds);
+  if (threadIdx.x == 0) a.partials[blockIdx.x] = v;
+}
+
+// All partials into the first one (several launches' worth).
+__global__ __launch_bounds__(256) void clip_join_kernel(const double* in, double* out,
+                                                        long long count, int kind) {
+  __shared__ double lds[4];
+  double s = 0;
+  for (long long i = threadIdx.x; i < count; i += 256) s = combine(s, in[i], kind);
+  s = reduce256(s, kind, lds);
+  if (threadIdx.x == 0) *out = s;
+}
+
+template <typename E>
+__device__ __forceinline__ void chunk_scale(const E* g, E* out, int n, float c) {
+  using V = VecOf<E>;
+  int done = 0;
+  if ((reinterpret_cast<unsigned long long>(g) | reinterpret_cast<unsigned long long>(out)) % 16 == 0) {
+    const typename V::type* v = reinterpret_cast<const typename V::type*>(g);
+    typename V::type* o = reinterpret_cast<typename V::type*>(out);
+    const int nv = n / V::N;
+    done = nv * V::N;
+    int i = threadIdx.x;
+    for (; i + 768 < nv; i += 1024) {
+      typename V::type q[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) q[u] = v[i + 256 * u];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) q[u][e] = (E)((float)q[u][e] * c);
+        store_out(o + i + 256 * u, q[u]);
+      }
+    }
+    for (; i < nv; i += 256) {
+      typename V::type q = v[i];
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) q[e] = (E)((float)q[e] * c);
+      store_out(o + i, q);
+    }
+  }
+  for (int i = done + threadIdx.x; i < n; i += 256) out[i] = (E)((float)g[i] * c);
+}
+
+__global__ __launch_bounds__(256) void clip_scale_kernel(const ClipArgs a) {
+  __shared__ double lds[4];
+  double s = 0;
+  for (long long i = threadIdx.x; i < a.count; i += 256) s = combine(s, a.partials[i], a.kind);
+  s = reduce256(s, a.kind, lds);
+  const double norm = a.kind == GRAD_NORM_2 ? sqrt(s) : s;
+  const double q = (double)a.max_norm / (norm + (double)a.eps);
+  const float c = q >= 1.0 ? 1.0f : (float)q;  // NaN stays NaN
+  if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
+  for (int k = blockIdx.x; k < a.chunks; k += gridDim.x) {
+    const ClipEntry& t = a.t[entry_of(a, k)];
+    if (c == 1.0f && t.out == t.g) continue;
+    const long long at = (long long)(k - t.first) << a.shift;
+    const int n = (int)min((long long)1 << a.shift, t.elems - at);
+    if (t.dtype == CONV_F32)
+      chunk_scale(static_cast<const float*>(t.g) + at, static_cast<float*>(t.out) + at, n, c);
+    else if (t.dtype == CONV_F16)
+      chunk_scale(static_cast<const _Float16*>(t.g) + at, static_cast<_Float16*>(t.out) + at, n, c);
+    else
+      chunk_scale(static_cast<const __bf16*>(t.g) + at, static_cast<__bf16*>(t.out) + at, n, c);
+  }
+}
+
+// The launch's table: tensors [i0, i0 + kClipTable) that hold elements.
+void fill(const grad_clip_problem* p, const ClipPlan& pl, int64_t i0, ClipArgs* a) {
+  a->n = 0;
+  int64_t chunks = 0;
+  for (int64_t i = i0; i < std::min<int64_t>(p->count, i0 + kClipTable); ++i) {
+    const grad_tensor& t = p->tensors[i];
+    if (t.elems == 0) continue;
+    a->t[a->n++] = {t.g, t.out, (long long)t.elems, t.dtype, (int)chunks};
+    chunks += ceil_div(t.elems, pl.chunk);
+  }
+  a->chunks = (int)chunks;
+}
+
+}  // namespace
+
+}  // namespace convfwd
+
+using namespace convfwd;
+
+extern "C" int grad_clip(const grad_clip_problem* p, float* norm, void* scratch,
+                         uint64_t scratch_bytes, void* stream) {
+  const int st = grad_clip_check(p, norm, scratch, scratch_bytes);
+  if (st) return st;
+  ClipPlan pl;
+  clip_validate(p, &pl);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  double* partials = static_cast<double*>(scratch);
+  ClipArgs a{};
+  a.kind = p->kind;
+  a.max_norm = p->max_norm;
+  a.eps = p->eps;
+  a.shift = 63 - __builtin_clzll((unsigned long long)pl.chunk);
+  int64_t count = 0;
+  for (int64_t l = 0; l < pl.launches; ++l) {
+    fill(p, pl, l * kClipTable, &a);
+    if (a.chunks == 0) continue;
+    const int grid = std::min(a.chunks, kClipPartials);
+    a.partials = partials + count;
+    if (a.kind == GRAD_NORM_2)
+      hipLaunchKernelGGL((clip_norm_kernel<GRAD_NORM_2>), dim3(grid), dim3(256), 0, s, a);
+    else if (a.kind == GRAD_NORM_1)
+      hipLaunchKernelGGL((clip_norm_kernel<GRAD_NORM_1>), dim3(grid), dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((clip_norm_kernel<GRAD_NORM_INF>), dim3(grid), dim3(256), 0, s, a);
+    if (hipGetLastError() != hipSuccess) return CONV_ERR_DEVICE;
+    count += grid;
+  }
+  a.partials = partials;
+  a.count = count;
+  if (count > kClipPartials) {
+    double* one = partials + pl.launches * kClipPartials;
+    hipLaunchKernelGGL(clip_join_kernel, dim3(1), dim3(256), 0, s, partials, one, (long long)count, a.kind);
+    if (hipGetLastError() != hipSuccess) return CONV_ERR_DEVICE;
+    a.partials = one;
+    a.count = 1;
+  }
+  a.norm = norm;
+  bool out = false;
+  for (int64_t i = 0; i < p->count && !out; ++i) out = p->tensors[i].elems > 0 && p->tensors[i].out;
+  for (int64_t l = 0; l < (out ? pl.launches : 1); ++l) {
+    if (pl.launches > 1 || l > 0) fill(p, pl, l * kClipTable, &a);
+    if (!out) a.chunks = 0;
+    if (a.chunks == 0 && !a.norm) continue;
+    const int grid = std::max(1, std::min(a.chunks, 2048));
+    hipLaunchKernelGGL(clip_scale_kernel, dim3(grid), dim3(256), 0, s, a);
+    if (hipGetLastError() != hipSuccess) return CONV_ERR_DEVICE;
+    a.norm = nullptr;
+  }
+  return CONV_OK;
+}

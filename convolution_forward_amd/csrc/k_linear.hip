@@ -1,0 +1,291 @@
+// Launch half of include/linear.h: runs the shape-only plans of linear_plan.cpp
+// as gfx950 launches on the caller's stream.  Nothing here allocates, frees or
+// synchronises.
+#include <string.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "linear_args.h"
+#include "linear_plan.h"
+
+using namespace convfwd;
+
+namespace {
+
+template <typename T>
+T* at(T* p, int64_t off, int es) {
+  typedef std::conditional_t<std::is_const_v<T>, const char, char> C;
+  return p ? static_cast<T*>(static_cast<C*>(p) + off * es) : nullptr;
+}
+
+bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// An operand row stride of whole 16-byte pieces from an aligned base.
+bool rows16(const void* p, int64_t ld, int es) { return al16(p) && ld * es % 16 == 0; }
+
+hipError_t product(int dtype, const ProductArgs& a, int tile, int layout, bool gated, bool dma,
+                   hipStream_t s) {
+  if (dtype == CONV_F16) return launch_product<_Float16>(a, tile, layout, gated, dma, s);
+  if (dtype == CONV_BF16) return launch_product<__bf16>(a, tile, layout, gated, dma, s);
+  return launch_product<float>(a, tile, layout, gated, dma, s);
+}
+
+hipError_t stream_product(int dtype, const ProductArgs& a, int blocks16, bool gated, bool vec,
+                          hipStream_t s) {
+  if (dtype == CONV_F16) return launch_stream<_Float16>(a, blocks16, gated, vec, s);
+  if (dtype == CONV_BF16) return launch_stream<__bf16>(a, blocks16, gated, vec, s);
+  return launch_stream<float>(a, blocks16, gated, vec, s);
+}
+
+hipError_t join(int dtype, const JoinArgs& a, bool gated, hipStream_t s) {
+  if (dtype == CONV_F16) return launch_join<_Float16>(a, gated, s);
+  if (dtype == CONV_BF16) return launch_join<__bf16>(a, gated, s);
+  return launch_join<float>(a, gated, s);
+}
+
+hipError_t dz_pass(int dtype, const DzArgs& a, bool gated, int chunks, hipStream_t s) {
+  if (dtype == CONV_F16) return launch_dz<_Float16>(a, gated, chunks, s);
+  if (dtype == CONV_BF16) return launch_dz<__bf16>(a, gated, chunks, s);
+  return launch_dz<float>(a, gated, chunks, s);
+}
+
+hipError_t sums_pass(int dtype, const SumsArgs& a, hipStream_t s) {
+  if (dtype == CONV_F16) return launch_sums<_Float16>(a, s);
+  if (dtype == CONV_BF16) return launch_sums<__bf16>(a, s);
+  return launch_sums<float>(a, s);
+}
+
+// Whether the operands can go to LDS directly: aligned bases, row strides and
+// contiguous extents of whole 16-byte pieces, or rows padded to that with zeros.
+bool direct(const ProductShape& s, const ProductArgs& a, int es, bool p_padded, bool q_padded) {
+  for (int i = 0; i < 2; ++i) {
+    if (a.P[i] && !rows16(a.P[i], a.ldp, es)) return false;
+    if (a.Q[i] && !rows16(a.Q[i], a.ldq, es)) return false;
+  }
+  if (!p_padded && (s.pt ? s.R : s.K) * es % 16 != 0) return false;
+  return q_padded || (s.qt ? s.C : s.K) * es % 16 == 0;
+}
+
+// Runs one planned product; a's operands and epilogue are set.
+hipError_t run_product(const ProductShape& s, int dtype, ProductArgs& a, bool p_padded,
+                       bool q_padded, void* planes, hipStream_t st) {
+  const int es = (int)dtype_size(dtype);
+  const ProductPlan pl = plan_product(s, es);
+  a.R = (int)s.R; a.C = (int)s.C; a.K = (int)s.K;
+  a.nseg = s.nseg; a.nz = s.nz;
+  a.ktiles = (int)pl.ktiles; a.splits = pl.splits; a.per_split = (int)pl.per_split;
+  a.planes = static_cast<float*>(planes);
+  a.plane_ld = pl.plane_ld;
+  a.e.R = a.R;
+  const bool dma = direct(s, a, es, p_padded, q_padded);
+  if (pl.tile == TILE_STREAM) return stream_product(dtype, a, pl.stream_t, s.gated, dma, st);
+  const int layout = s.pt ? (s.qt ? 2 : 1) : 0;
+  hipError_t e = product(dtype, a, pl.tile, layout, s.gated, dma, st);
+  if (e != hipSuccess || pl.splits == 1) return e;
+  JoinArgs j{};
+  j.planes = a.planes;
+  j.plane_ld = pl.plane_ld;
+  j.plane_stride = pl.plane_ld * s.C * s.nz * (s.gated ? 2 : 1);
+  j.splits = pl.splits;
+  j.C = a.C;
+  j.nz = s.nz;
+  j.e = a.e;
+  return join(dtype, j, s.gated, st);
+}
+
+int status(hipError_t e) { return e == hipSuccess ? CONV_OK : CONV_ERR_DEVICE; }
+
+}  // namespace
+
+extern "C" {
+
+int linear_forward(const linear_problem* p, int dtype, const void* x, const void* w, const void* b,
+                   const void* r, void* y, void* z, void* scratch, uint64_t scratch_bytes,
+                   void* stream) {
+  const int st = linear_check(p, dtype, x, w, b, r, y, z, scratch, scratch_bytes);
+  if (st) return st;
+  LinearGeo g;
+  linear_validate(p, dtype, &g);
+  if (g.m == 0) return CONV_OK;
+  ProductArgs a{};
+  a.P[0] = at(w, p->w_off, g.es);
+  a.Q[0] = at(x, p->x_off, g.es);
+  a.ldp = g.ldw; a.ldq = g.ldx;
+  LinEpilogue& e = a.e;
+  e.bias[0] = p->has_bias ? at(b, p->b_off, g.es) : nullptr;
+  e.res = p->has_residual ? at(r, p->r_off, g.es) : nullptr;
+  e.res_mode = p->has_residual;
+  e.out[0] = at(y, p->y_off, g.es);
+  e.save[0] = p->save_z ? at(z, p->z_off, g.es) : nullptr;
+  e.ldo = g.ldy; e.ldres = g.ldr; e.ldsave = g.ldz;
+  e.act = p->activation; e.alpha = p->act_alpha; e.beta = p->act_beta;
+  e.vec = rows16(e.out[0], g.ldy, g.es) && (!e.bias[0] || al16(e.bias[0])) &&
+          (!e.res || rows16(e.res, g.ldr, g.es)) && (!e.save[0] || rows16(e.save[0], g.ldz, g.es));
+  return status(run_product(linear_product(p, g), dtype, a, false, false, scratch,
+                            static_cast<hipStream_t>(stream)));
+}
+
+int gated_forward(const gated_problem* p, int dtype, const void* x, const void* wg, const void* wu,
+                  const void* bg, const void* bu, void* h, void* pg, void* pu, void* scratch,
+                  uint64_t scratch_bytes, void* stream) {
+  const int st = gated_check(p, dtype, x, wg, wu, bg, bu, h, pg, pu, scratch, scratch_bytes);
+  if (st) return st;
+  GatedGeo g;
+  gated_validate(p, dtype, &g);
+  if (g.m == 0) return CONV_OK;
+  ProductArgs a{};
+  a.P[0] = at(wg, p->wg_off, g.es);
+  a.P[1] = at(wu, p->wu_off, g.es);
+  a.Q[0] = at(x, p->x_off, g.es);
+  a.ldp = g.ldw; a.ldq = g.ldx;
+  LinEpilogue& e = a.e;
+  if (p->has_bias) {
+    e.bias[0] = at(bg, p->bg_off, g.es);
+    e.bias[1] = at(bu, p->bu_off, g.es);
+  }
+  e.out[0] = at(h, p->h_off, g.es);
+  if (p->save_p) {
+    e.save[0] = at(pg, p->pg_off, g.es);
+    e.save[1] = at(pu, p->pu_off, g.es);
+  }
+  e.ldo = g.ldh; e.ldsave = g.ldp;
+  e.act = p->activation; e.alpha = p->act_alpha; e.beta = p->act_beta;
+  e.vec = rows16(e.out[0], g.ldh, g.es) &&
+          (!e.bias[0] || (al16(e.bias[0]) && al16(e.bias[1]))) &&
+          (!e.save[0] || (rows16(e.save[0], g.ldp, g.es) && al16(e.save[1])));
+  return status(run_product(gated_product(p, g), dtype, a, false, false, scratch,
+                            static_cast<hipStream_t>(stream)));
+}
+
+int linear_backward(const linear_problem* p, int dtype, const void* x, const void* w, const void* z,
+                    const void* dy, void* dx, void* dw, void* db, void* dr, void* scratch,
+                    uint64_t scratch_bytes, void* stream) {
+  const int st = linear_backward_check(p, dtype, x, w, z, dy, dx, dw, db, dr, scratch, scratch_bytes);
+  if (st) return st;
+  LinearGeo g;
+  linear_validate(p, dtype, &g);
+  const BackwardScratch sc = linear_backward_scratch(p, g);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* sb = static_cast<char*>(scratch);
+  const bool act = p->activation != CONV_ACT_IDENTITY;
+  const bool dr_is_dy = dr && (!act || p->has_residual == LINEAR_RES_AFTER);
+  dy = at(dy, p->dy_off, g.es);
+  dr = at(dr, p->dr_off, g.es);
+  if (dr == dy && dr_is_dy) dr = nullptr;  // in place and unchanged
+  const bool need_dz = act && (dx || dw);
+  hipError_t e = hipSuccess;
+  if (need_dz || db || dr) {
+    const ColsumPlan cp = plan_colsum(g.m, g.n);
+    DzArgs a{};
+    a.dy = dy;
+    a.z[0] = act && !(!need_dz && !db && dr_is_dy) ? at(z, p->z_off, g.es) : nullptr;
+    a.act = a.z[0] ? p->activation : CONV_ACT_IDENTITY;
+    a.dz = need_dz ? sb + sc.dz : nullptr;
+    a.dr = dr;
+    a.dr_is_dy = dr_is_dy;
+    a.sums = db ? reinterpret_cast<float*>(sb + sc.sums) : nullptr;
+    a.ldy = g.ldy; a.ldz = g.ldz; a.lddz = sc.dz_ld; a.lddr = g.lddr;
+    a.m = g.m; a.rows = cp.rows;
+    a.n = (int)g.n; a.np = (int)round_up(g.n, 8);
+    a.alpha = p->act_alpha; a.beta = p->act_beta;
+    a.vec = rows16(dy, g.ldy, g.es) && (!a.z[0] || rows16(a.z[0], g.ldz, g.es)) &&
+            (!dr || rows16(dr, g.lddr, g.es));
+    e = dz_pass(dtype, a, false, (int)cp.chunks, s);
+    if (e == hipSuccess && db) {
+      SumsArgs q{};
+      q.sums = a.sums;
+      q.db[0] = at(db, p->db_off, g.es);
+      q.chunks = (int)cp.chunks; q.n = a.n; q.np = a.np; q.parts = 1;
+      e = sums_pass(dtype, q, s);
+    }
+  }
+  const void* d = act ? static_cast<const void*>(sb + sc.dz) : dy;
+  const int64_t ldd = act ? sc.dz_ld : g.ldy;
+  if (e == hipSuccess && dx && g.m > 0) {
+    ProductArgs a{};
+    a.P[0] = at(w, p->w_off, g.es);
+    a.Q[0] = d;
+    a.ldp = g.ldw; a.ldq = ldd;
+    a.e.out[0] = at(dx, p->dx_off, g.es);
+    a.e.ldo = g.lddx;
+    a.e.vec = rows16(a.e.out[0], g.lddx, g.es);
+    e = run_product(linear_dx_product(p, g), dtype, a, false, act, sb + sc.planes, s);
+  }
+  if (e == hipSuccess && dw) {
+    ProductArgs a{};
+    const void* xb = at(x, p->x_off, g.es);
+    a.P[0] = g.kn ? d : xb;
+    a.Q[0] = g.kn ? xb : d;
+    a.ldp = g.kn ? ldd : g.ldx;
+    a.ldq = g.kn ? g.ldx : ldd;
+    a.e.out[0] = at(dw, p->dw_off, g.es);
+    a.e.ldo = g.lddw;
+    a.e.vec = rows16(a.e.out[0], g.lddw, g.es);
+    e = run_product(linear_dw_product(p, g), dtype, a, act && g.kn, act && !g.kn, sb + sc.planes, s);
+  }
+  return status(e);
+}
+
+int gated_backward(const gated_problem* p, int dtype, const void* x, const void* wg, const void* wu,
+                   const void* pg, const void* pu, const void* dh, void* dx, void* dwg, void* dwu,
+                   void* dbg, void* dbu, void* scratch, uint64_t scratch_bytes, void* stream) {
+  const int st = gated_backward_check(p, dtype, x, wg, wu, pg, pu, dh, dx, dwg, dwu, dbg, dbu,
+                                      scratch, scratch_bytes);
+  if (st) return st;
+  GatedGeo g;
+  gated_validate(p, dtype, &g);
+  const BackwardScratch sc = gated_backward_scratch(p, g);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* sb = static_cast<char*>(scratch);
+  const ColsumPlan cp = plan_colsum(g.m, g.f);
+  DzArgs a{};
+  a.dy = at(dh, p->dh_off, g.es);
+  a.z[0] = at(pg, p->pg_off, g.es);
+  a.z[1] = at(pu, p->pu_off, g.es);
+  a.dz = sb + sc.dz;
+  a.sums = dbg ? reinterpret_cast<float*>(sb + sc.sums) : nullptr;
+  a.ldy = g.ldh; a.ldz = g.ldp; a.lddz = sc.dz_ld;
+  a.m = g.m; a.rows = cp.rows;
+  a.n = (int)g.f; a.np = (int)round_up(g.f, 8);
+  a.act = p->activation; a.alpha = p->act_alpha; a.beta = p->act_beta;
+  a.vec = rows16(a.dy, g.ldh, g.es) && rows16(a.z[0], g.ldp, g.es) && al16(a.z[1]);
+  hipError_t e = dz_pass(dtype, a, true, (int)cp.chunks, s);
+  if (e == hipSuccess && dbg) {
+    SumsArgs q{};
+    q.sums = a.sums;
+    q.db[0] = at(dbg, p->dbg_off, g.es);
+    q.db[1] = at(dbu, p->dbu_off, g.es);
+    q.chunks = (int)cp.chunks; q.n = a.n; q.np = a.np; q.parts = 2;
+    e = sums_pass(dtype, q, s);
+  }
+  const char* dg = sb + sc.dz;
+  const char* du = dg + (int64_t)a.np * g.es;
+  if (e == hipSuccess && dx && g.m > 0) {
+    ProductArgs q{};
+    q.P[0] = at(wg, p->wg_off, g.es);
+    q.P[1] = at(wu, p->wu_off, g.es);
+    q.Q[0] = dg;
+    q.Q[1] = du;
+    q.ldp = g.ldw; q.ldq = sc.dz_ld;
+    q.e.out[0] = at(dx, p->dx_off, g.es);
+    q.e.ldo = g.lddx;
+    q.e.vec = rows16(q.e.out[0], g.lddx, g.es);
+    e = run_product(gated_dx_product(p, g), dtype, q, false, true, sb + sc.planes, s);
+  }
+  if (e == hipSuccess && dwg) {
+    ProductArgs q{};
+    q.P[0] = at(x, p->x_off, g.es);
+    q.Q[0] = dg;
+    q.Q[1] = du;
+    q.ldp = g.ldx; q.ldq = sc.dz_ld;
+    q.e.out[0] = at(dwg, p->dwg_off, g.es);
+    q.e.out[1] = at(dwu, p->dwu_off, g.es);
+    q.e.ldo = g.lddw;
+    q.e.vec = rows16(q.e.out[0], g.lddw, g.es) && al16(q.e.out[1]);
+    e = run_product(gated_dw_product(p, g), dtype, q, false, true, sb + sc.planes, s);
+  }
+  return status(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,51 @@
+// Instantiation and launch of the tile kernel for one element type; included by
+// one source file per type.
+#pragma once
+
+#include "linear_plan.h"
+#include "linear_tile.h"
+
+namespace convfwd {
+
+template <typename E, bool PT, bool QT, int BR, int BC, int WVR, int WVC, bool DMA, bool GATED>
+static hipError_t launch_tile(ProductArgs a, hipStream_t s) {
+  a.ntr = (a.R + (GATED ? BR / 2 : BR) - 1) / (GATED ? BR / 2 : BR);
+  a.ntc = (a.C + BC - 1) / BC;
+  const int grid = a.ntr * a.ntc * a.nz * a.splits;
+  hipLaunchKernelGGL((linear_tile_kernel<E, PT, QT, BR, BC, WVR, WVC, DMA, GATED>), dim3(grid),
+                     dim3(WVR * WVC * 64), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename E, bool PT, bool QT>
+static hipError_t launch_layout(const ProductArgs& a, int tile, bool dma, hipStream_t s) {
+  if constexpr (sizeof(E) == 2) {
+    if (tile == TILE_256 && dma) return launch_tile<E, PT, QT, 256, 256, 2, 4, true, false>(a, s);
+  }
+  if (tile == TILE_64)
+    return dma ? launch_tile<E, PT, QT, 64, 64, 2, 2, true, false>(a, s)
+               : launch_tile<E, PT, QT, 64, 64, 2, 2, false, false>(a, s);
+  return dma ? launch_tile<E, PT, QT, 128, 128, 2, 2, true, false>(a, s)
+             : launch_tile<E, PT, QT, 128, 128, 2, 2, false, false>(a, s);
+}
+
+template <typename E>
+hipError_t launch_product(const ProductArgs& a, int tile, int layout, bool gated, bool dma,
+                          hipStream_t s) {
+  if (gated) {
+    if constexpr (sizeof(E) == 2) {
+      if (tile == TILE_256 && dma)
+        return launch_tile<E, false, false, 256, 256, 2, 4, true, true>(a, s);
+    }
+    if (tile == TILE_64)
+      return dma ? launch_tile<E, false, false, 64, 64, 1, 4, true, true>(a, s)
+                 : launch_tile<E, false, false, 64, 64, 1, 4, false, true>(a, s);
+    return dma ? launch_tile<E, false, false, 128, 128, 2, 2, true, true>(a, s)
+               : launch_tile<E, false, false, 128, 128, 2, 2, false, true>(a, s);
+  }
+  if (layout == 0) return launch_layout<E, false, false>(a, tile, dma, s);
+  if (layout == 1) return launch_layout<E, true, false>(a, tile, dma, s);
+  return launch_layout<E, true, true>(a, tile, dma, s);
+}
+
+}  // namespace convfwd

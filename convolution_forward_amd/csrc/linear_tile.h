@@ -1,0 +1,404 @@
+// Tiled matrix product on MFMA for gfx950: out[c][r] = sum_k P(r, k) Q(c, k),
+// float32 sums, with the epilogue of linear_epilogue.h.  One kernel template for
+// the linear layer, the gated projections and every gradient: each operand is
+// k-major (rows run along the contraction) or transposed (rows of constant k).
+//
+//  * A workgroup owns BR x BC outputs; P rows feed MFMA's A operand and Q rows
+//    its B operand, so a lane ends with 4 consecutive r of one c.
+//  * Contraction step: 128 bytes of k (64 halves, 32 floats).  Both operands are
+//    staged in LDS, two buffers; step t + 1 is in flight while t is multiplied.
+//  * DMA: global to LDS directly (16 bytes a lane, no registers), for rows of
+//    whole aligned 16-byte vectors; descriptor range checks give zeros past the
+//    last row and, per lane, past the end of k.  Otherwise (odd strides, sizes or
+//    bases) the vectors are gathered through registers, element by element where
+//    one crosses an end.
+//  * k-major image in LDS: 128-byte rows, 16-byte piece p of row i kept at slot
+//    p ^ (i & 7): the 16 rows of a fragment read hit all banks.  Transposed
+//    image: one row per k, kept as it lies, in 32-byte units (16 halves) moved to
+//    unit u ^ h(k); fragments come out transposed by the LDS transpose read
+//    (16-bit), or are read element by element (float32, 64-byte units).
+//  * Epilogue through LDS, wave by wave: 16 rows c of WR sums, read back as runs
+//    of 8 consecutive r, so that loads and stores are 16-byte pieces of rows.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "linear_epilogue.h"
+#include "mfma16.h"
+
+namespace convfwd {
+
+namespace lin {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char lds_char;
+
+constexpr int kOob = (int)0x80000000;  // byte offset past every descriptor's range
+
+__device__ __forceinline__ unsigned lds_addr(const void* p) {
+  return (unsigned)(unsigned long long)(lds_char*)const_cast<void*>(p);
+}
+
+// Raw buffer descriptor over [p, p + bytes), wave-uniform.
+__device__ __forceinline__ i32x4 make_rsrc(const char* p, long long bytes) {
+  const unsigned long long v = reinterpret_cast<unsigned long long>(p);
+  const int n = (int)min(max(bytes, 0LL), 0x7fffffffLL);
+  i32x4 r;
+  r[0] = __builtin_amdgcn_readfirstlane((int)v);
+  r[1] = __builtin_amdgcn_readfirstlane((int)(v >> 32) & 0xffff);
+  r[2] = __builtin_amdgcn_readfirstlane(n);
+  r[3] = 0x00020000;
+  return r;
+}
+
+// 16 bytes per lane from rsrc + voff to LDS at lds + 16 * lane (out of range:
+// zeros).  Nothing is returned to registers; wait with vm_wait before reading.
+__device__ __forceinline__ void dma16(i32x4 rsrc, int voff, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(voff), "s"(rsrc) : "memory", "m0");
+}
+
+template <int N>
+__device__ __forceinline__ void vm_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
+}
+__device__ __forceinline__ void lds_wait() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Unit rotation of the transposed image (see above).
+template <typename E>
+__device__ __forceinline__ int unit_xor(int k) {
+  if constexpr (sizeof(E) == 2) return (k & 3) | (((k >> 3) & 3) << 2);
+  return (k >> 2) & 3;
+}
+
+// One operand's tile: ROWS rows (r or c) x 128 bytes of k.
+template <typename E, int ROWS, bool T, int NT>
+struct Tile {
+  static constexpr int EB = (int)sizeof(E);
+  static constexpr int EPC = 16 / EB;              // elements per 16-byte piece
+  static constexpr int BKE = 128 / EB;             // k per step
+  static constexpr int ITEMS = ROWS * 8 / NT;      // pieces per thread
+  static constexpr int ROWB = T ? ROWS * EB : 128; // bytes of an LDS row
+  static constexpr int CPR = ROWB / 16;            // pieces per LDS row
+  static constexpr int UNIT = EB == 2 ? 2 : 4;     // pieces per unit (transposed)
+  static constexpr int UNITS = CPR / UNIT;
+  static constexpr int BYTES = ROWS * 128;
+  static_assert(ROWS * 8 % NT == 0, "whole pieces per thread");
+
+  // LDS row and global piece (within the row) of item i
+  static __device__ __forceinline__ void item(int i, int tid, int* row, int* piece) {
+    const int q = i * NT + tid;
+    const int lr = q / CPR, slot = q % CPR;
+    *row = lr;
+    if constexpr (T)
+      *piece = (((slot / UNIT) ^ (unit_xor<E>(lr) & (UNITS - 1))) * UNIT) | (slot % UNIT);
+    else
+      *piece = slot ^ (lr & 7);
+  }
+
+  // A 16-row fragment at row0 (a multiple of 16), 64 bytes of k (16-bit: 32 k,
+  // float32: 16 k; lane group g holds k 8g.. or 4g..), step half j.
+  typedef std::conditional_t<EB == 2, s16x8, f32x4> Frag;
+  static __device__ __forceinline__ Frag frag(const char* base, int row0, int j, int lane) {
+    const int l = lane & 15, g = lane >> 4;
+    if constexpr (!T) {
+      return *reinterpret_cast<const Frag*>(base + (row0 + l) * 128 + (((4 * j + g) ^ (l & 7)) << 4));
+    } else if constexpr (EB == 2) {
+      const int i = l >> 2;
+      const int u = (row0 / 16) ^ ((i | (g << 2)) & (UNITS - 1));
+      const char* p = base + (32 * j + 8 * g + i) * ROWB + u * 32 + (l & 3) * 8;
+      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)const_cast<char*>(p));
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s16x4*)const_cast<char*>(p + 4 * ROWB));
+      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      Frag f;
+      const int u = (row0 / 16) ^ (g & (UNITS - 1));
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        f[s] = *reinterpret_cast<const float*>(base + (16 * j + 4 * g + s) * ROWB + u * 64 + l * 4);
+      return f;
+    }
+  }
+};
+
+template <typename E, typename F>
+__device__ __forceinline__ mfma_f32x4 multiply(const F& p, const F& q, mfma_f32x4 c) {
+  if constexpr (sizeof(E) == 2) {
+    return mfma_16x16x32<E>(p, q, c);
+  } else {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x4f32(p[s], q[s], c, 0, 0, 0);
+    return c;
+  }
+}
+
+// One 16-byte piece gathered element by element where it crosses an end.
+template <typename E, bool T>
+__device__ __forceinline__ i32x4 gather(const E* base, long long ld, int row, int piece,
+                                        long long nrow, long long nk) {
+  constexpr int EPC = 16 / (int)sizeof(E);
+  struct __attribute__((packed, aligned(sizeof(E)))) U { i32x4 v; };
+  const long long at = (long long)piece * EPC;
+  const long long have = (T ? nrow : nk) - at;  // valid elements of the row from here
+  const bool ok = T ? row < nk : row < nrow;
+  const E* p = base + (long long)row * ld + at;
+  if (ok && have >= EPC) return reinterpret_cast<const U*>(p)->v;
+  union { E e[EPC]; i32x4 v; } u;
+  u.v = i32x4{0, 0, 0, 0};
+  if (ok) {
+#pragma unroll
+    for (int i = 0; i < EPC; ++i)
+      if (i < have) u.e[i] = p[i];
+  }
+  return u.v;
+}
+
+}  // namespace lin
+
+// WVR x WVC waves; GATED: P's rows are gate and up rows, side by side within
+// each wave's share.
+template <typename E, bool PT, bool QT, int BR, int BC, int WVR, int WVC, bool DMA, bool GATED>
+__global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const ProductArgs a) {
+  using namespace lin;
+  constexpr int NT = WVR * WVC * 64;
+  constexpr int WR = BR / WVR, WC = BC / WVC, NI = WR / 16, NJ = WC / 16;
+  constexpr int HW = WR / 2;  // gated: rows of each kind per wave
+  using TP = Tile<E, BR, PT, NT>;
+  using TQ = Tile<E, BC, QT, NT>;
+  constexpr int STAGE = TP::BYTES + TQ::BYTES;
+  constexpr int EPW = 16 * (WR + 4) * 4;  // epilogue bytes per wave
+  constexpr int SMEM = 2 * STAGE > NT / 64 * EPW ? 2 * STAGE : NT / 64 * EPW;
+  static_assert(!GATED || (!PT && !QT), "gated weights are k-major");
+  __shared__ __attribute__((aligned(1024))) char smem[SMEM];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave % WVR, wc = wave / WVR;
+
+  // tile of this workgroup: bands of 8 tiles along c, so that the tiles an XCD
+  // runs at one time share few rows of P and Q
+  const int per = a.ntr * a.ntc;
+  const int id = xcd_logical(blockIdx.x, gridDim.x);
+  const int batch = id / per;  // split * nz + z
+  const int z = batch % a.nz, split = batch / a.nz;
+  const int idx = id - batch * per;
+  const int band = idx / (8 * a.ntr), bw = min(8, a.ntc - 8 * band);
+  const int in = idx - band * 8 * a.ntr;
+  const int tr = in / bw, tc = 8 * band + in - tr * bw;
+  const int r0 = tr * (GATED ? BR / 2 : BR);
+  const long long c0 = (long long)tc * BC;
+  const long long nr = a.R - r0, nc = a.C - c0;  // rows left
+
+  const int t_all = a.ktiles * a.nseg;
+  const int t0 = split * a.per_split, t1 = min(t0 + a.per_split, t_all);
+
+  mfma_f32x4 acc[NI][NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_f32x4{0, 0, 0, 0};
+
+  // per-item offsets: constant over the contraction
+  int poff[TP::ITEMS], qoff[TQ::ITEMS], pk[TP::ITEMS], qk[TQ::ITEMS];
+#pragma unroll
+  for (int i = 0; i < TP::ITEMS; ++i) {
+    int row, piece;
+    TP::item(i, tid, &row, &piece);
+    if constexpr (GATED) row = (row / WR) * HW + row % HW;
+    poff[i] = (int)(row * a.ldp * TP::EB) + piece * 16;
+    pk[i] = piece * TP::EPC;
+  }
+#pragma unroll
+  for (int i = 0; i < TQ::ITEMS; ++i) {
+    int row, piece;
+    TQ::item(i, tid, &row, &piece);
+    qoff[i] = (int)(row * a.ldq * TQ::EB) + piece * 16;
+    qk[i] = piece * TQ::EPC;
+  }
+  const unsigned lds0 = lds_addr(smem);
+
+  auto bases = [&](int t, const char** p0, const char** p1, const char** q, int* kk) {
+    const int seg = t >= a.ktiles ? 1 : 0;
+    const int k0 = (t - seg * a.ktiles) * TP::BKE;
+    const long long po = PT ? k0 * a.ldp + r0 : r0 * a.ldp + k0;
+    const long long qo = QT ? k0 * a.ldq + c0 : c0 * a.ldq + k0;
+    *p0 = static_cast<const char*>(a.P[GATED ? 0 : seg]) + po * TP::EB;
+    *p1 = GATED ? static_cast<const char*>(a.P[1]) + po * TP::EB : *p0;
+    *q = static_cast<const char*>(a.Q[seg | z]) + qo * TP::EB;
+    *kk = a.K - k0;  // k left in this segment
+  };
+
+  auto compute = [&](const char* buf) {
+    const char* pb = buf;
+    const char* qb = buf + TP::BYTES;
+#pragma unroll
+    for (int j2 = 0; j2 < 2; ++j2) {
+      typename TP::Frag p[NI];
+      typename TQ::Frag q[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) q[j] = TQ::frag(qb, wc * WC + j * 16, j2, lane);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) p[i] = TP::frag(pb, wr * WR + i * 16, j2, lane);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = multiply<E>(p[i], q[j], acc[i][j]);
+    }
+  };
+
+  if constexpr (DMA) {
+    auto issue = [&](int t, int b) {
+      const char *p0, *p1, *q;
+      int kk;
+      bases(t, &p0, &p1, &q, &kk);
+      const int kv = min(kk, TP::BKE);
+      // bytes from the base to the end of the last valid row's last piece (which a
+      // padded operand fills with zeros)
+      auto range = [&](bool tr_, long long rows, long long ld) {
+        const long long n = tr_ ? rows : kk, up = (n + TP::EPC - 1) / TP::EPC * TP::EPC;
+        return ((tr_ ? kv - 1 : min(rows, 256LL) - 1) * ld + up) * TP::EB;
+      };
+      const long long pr = range(PT, nr, a.ldp), qr = range(QT, nc, a.ldq);
+      const i32x4 rp0 = make_rsrc(p0, pr), rp1 = GATED ? make_rsrc(p1, pr) : rp0;
+      const i32x4 rq = make_rsrc(q, qr);
+      const unsigned lp = lds0 + b * STAGE + wave * 1024, lq = lp + TP::BYTES;
+      const bool tail = kk < TP::BKE;
+#pragma unroll
+      for (int i = 0; i < TP::ITEMS; ++i) {
+        const int off = !PT && tail && pk[i] >= kk ? kOob : poff[i];
+        const bool up = GATED && ((i * (NT / 8) + wave * 8) % WR) >= HW;
+        dma16(up ? rp1 : rp0, off, lp + i * NT * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < TQ::ITEMS; ++i) {
+        const int off = !QT && tail && qk[i] >= kk ? kOob : qoff[i];
+        dma16(rq, off, lq + i * NT * 16);
+      }
+    };
+    int b = 0;
+    if (t0 < t1) issue(t0, 0);
+    for (int t = t0; t < t1; ++t) {
+      if (t + 1 < t1) {
+        issue(t + 1, b ^ 1);
+        vm_wait<TP::ITEMS + TQ::ITEMS>();
+      } else {
+        vm_wait<0>();
+      }
+      barrier();
+      compute(smem + b * STAGE);
+      lds_wait();
+      barrier();
+      b ^= 1;
+    }
+  } else {
+    i32x4 pv[TP::ITEMS], qv[TQ::ITEMS];
+    auto fetch = [&](int t) {
+      const char *p0, *p1, *q;
+      int kk;
+      bases(t, &p0, &p1, &q, &kk);
+#pragma unroll
+      for (int i = 0; i < TP::ITEMS; ++i) {
+        int row, piece;
+        TP::item(i, tid, &row, &piece);
+        const char* base = p0;
+        if constexpr (GATED) {
+          if (row % WR >= HW) base = p1;
+          row = (row / WR) * HW + row % HW;
+        }
+        pv[i] = gather<E, PT>(reinterpret_cast<const E*>(base), a.ldp, row, piece, nr, kk);
+      }
+#pragma unroll
+      for (int i = 0; i < TQ::ITEMS; ++i) {
+        int row, piece;
+        TQ::item(i, tid, &row, &piece);
+        qv[i] = gather<E, QT>(reinterpret_cast<const E*>(q), a.ldq, row, piece, nc, kk);
+      }
+    };
+    auto put = [&](int b) {
+      char* d = smem + b * STAGE;
+#pragma unroll
+      for (int i = 0; i < TP::ITEMS; ++i) *reinterpret_cast<i32x4*>(d + (i * NT + tid) * 16) = pv[i];
+#pragma unroll
+      for (int i = 0; i < TQ::ITEMS; ++i)
+        *reinterpret_cast<i32x4*>(d + TP::BYTES + (i * NT + tid) * 16) = qv[i];
+    };
+    int b = 0;
+    if (t0 < t1) {
+      fetch(t0);
+      put(0);
+    }
+    for (int t = t0; t < t1; ++t) {
+      if (t + 1 < t1) fetch(t + 1);
+      lds_wait();
+      barrier();  // step t is staged; buffer b ^ 1 was last read before this
+      compute(smem + b * STAGE);
+      if (t + 1 < t1) put(b ^ 1);
+      b ^= 1;
+    }
+    lds_wait();
+    barrier();  // the epilogue reuses the buffers
+  }
+
+  // epilogue: each wave alone in its part of the LDS
+  float* ep = reinterpret_cast<float*>(smem + wave * EPW);
+  constexpr int RUN = GATED ? HW : WR;  // outputs per row and kind
+  constexpr int LPR = RUN / 8;          // lanes per row
+  constexpr int RPP = 64 / LPR;         // rows per pass
+  const int l = lane & 15, g = lane >> 4;
+  const int er = (lane % LPR) * 8, ec = lane / LPR;
+  const int r = r0 + wr * RUN + er;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      *reinterpret_cast<mfma_f32x4*>(ep + l * (WR + 4) + i * 16 + g * 4) = acc[i][j];
+    lds_wait();
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+    for (int p = 0; p < 16 / RPP; ++p) {
+      const int row = p * RPP + ec;
+      const long long c = c0 + wc * WC + j * 16 + row;
+      const float* s = ep + row * (WR + 4) + er;
+      if (r < a.R && c < a.C) {
+        float v[8], u[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = s[q];
+        if constexpr (GATED) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) u[q] = s[HW + q];
+        }
+        if (a.splits > 1) {
+          constexpr int KINDS = GATED ? 2 : 1;
+          float* d = a.planes + (((long long)split * a.nz + z) * KINDS * a.C + c) * a.plane_ld + r;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) d[q] = v[q];  // rows padded to 8 floats
+          if constexpr (GATED) {
+            d += (long long)a.C * a.plane_ld;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) d[q] = u[q];
+          }
+        } else if constexpr (GATED) {
+          finish_gated<E>(a.e, c, r, v, u);
+        } else {
+          finish_linear<E>(a.e, z, c, r, v);
+        }
+      }
+    }
+    lds_wait();
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+}  // namespace convfwd
