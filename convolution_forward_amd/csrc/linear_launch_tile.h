@@ -2,8 +2,8 @@
 // one source file per type.
 #pragma once
 
+#include "linear_pingpong.h"
 #include "linear_plan.h"
-#include "linear_tile.h"
 
 namespace convfwd {
 
@@ -17,10 +17,20 @@ static hipError_t launch_tile(ProductArgs a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename E, bool PT, bool QT, int BC, bool GATED>
+static hipError_t launch_pingpong(ProductArgs a, hipStream_t s) {
+  constexpr int BR = GATED ? 128 : 256;
+  a.ntr = (a.R + BR - 1) / BR;
+  a.ntc = (a.C + BC - 1) / BC;
+  const int grid = a.ntr * a.ntc * a.nz * a.splits;
+  hipLaunchKernelGGL((linear_pingpong_kernel<E, PT, QT, BC, GATED>), dim3(grid), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
 template <typename E, bool PT, bool QT>
 static hipError_t launch_layout(const ProductArgs& a, int tile, bool dma, hipStream_t s) {
   if constexpr (sizeof(E) == 2) {
-    if (tile == TILE_256 && dma) return launch_tile<E, PT, QT, 256, 256, 2, 4, true, false>(a, s);
+    if (tile == TILE_256 && dma) return launch_pingpong<E, PT, QT, 256, false>(a, s);
   }
   if (tile == TILE_64)
     return dma ? launch_tile<E, PT, QT, 64, 64, 2, 2, true, false>(a, s)
@@ -34,8 +44,7 @@ hipError_t launch_product(const ProductArgs& a, int tile, int layout, bool gated
                           hipStream_t s) {
   if (gated) {
     if constexpr (sizeof(E) == 2) {
-      if (tile == TILE_256 && dma)
-        return launch_tile<E, false, false, 256, 256, 2, 4, true, true>(a, s);
+      if (tile == TILE_256 && dma) return launch_pingpong<E, false, false, 256, true>(a, s);
     }
     if (tile == TILE_64)
       return dma ? launch_tile<E, false, false, 64, 64, 1, 4, true, true>(a, s)
