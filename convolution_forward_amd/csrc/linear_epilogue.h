@@ -53,9 +53,44 @@ __device__ __forceinline__ void store8(E* p, int nv, bool vec, const float (&v)[
   }
 }
 
-// GELU, erf form.
+// Phi(-|v|), the normal distribution function's tail, from erfc(x) = e^(-x^2) t P(t)
+// with t = 1 / (1 + 0.38 x), x = |v| / sqrt 2; P's coefficients are a fit of least
+// relative error (1.04e-6 for x in [0, 13], far into the tail), halved.  Together
+// with the hardware's exp2 and reciprocal within 3e-6 of the value, below a 16-bit
+// output's rounding; 14 operations for erff's 40 and more.
+__device__ __forceinline__ float normal_tail_fast(float v) {
+  const float a = fabsf(v), t = __builtin_amdgcn_rcpf(fmaf(0.26870058f, a, 1.0f));
+  float p = -0.0627085285f;
+  p = fmaf(p, t, 0.1680174795f);
+  p = fmaf(p, t, -0.03495600065f);
+  p = fmaf(p, t, 0.123917023f);
+  p = fmaf(p, t, 0.0902971255f);
+  p = fmaf(p, t, 0.1082887315f);
+  p = fmaf(p, t, 0.107143653f);
+  return p * t * __builtin_amdgcn_exp2f(-0.72134752f * a * a);
+}
+
+// GELU, erf form: v Phi(v).  The fast form's limits are inf and -0 at the infinities.
+template <bool FX>
 __device__ __forceinline__ float gelu_erf(float v) {
+  if constexpr (FX) {
+    const float w = fminf(fabsf(v), 1e4f) * normal_tail_fast(v);
+    return v < 0.0f ? -w : v - w;
+  }
   return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+}
+
+// tanh from the hardware's exp2 and reciprocal, by its series (to x^9) below 0.35
+// where 1 - e^-2x would cancel: within 4e-7 of the value.
+__device__ __forceinline__ float tanh_fast(float v) {
+  const float a = fabsf(v), q = v * v;
+  const float e = __builtin_amdgcn_exp2f(-2.885390082f * a);
+  const float big = copysignf((1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e), v);
+  float p = 0.0218694885f;
+  p = fmaf(p, q, -0.0539682540f);
+  p = fmaf(p, q, 0.1333333333f);
+  p = fmaf(p, q, -0.3333333333f);
+  return a < 0.35f ? fmaf(p * q, v, v) : big;
 }
 
 // GELU, tanh form: v/2 (1 + tanh u) = v / (1 + e^-2u), which keeps the relative
@@ -67,17 +102,30 @@ __device__ __forceinline__ float gelu_tanh(float v) {
   return v / (1.0f + expf(-u2));
 }
 
-// Every activation of include/linear.h over a batch, one uniform branch.
+// Every activation of include/linear.h over a batch: one uniform branch, then 8
+// values at a time (more of them side by side would cost registers).
 template <bool FX, int N>
 __device__ __forceinline__ void lin_act(float (&v)[N], int act, float alpha, float beta) {
-  if (act < 9) {
-    act_array<FX>(v, act, alpha, beta);
-  } else if (act == 9) {
+  auto each = [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = gelu_erf(v[i]);
-  } else {
+    for (int n = 0; n < N; n += 8) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = gelu_tanh<FX>(v[i]);
+      for (int i = n; i < n + 8; ++i) v[i] = f(v[i]);
+      if (N > 8) __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  switch (act) {
+    case 1: each([&](float q) { return act_t<1, FX>(q, alpha, beta); }); break;
+    case 2: each([&](float q) { return FX ? tanh_fast(q) : tanhf(q); }); break;
+    case 3: each([&](float q) { return act_t<3, FX>(q, alpha, beta); }); break;
+    case 4: each([&](float q) { return act_t<4, FX>(q, alpha, beta); }); break;
+    case 5: each([&](float q) { return act_t<5, FX>(q, alpha, beta); }); break;
+    case 6: each([&](float q) { return act_t<6, FX>(q, alpha, beta); }); break;
+    case 7: each([&](float q) { return act_t<7, FX>(q, alpha, beta); }); break;
+    case 8: each([&](float q) { return act_t<8, FX>(q, alpha, beta); }); break;
+    case 9: each([&](float q) { return gelu_erf<FX>(q); }); break;
+    case 10: each([&](float q) { return gelu_tanh<FX>(q); }); break;
+    default: break;
   }
 }
 
@@ -118,55 +166,116 @@ __device__ __forceinline__ void act_and_slope(float v, int act, float alpha, flo
   }
 }
 
-// Linear: v holds the sums of outputs (c, r .. r + nv - 1).
+// Two blocks of 16 r as the matrix cores leave them (lane (l, g): r = 4g .. 4g + 3 of
+// column l) into runs of 8 consecutive r: lane (l, g) gets block g & 1 from r =
+// 8 (g >> 1) on.  The odd quarter of the lanes of a changes places with the even
+// quarter of b: four swaps between registers in place of a trip through LDS.
+template <typename V>
+__device__ __forceinline__ void runs_of_8(const V& a, const V& b, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float ai = a[i], bi = b[i];
+    const auto s = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, ai),
+                                                    __builtin_bit_cast(unsigned, bi), false, false);
+    const unsigned lo = s[0], hi = s[1];
+    v[i] = __builtin_bit_cast(float, lo);
+    v[4 + i] = __builtin_bit_cast(float, hi);
+  }
+}
+// The offset of a lane's run from the first block's first row.
+__device__ __forceinline__ int run_offset(int lane) {
+  return ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+}
+
+// Linear: v holds the sums of one row c, NR runs of 8 outputs at r + off(n).  whole
+// (uniform): every run is inside and every operand vectorised; in: c is a row.  The
+// runs' loads are in flight together and one branch picks the activation for all.
+template <typename E, int NR, typename Off>
+__device__ __forceinline__ void finish_linear_runs(const LinEpilogue& e, int z, long long c,
+                                                   bool in, int r, Off off, bool whole,
+                                                   float (&v)[NR * 8]) {
+  auto add = [&](const void* from, long long at) {
+    const E* p = static_cast<const E*>(from) + at + r;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      float t[8];
+      if (whole) load8(p + off(n), 8, true, t);
+      else load8(p + off(n), min(8, e.R - r - off(n)), e.vec, t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[n * 8 + i] += t[i];
+    }
+  };
+  auto store = [&](void* to, long long at) {
+    E* p = static_cast<E*>(to) + at + r;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      float t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = v[n * 8 + i];
+      if (whole) store8(p + off(n), 8, true, t);
+      else store8(p + off(n), min(8, e.R - r - off(n)), e.vec, t);
+    }
+  };
+  if (e.bias[0]) add(e.bias[0], 0);
+  if (e.res_mode == 1 && in) add(e.res, c * e.ldres);
+  if (e.save[0] && in) store(e.save[0], c * e.ldsave);
+  lin_act<sizeof(E) == 2>(v, e.act, e.alpha, e.beta);
+  if (in) {
+    if (e.res_mode == 2) add(e.res, c * e.ldres);
+    store(e.out[z], c * e.ldo);
+  }
+}
+
 template <typename E>
 __device__ __forceinline__ void finish_linear(const LinEpilogue& e, int z, long long c, int r,
                                               float (&v)[8]) {
-  const int nv = min(8, e.R - r);
-  const bool vec = e.vec;
-  float t[8];
-  if (e.bias[0]) {
-    load8(static_cast<const E*>(e.bias[0]) + r, nv, vec, t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += t[i];
-  }
-  if (e.res_mode != 0) load8(static_cast<const E*>(e.res) + c * e.ldres + r, nv, vec, t);
-  if (e.res_mode == 1) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += t[i];
-  }
-  if (e.save[0]) store8(static_cast<E*>(e.save[0]) + c * e.ldsave + r, nv, vec, v);
-  lin_act<sizeof(E) == 2>(v, e.act, e.alpha, e.beta);
-  if (e.res_mode == 2) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += t[i];
-  }
-  store8(static_cast<E*>(e.out[z]) + c * e.ldo + r, nv, vec, v);
+  finish_linear_runs<E, 1>(e, z, c, true, r, [](int) { return 0; }, false, v);
 }
 
 // Gated: g and u hold both projections' sums.
-template <typename E>
-__device__ __forceinline__ void finish_gated(const LinEpilogue& e, long long c, int r,
-                                             float (&g)[8], float (&u)[8]) {
-  const int nv = min(8, e.R - r);
-  const bool vec = e.vec;
+template <typename E, int NR, typename Off>
+__device__ __forceinline__ void finish_gated_runs(const LinEpilogue& e, long long c, bool in, int r,
+                                                  Off off, bool whole, float (&g)[NR * 8],
+                                                  float (&u)[NR * 8]) {
+  auto add = [&](const E* p, float (&v)[NR * 8]) {
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      float t[8];
+      if (whole) load8(p + r + off(n), 8, true, t);
+      else load8(p + r + off(n), min(8, e.R - r - off(n)), e.vec, t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[n * 8 + i] += t[i];
+    }
+  };
+  auto store = [&](void* out, long long ld, const float (&v)[NR * 8]) {
+    E* p = static_cast<E*>(out) + c * ld;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      float t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = v[n * 8 + i];
+      if (whole) store8(p + r + off(n), 8, true, t);
+      else store8(p + r + off(n), min(8, e.R - r - off(n)), e.vec, t);
+    }
+  };
   if (e.bias[0]) {
-    float t[8];
-    load8(static_cast<const E*>(e.bias[0]) + r, nv, vec, t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] += t[i];
-    load8(static_cast<const E*>(e.bias[1]) + r, nv, vec, t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] += t[i];
+    add(static_cast<const E*>(e.bias[0]), g);
+    add(static_cast<const E*>(e.bias[1]), u);
   }
-  if (e.save[0]) {
-    store8(static_cast<E*>(e.save[0]) + c * e.ldsave + r, nv, vec, g);
-    store8(static_cast<E*>(e.save[1]) + c * e.ldsave + r, nv, vec, u);
+  if (e.save[0] && in) {
+    store(e.save[0], e.ldsave, g);
+    store(e.save[1], e.ldsave, u);
   }
   lin_act<sizeof(E) == 2>(g, e.act, e.alpha, e.beta);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) g[i] *= u[i];
-  store8(static_cast<E*>(e.out[0]) + c * e.ldo + r, nv, vec, g);
+  for (int i = 0; i < NR * 8; ++i) g[i] *= u[i];
+  if (in) store(e.out[0], e.ldo, g);
+}
+
+template <typename E>
+__device__ __forceinline__ void finish_gated(const LinEpilogue& e, long long c, int r,
+                                             float (&g)[8], float (&u)[8]) {
+  finish_gated_runs<E, 1>(e, c, true, r, [](int) { return 0; }, false, g, u);
 }
 
 }  // namespace convfwd

@@ -31,6 +31,7 @@ template <typename E, bool PT, bool QT>
 static hipError_t launch_layout(const ProductArgs& a, int tile, bool dma, hipStream_t s) {
   if constexpr (sizeof(E) == 2) {
     if (tile == TILE_256 && dma) return launch_pingpong<E, PT, QT, 256, false>(a, s);
+    if (tile == TILE_256X128 && dma) return launch_pingpong<E, PT, QT, 128, false>(a, s);
   }
   if (tile == TILE_64)
     return dma ? launch_tile<E, PT, QT, 64, 64, 2, 2, true, false>(a, s)
@@ -45,6 +46,7 @@ hipError_t launch_product(const ProductArgs& a, int tile, int layout, bool gated
   if (gated) {
     if constexpr (sizeof(E) == 2) {
       if (tile == TILE_256 && dma) return launch_pingpong<E, false, false, 256, true>(a, s);
+      if (tile == TILE_256X128 && dma) return launch_pingpong<E, false, false, 128, true>(a, s);
     }
     if (tile == TILE_64)
       return dma ? launch_tile<E, false, false, 64, 64, 1, 4, true, true>(a, s)

@@ -2,9 +2,10 @@
 // linear_tile.h for operands, layouts in LDS and the epilogue's idea): 256 outputs
 // r by BC = 256 or 128 outputs c for 8 waves, two waves on each SIMD.
 //
-//  * Both operands are cut into halves (128 rows of P, BC / 2 of Q).  A wave owns
-//    64 rows of each half of P and BC / 8 of each half of Q: four quadrants of the
-//    accumulators, one for each pair of halves, taken one a phase.
+//  * Both operands are cut into halves (128 rows of P, BC / 2 of Q).  A wave owns a
+//    part of each half (2 x 4 waves share 256 x 256, 4 x 2 share 256 x 128, so that
+//    parts stay near square): four quadrants of the accumulators, one for each pair
+//    of halves, taken one a phase.
 //  * The waves form two groups of four, one wave of each on every SIMD, half a
 //    phase apart: while one group multiplies a quadrant, the other reads its next
 //    fragments from LDS and issues global loads, and the SIMD's matrix core is fed
@@ -14,9 +15,11 @@
 //  * Half tiles live in two LDS buffers.  The half that a phase has read for the
 //    last time is overwritten from the next phase on by the half of two steps
 //    later; seven phases pass between a half's load and its use, so six halves (96
-//    KB) are in flight at any time and no phase waits for memory in steady state.
+//    or 72 KB) are in flight and no phase waits for memory in steady state.
 //  * Gated products: half 0 of P is gate rows, half 1 the same rows of up, and a
 //    wave holds both sums of its outputs.
+//  * The epilogue takes the sums from registers (runs_of_8): a trip through LDS,
+//    16 rows at a time, took 21000 cycles a tile, as much as 9 steps.
 #pragma once
 
 #include "linear_tile.h"
@@ -31,20 +34,23 @@ template <typename E, bool PT, bool QT, int BC, bool GATED>
 struct PingPong {
   static_assert(sizeof(E) == 2 && (BC == 256 || BC == 128), "16-bit operands");
   static constexpr int NT = 512, HR = 128, HC = BC / 2;
-  static constexpr int NI = 4, NJ = BC / 128;  // 16-row blocks of a quadrant
+  static constexpr int WVR = BC == 256 ? 2 : 4, WVC = 8 / WVR;  // waves along r and c
+  static constexpr int WR = HR / WVR, WC = HC / WVC;  // a wave's part of a half
+  static constexpr int NI = WR / 16, NJ = WC / 16;
   using TP = Tile<E, HR, PT, NT>;
   using TQ = Tile<E, HC, QT, NT>;
-  static constexpr int BUF = 2 * (TP::BYTES + TQ::BYTES);
-  static constexpr int EPLD = 64 + 4;
-  static constexpr int EPW = 16 * EPLD * 4 * (GATED ? 2 : 1);
-  static constexpr int SMEM = 2 * BUF > 8 * EPW ? 2 * BUF : 8 * EPW;
+  static constexpr int SMEM = 4 * (TP::BYTES + TQ::BYTES);
+  // an operand's four half tiles lie side by side, within an LDS instruction's
+  // 64 KB offset of one address
+  static constexpr int p_at(int half, int buf) { return (2 * buf + half) * TP::BYTES; }
+  static constexpr int q_at(int half, int buf) { return 4 * TP::BYTES + (2 * buf + half) * TQ::BYTES; }
   static constexpr int FLIGHT = 3 * (TP::ITEMS + TQ::ITEMS);  // six halves
 
   // id: index of this workgroup among the product's own, after xcd_logical
   static __device__ __forceinline__ void run(const ProductArgs& a, int id, char* smem) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wr = wave & 1, wc = wave >> 1;
+    const int wr = wave % WVR, wc = wave / WVR;
 
     const int per = a.ntr * a.ntc;
     const int batch = id / per;  // split * nz + z
@@ -113,28 +119,28 @@ struct PingPong {
       const char* m = GATED && half ? P1 : P0;
       const int h = GATED ? 0 : half * HR;
       issue(std::integral_constant<bool, PT>(), m, GATED ? m : P1, a.ldp, r0 + h, nr - h, HR, poff,
-            TP::ITEMS, pk, t, lds0 + buf * BUF + half * TP::BYTES);
+            TP::ITEMS, pk, t, lds0 + p_at(half, buf));
     };
     auto issue_q = [&](int t, int half, int buf) {
       issue(std::integral_constant<bool, QT>(), Q0, Q1, a.ldq, c0 + half * HC, nc - half * HC, HC,
-            qoff, TQ::ITEMS, qk, t, lds0 + buf * BUF + 2 * TP::BYTES + half * TQ::BYTES);
+            qoff, TQ::ITEMS, qk, t, lds0 + q_at(half, buf));
     };
 
     typename TP::Frag p[NI][2];
     typename TQ::Frag q[2][NJ][2];
     auto read_p = [&](int half, int buf) {
-      const char* b = smem + buf * BUF + half * TP::BYTES;
+      const char* b = smem + p_at(half, buf);
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int j2 = 0; j2 < 2; ++j2) p[i][j2] = TP::frag(b, wr * 64 + i * 16, j2, lane);
+        for (int j2 = 0; j2 < 2; ++j2) p[i][j2] = TP::frag(b, wr * WR + i * 16, j2, lane);
     };
     auto read_q = [&](int half, int buf) {
-      const char* b = smem + buf * BUF + 2 * TP::BYTES + half * TQ::BYTES;
+      const char* b = smem + q_at(half, buf);
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int j2 = 0; j2 < 2; ++j2) q[half][j][j2] = TQ::frag(b, wc * (HC / 4) + j * 16, j2, lane);
+        for (int j2 = 0; j2 < 2; ++j2) q[half][j][j2] = TQ::frag(b, wc * WC + j * 16, j2, lane);
     };
     // end of a phase's reads: they are in registers, and the half that the next
     // phase reads has arrived for every wave behind the barrier
@@ -202,62 +208,47 @@ struct PingPong {
       step(t + 1, std::integral_constant<int, 1>());
     }
     if (!late) barrier();
-    vm_wait<0>();  // loads past the end (zeros) land before the LDS is reused
-    fence();
-    barrier();
+    vm_wait<0>();  // loads past the end (zeros) land before the workgroup's LDS is given up
 
-    // epilogue: each wave alone in its part of the LDS, 16 rows c at a time
-    float* ep = reinterpret_cast<float*>(smem + wave * EPW);
-    const int l = lane & 15, g = lane >> 4;
-    const int er = (lane & 7) * 8, ec = lane >> 3;
-#pragma unroll
-    for (int hq = 0; hq < 2; ++hq)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int hp = 0; hp < (GATED ? 1 : 2); ++hp) {
-#pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            float* d = ep + l * EPLD + i * 16 + g * 4;
-            *reinterpret_cast<mfma_f32x4*>(d) = acc[hp][hq][i][j];
-            if constexpr (GATED) *reinterpret_cast<mfma_f32x4*>(d + 16 * EPLD) = acc[1][hq][i][j];
-          }
-          lds_wait();
-          __builtin_amdgcn_wave_barrier();
-          const int r = r0 + hp * HR + wr * 64 + er;
+    // epilogue: 16 rows c at a time, one a lane, its outputs in runs of 8
+    constexpr int NR = GATED ? NI / 2 : NI;
+    auto off = [](int n) { return n % (NI / 2) * 32 + n / (NI / 2) * HR; };
+    const int rl = r0 + wr * WR + run_offset(lane);
+    const bool whole = a.e.vec && nr >= (GATED ? HR : 2 * HR);
 #pragma unroll 1
-          for (int pass = 0; pass < 2; ++pass) {
-            const int row = pass * 8 + ec;
-            const long long c = c0 + hq * HC + wc * (HC / 4) + j * 16 + row;
-            const float* s = ep + row * EPLD + er;
-            if (r < a.R && c < a.C) {
-              float v[8], u[8];
+    for (int round = 0; round < 2 * NJ; ++round) {
+      float v[NR * 8], u[GATED ? NR * 8 : 1];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = s[e];
-              if constexpr (GATED) {
+      for (int n = 0; n < 2 * NJ; ++n)
+        if (n == round) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = s[16 * EPLD + e];
-              }
-              if (a.splits > 1) {
-                constexpr int KINDS = GATED ? 2 : 1;
-                float* d = a.planes + (((long long)split * a.nz + z) * KINDS * a.C + c) * a.plane_ld + r;
+          for (int i = 0; i < NR; ++i) {
+            const int h = GATED ? 0 : i / (NI / 2), b = i % (NI / 2) * 2;
+            runs_of_8(acc[h][n / NJ][b][n % NJ], acc[h][n / NJ][b + 1][n % NJ], v + i * 8);
+            if constexpr (GATED)
+              runs_of_8(acc[1][n / NJ][b][n % NJ], acc[1][n / NJ][b + 1][n % NJ], u + i * 8);
+          }
+        }
+      const long long c = c0 + round / NJ * HC + wc * WC + round % NJ * 16 + (lane & 15);
+      const bool in = c < a.C;
+      if (a.splits > 1) {
+        constexpr int KINDS = GATED ? 2 : 1;
+        float* d = a.planes + (((long long)split * a.nz + z) * KINDS * a.C + c) * a.plane_ld + rl;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] = v[e];  // rows padded to 8 floats
-                if constexpr (GATED) {
-                  d += (long long)a.C * a.plane_ld;
+        for (int n = 0; n < NR; ++n)
+          if (in && rl + off(n) < a.R) {  // rows padded to 8 floats
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) d[e] = u[e];
-                }
-              } else if constexpr (GATED) {
-                finish_gated<E>(a.e, c, r, v, u);
-              } else {
-                finish_linear<E>(a.e, z, c, r, v);
-              }
+            for (int e = 0; e < 8; ++e) {
+              d[off(n) + e] = v[n * 8 + e];
+              if constexpr (GATED) d[(long long)a.C * a.plane_ld + off(n) + e] = u[n * 8 + e];
             }
           }
-          lds_wait();
-          __builtin_amdgcn_wave_barrier();
-        }
+      } else if constexpr (GATED) {
+        finish_gated_runs<E, NR>(a.e, c, in, rl, off, whole, v, u);
+      } else {
+        finish_linear_runs<E, NR>(a.e, z, c, in, rl, off, whole, v);
+      }
+    }
   }
 };
 

@@ -21,7 +21,7 @@ struct ProductShape {
   bool aligned;     // rows of whole 16-byte vectors (strides, extents, offsets)
 };
 
-enum ProductTile { TILE_256 = 0, TILE_128 = 1, TILE_64 = 2, TILE_STREAM = 3 };
+enum ProductTile { TILE_256 = 0, TILE_128 = 1, TILE_64 = 2, TILE_STREAM = 3, TILE_256X128 = 4 };
 
 struct ProductPlan {
   int tile;

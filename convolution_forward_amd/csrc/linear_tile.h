@@ -17,8 +17,9 @@
 //    image: one row per k, kept as it lies, in 32-byte units (16 halves) moved to
 //    unit u ^ h(k); fragments come out transposed by the LDS transpose read
 //    (16-bit), or are read element by element (float32, 64-byte units).
-//  * Epilogue through LDS, wave by wave: 16 rows c of WR sums, read back as runs
-//    of 8 consecutive r, so that loads and stores are 16-byte pieces of rows.
+//  * Epilogue from registers: 16 rows c at a time, one a lane, each lane's sums
+//    exchanged into runs of 8 consecutive r (runs_of_8), so that loads and stores
+//    are 16-byte pieces of rows.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -178,10 +179,8 @@ __global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const Produ
   using TP = Tile<E, BR, PT, NT>;
   using TQ = Tile<E, BC, QT, NT>;
   constexpr int STAGE = TP::BYTES + TQ::BYTES;
-  constexpr int EPW = 16 * (WR + 4) * 4;  // epilogue bytes per wave
-  constexpr int SMEM = 2 * STAGE > NT / 64 * EPW ? 2 * STAGE : NT / 64 * EPW;
   static_assert(!GATED || (!PT && !QT), "gated weights are k-major");
-  __shared__ __attribute__((aligned(1024))) char smem[SMEM];
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -347,57 +346,41 @@ __global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const Produ
       if (t + 1 < t1) put(b ^ 1);
       b ^= 1;
     }
-    lds_wait();
-    barrier();  // the epilogue reuses the buffers
   }
 
-  // epilogue: each wave alone in its part of the LDS
-  float* ep = reinterpret_cast<float*>(smem + wave * EPW);
-  constexpr int RUN = GATED ? HW : WR;  // outputs per row and kind
-  constexpr int LPR = RUN / 8;          // lanes per row
-  constexpr int RPP = 64 / LPR;         // rows per pass
-  const int l = lane & 15, g = lane >> 4;
-  const int er = (lane % LPR) * 8, ec = lane / LPR;
-  const int r = r0 + wr * RUN + er;
+  // epilogue: 16 rows c at a time, one a lane, its outputs in runs of 8
+  constexpr int RUN = GATED ? HW : WR;  // outputs of a wave's row and kind
+  constexpr int NR = RUN / 32;
+  auto off = [](int n) { return n * 32; };
+  const int rl = r0 + wr * RUN + run_offset(lane);
+  const bool whole = a.e.vec && nr >= WVR * RUN;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
+    float v[NR * 8], u[GATED ? NR * 8 : 1];
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-      *reinterpret_cast<mfma_f32x4*>(ep + l * (WR + 4) + i * 16 + g * 4) = acc[i][j];
-    lds_wait();
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-    for (int p = 0; p < 16 / RPP; ++p) {
-      const int row = p * RPP + ec;
-      const long long c = c0 + wc * WC + j * 16 + row;
-      const float* s = ep + row * (WR + 4) + er;
-      if (r < a.R && c < a.C) {
-        float v[8], u[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = s[q];
-        if constexpr (GATED) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) u[q] = s[HW + q];
-        }
-        if (a.splits > 1) {
-          constexpr int KINDS = GATED ? 2 : 1;
-          float* d = a.planes + (((long long)split * a.nz + z) * KINDS * a.C + c) * a.plane_ld + r;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) d[q] = v[q];  // rows padded to 8 floats
-          if constexpr (GATED) {
-            d += (long long)a.C * a.plane_ld;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) d[q] = u[q];
-          }
-        } else if constexpr (GATED) {
-          finish_gated<E>(a.e, c, r, v, u);
-        } else {
-          finish_linear<E>(a.e, z, c, r, v);
-        }
-      }
+    for (int i = 0; i < NR; ++i) {
+      runs_of_8(acc[2 * i][j], acc[2 * i + 1][j], v + i * 8);
+      if constexpr (GATED) runs_of_8(acc[NI / 2 + 2 * i][j], acc[NI / 2 + 2 * i + 1][j], u + i * 8);
     }
-    lds_wait();
-    __builtin_amdgcn_wave_barrier();
+    const long long c = c0 + wc * WC + j * 16 + (lane & 15);
+    const bool in = c < a.C;
+    if (a.splits > 1) {
+      constexpr int KINDS = GATED ? 2 : 1;
+      float* d = a.planes + (((long long)split * a.nz + z) * KINDS * a.C + c) * a.plane_ld + rl;
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+        if (in && rl + off(n) < a.R) {  // rows padded to 8 floats
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            d[off(n) + e] = v[n * 8 + e];
+            if constexpr (GATED) d[(long long)a.C * a.plane_ld + off(n) + e] = u[n * 8 + e];
+          }
+        }
+    } else if constexpr (GATED) {
+      finish_gated_runs<E, NR>(a.e, c, in, rl, off, whole, v, u);
+    } else {
+      finish_linear_runs<E, NR>(a.e, z, c, in, rl, off, whole, v);
+    }
   }
 }
 
