@@ -94,6 +94,39 @@ hipError_t run_product(const ProductShape& s, int dtype, ProductArgs& a, bool p_
   return join(dtype, j, s.gated, st);
 }
 
+hipError_t pair(int dtype, const PairArgs& a, int tile, bool dx_transposed, hipStream_t s) {
+  if (dtype == CONV_F16) return launch_pair<_Float16>(a, tile, dx_transposed, s);
+  return launch_pair<__bf16>(a, tile, dx_transposed, s);
+}
+
+// Both products of a backward pass: in one launch where the plan pairs them and the
+// operands allow it, one after the other otherwise.
+hipError_t run_both(const ProductShape& sx, const ProductShape& sw, int dtype, ProductArgs& dx,
+                    ProductArgs& dw, bool dx_p_padded, bool dx_q_padded, bool dw_p_padded,
+                    bool dw_q_padded, void* planes, hipStream_t st) {
+  const int es = (int)dtype_size(dtype);
+  const int tile = plan_pair(sx, sw, es);
+  if (tile >= 0 && direct(sx, dx, es, dx_p_padded, dx_q_padded) &&
+      direct(sw, dw, es, dw_p_padded, dw_q_padded)) {
+    PairArgs a{};
+    const ProductShape* shapes[2] = {&sx, &sw};
+    ProductArgs* args[2] = {&dx, &dw};
+    for (int i = 0; i < 2; ++i) {
+      ProductArgs& q = *args[i];
+      q.R = (int)shapes[i]->R; q.C = (int)shapes[i]->C; q.K = (int)shapes[i]->K;
+      q.nseg = shapes[i]->nseg; q.nz = shapes[i]->nz;
+      q.ktiles = (int)ceil_div(shapes[i]->K, 64);
+      q.splits = 1; q.per_split = q.ktiles * q.nseg;
+      q.e.R = q.R;
+    }
+    a.dx = dx;
+    a.dw = dw;
+    return pair(dtype, a, tile, sx.pt, st);
+  }
+  const hipError_t e = run_product(sx, dtype, dx, dx_p_padded, dx_q_padded, planes, st);
+  return e != hipSuccess ? e : run_product(sw, dtype, dw, dw_p_padded, dw_q_padded, planes, st);
+}
+
 int status(hipError_t e) { return e == hipSuccess ? CONV_OK : CONV_ERR_DEVICE; }
 
 }  // namespace
@@ -202,28 +235,33 @@ int linear_backward(const linear_problem* p, int dtype, const void* x, const voi
   }
   const void* d = act ? static_cast<const void*>(sb + sc.dz) : dy;
   const int64_t ldd = act ? sc.dz_ld : g.ldy;
-  if (e == hipSuccess && dx && g.m > 0) {
-    ProductArgs a{};
-    a.P[0] = at(w, p->w_off, g.es);
-    a.Q[0] = d;
-    a.ldp = g.ldw; a.ldq = ldd;
-    a.e.out[0] = at(dx, p->dx_off, g.es);
-    a.e.ldo = g.lddx;
-    a.e.vec = rows16(a.e.out[0], g.lddx, g.es);
-    e = run_product(linear_dx_product(p, g), dtype, a, false, act, sb + sc.planes, s);
+  const bool want_dx = dx && g.m > 0;
+  ProductArgs ax{}, aw{};
+  if (want_dx) {
+    ax.P[0] = at(w, p->w_off, g.es);
+    ax.Q[0] = d;
+    ax.ldp = g.ldw; ax.ldq = ldd;
+    ax.e.out[0] = at(dx, p->dx_off, g.es);
+    ax.e.ldo = g.lddx;
+    ax.e.vec = rows16(ax.e.out[0], g.lddx, g.es);
   }
-  if (e == hipSuccess && dw) {
-    ProductArgs a{};
+  if (dw) {
     const void* xb = at(x, p->x_off, g.es);
-    a.P[0] = g.kn ? d : xb;
-    a.Q[0] = g.kn ? xb : d;
-    a.ldp = g.kn ? ldd : g.ldx;
-    a.ldq = g.kn ? g.ldx : ldd;
-    a.e.out[0] = at(dw, p->dw_off, g.es);
-    a.e.ldo = g.lddw;
-    a.e.vec = rows16(a.e.out[0], g.lddw, g.es);
-    e = run_product(linear_dw_product(p, g), dtype, a, act && g.kn, act && !g.kn, sb + sc.planes, s);
+    aw.P[0] = g.kn ? d : xb;
+    aw.Q[0] = g.kn ? xb : d;
+    aw.ldp = g.kn ? ldd : g.ldx;
+    aw.ldq = g.kn ? g.ldx : ldd;
+    aw.e.out[0] = at(dw, p->dw_off, g.es);
+    aw.e.ldo = g.lddw;
+    aw.e.vec = rows16(aw.e.out[0], g.lddw, g.es);
   }
+  const ProductShape sx = linear_dx_product(p, g), sw = linear_dw_product(p, g);
+  if (e == hipSuccess && want_dx && dw)
+    e = run_both(sx, sw, dtype, ax, aw, false, act, act && g.kn, act && !g.kn, sb + sc.planes, s);
+  else if (e == hipSuccess && want_dx)
+    e = run_product(sx, dtype, ax, false, act, sb + sc.planes, s);
+  else if (e == hipSuccess && dw)
+    e = run_product(sw, dtype, aw, act && g.kn, act && !g.kn, sb + sc.planes, s);
   return status(e);
 }
 
@@ -261,30 +299,35 @@ int gated_backward(const gated_problem* p, int dtype, const void* x, const void*
   }
   const char* dg = sb + sc.dz;
   const char* du = dg + (int64_t)a.np * g.es;
-  if (e == hipSuccess && dx && g.m > 0) {
-    ProductArgs q{};
-    q.P[0] = at(wg, p->wg_off, g.es);
-    q.P[1] = at(wu, p->wu_off, g.es);
-    q.Q[0] = dg;
-    q.Q[1] = du;
-    q.ldp = g.ldw; q.ldq = sc.dz_ld;
-    q.e.out[0] = at(dx, p->dx_off, g.es);
-    q.e.ldo = g.lddx;
-    q.e.vec = rows16(q.e.out[0], g.lddx, g.es);
-    e = run_product(gated_dx_product(p, g), dtype, q, false, true, sb + sc.planes, s);
+  const bool want_dx = dx && g.m > 0;
+  ProductArgs ax{}, aw{};
+  if (want_dx) {
+    ax.P[0] = at(wg, p->wg_off, g.es);
+    ax.P[1] = at(wu, p->wu_off, g.es);
+    ax.Q[0] = dg;
+    ax.Q[1] = du;
+    ax.ldp = g.ldw; ax.ldq = sc.dz_ld;
+    ax.e.out[0] = at(dx, p->dx_off, g.es);
+    ax.e.ldo = g.lddx;
+    ax.e.vec = rows16(ax.e.out[0], g.lddx, g.es);
   }
-  if (e == hipSuccess && dwg) {
-    ProductArgs q{};
-    q.P[0] = at(x, p->x_off, g.es);
-    q.Q[0] = dg;
-    q.Q[1] = du;
-    q.ldp = g.ldx; q.ldq = sc.dz_ld;
-    q.e.out[0] = at(dwg, p->dwg_off, g.es);
-    q.e.out[1] = at(dwu, p->dwu_off, g.es);
-    q.e.ldo = g.lddw;
-    q.e.vec = rows16(q.e.out[0], g.lddw, g.es) && al16(q.e.out[1]);
-    e = run_product(gated_dw_product(p, g), dtype, q, false, true, sb + sc.planes, s);
+  if (dwg) {
+    aw.P[0] = at(x, p->x_off, g.es);
+    aw.Q[0] = dg;
+    aw.Q[1] = du;
+    aw.ldp = g.ldx; aw.ldq = sc.dz_ld;
+    aw.e.out[0] = at(dwg, p->dwg_off, g.es);
+    aw.e.out[1] = at(dwu, p->dwu_off, g.es);
+    aw.e.ldo = g.lddw;
+    aw.e.vec = rows16(aw.e.out[0], g.lddw, g.es) && al16(aw.e.out[1]);
   }
+  const ProductShape sx = gated_dx_product(p, g), sw = gated_dw_product(p, g);
+  if (e == hipSuccess && want_dx && dwg)
+    e = run_both(sx, sw, dtype, ax, aw, false, true, false, true, sb + sc.planes, s);
+  else if (e == hipSuccess && want_dx)
+    e = run_product(sx, dtype, ax, false, true, sb + sc.planes, s);
+  else if (e == hipSuccess && dwg)
+    e = run_product(sw, dtype, aw, false, true, sb + sc.planes, s);
   return status(e);
 }
 

@@ -28,43 +28,54 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const DzArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[d][i] = 0.0f;
   if (nv > 0) {
-    for (long long m = m0 + rg; m < m1; m += 8) {
-      float dy[8], z[8], t[8];
-      load8(static_cast<const E*>(a.dy) + m * a.ldy + col, nv, a.vec, dy);
-      if constexpr (GATED) {
-        float pu[8];
-        load8(static_cast<const E*>(a.z[0]) + m * a.ldz + col, nv, a.vec, z);
-        load8(static_cast<const E*>(a.z[1]) + m * a.ldz + col, nv, a.vec, pu);
+    constexpr bool FX = sizeof(E) == 2;
+    const E* gy = static_cast<const E*>(a.dy) + col;
+    const E* gz = static_cast<const E*>(a.z[0]) + col;
+    const E* gu = GATED ? static_cast<const E*>(a.z[1]) + col : nullptr;
+    // two rows at a time: their loads are in flight together
+    for (long long m = m0 + rg; m < m1; m += 16) {
+      const bool two = m + 8 < m1;
+      float dy[2][8], z[2][8], t[2][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float f, d;
-          act_and_slope(z[i], a.act, a.alpha, a.beta, &f, &d);
-          t[i] = i < nv ? dy[i] * f : 0.0f;           // du
-          z[i] = i < nv ? dy[i] * pu[i] * d : 0.0f;   // dg
-          sum[0][i] += z[i];
-          sum[KINDS - 1][i] += t[i];
-        }
-        E* o = static_cast<E*>(a.dz) + m * a.lddz + col;
-        store8(o, 8, true, z);
-        store8(o + a.np, 8, true, t);
-      } else {
-        if (a.act != 0) {
-          load8(static_cast<const E*>(a.z[0]) + m * a.ldz + col, nv, a.vec, z);
+      for (int k = 0; k < 2; ++k) {
+        if (k == 1 && !two) break;
+        const long long row = m + 8 * k;
+        load8(gy + row * a.ldy, nv, a.vec, dy[k]);
+        if (GATED || a.act != 0) load8(gz + row * a.ldz, nv, a.vec, z[k]);
+        if constexpr (GATED) load8(gu + row * a.ldz, nv, a.vec, t[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (k == 1 && !two) break;
+        const long long row = m + 8 * k;
+        float f[8];
+        if constexpr (GATED) {
+          acts_and_slopes<FX>(z[k], f, a.act, a.alpha, a.beta);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            float f, d;
-            act_and_slope(z[i], a.act, a.alpha, a.beta, &f, &d);
-            t[i] = i < nv ? dy[i] * d : 0.0f;
+            z[k][i] = i < nv ? dy[k][i] * t[k][i] * z[k][i] : 0.0f;  // dg
+            t[k][i] = i < nv ? dy[k][i] * f[i] : 0.0f;               // du
+            sum[0][i] += z[k][i];
+            sum[KINDS - 1][i] += t[k][i];
           }
+          E* o = static_cast<E*>(a.dz) + row * a.lddz + col;
+          store8(o, 8, true, z[k]);
+          store8(o + a.np, 8, true, t[k]);
         } else {
+          if (a.act != 0) {
+            acts_and_slopes<FX>(z[k], f, a.act, a.alpha, a.beta);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) t[i] = dy[i];
+            for (int i = 0; i < 8; ++i) t[k][i] = i < nv ? dy[k][i] * z[k][i] : 0.0f;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[k][i] = dy[k][i];
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[0][i] += t[k][i];
+          if (a.dz) store8(static_cast<E*>(a.dz) + row * a.lddz + col, 8, true, t[k]);
+          if (a.dr)
+            store8(static_cast<E*>(a.dr) + row * a.lddr + col, nv, a.vec, a.dr_is_dy ? dy[k] : t[k]);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[0][i] += t[i];
-        if (a.dz) store8(static_cast<E*>(a.dz) + m * a.lddz + col, 8, true, t);
-        if (a.dr)
-          store8(static_cast<E*>(a.dr) + m * a.lddr + col, nv, a.vec, a.dr_is_dy ? dy : t);
       }
     }
   }
@@ -86,15 +97,28 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const DzArgs a) {
   }
 }
 
+// 32 columns a workgroup; each of 8 groups of lanes adds an eighth of the chunks in
+// order, then the groups in order.
 template <typename E>
-__global__ __launch_bounds__(64) void linear_sums_kernel(const SumsArgs a) {
-  const int c = blockIdx.x * 64 + threadIdx.x, d = blockIdx.y;
-  if (c >= a.n) return;
-  const float* p = a.sums + (long long)d * a.np + c;
-  const long long step = (long long)a.parts * a.np;
+__global__ __launch_bounds__(256) void linear_sums_kernel(const SumsArgs a) {
+  __shared__ float red[8][32];
+  const int cl = threadIdx.x & 31, g = threadIdx.x >> 5, d = blockIdx.y;
+  const int c = blockIdx.x * 32 + cl;
+  const int per = (a.chunks + 7) / 8, i1 = min(a.chunks, (g + 1) * per);
   float s = 0.0f;
-  for (int i = 0; i < a.chunks; ++i) s += p[i * step];
-  static_cast<E*>(a.db[d])[c] = (E)s;
+  if (c < a.n) {
+    const float* p = a.sums + (long long)d * a.np + c;
+    const long long step = (long long)a.parts * a.np;
+#pragma unroll 8
+    for (int i = g * per; i < i1; ++i) s += p[i * step];
+  }
+  red[g][cl] = s;
+  __syncthreads();
+  if (g == 0 && c < a.n) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += red[i][cl];
+    static_cast<E*>(a.db[d])[c] = (E)s;
+  }
 }
 
 }  // namespace
@@ -109,7 +133,7 @@ hipError_t launch_dz(const DzArgs& a, bool gated, int chunks, hipStream_t s) {
 
 template <typename E>
 hipError_t launch_sums(const SumsArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((linear_sums_kernel<E>), dim3((a.n + 63) / 64, a.parts), dim3(64), 0, s, a);
+  hipLaunchKernelGGL((linear_sums_kernel<E>), dim3((a.n + 31) / 32, a.parts), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -39,6 +39,13 @@ struct ProductArgs {
   LinEpilogue e;
 };
 
+// Two products of one launch (neither split).
+struct PairArgs {
+  ProductArgs dx, dw;
+  int first;     // workgroups of the one that comes first
+  int dw_first;  // which one that is
+};
+
 // Second pass of a split contraction.
 struct JoinArgs {
   const float* planes;
@@ -74,6 +81,9 @@ struct SumsArgs {
 template <typename E>
 hipError_t launch_product(const ProductArgs& a, int tile, int layout, bool gated, bool dma,
                           hipStream_t s);
+// tile: TILE_256 or TILE_256X128; both products' operands go to LDS directly.
+template <typename E>
+hipError_t launch_pair(const PairArgs& a, int tile, bool dx_transposed, hipStream_t s);
 template <typename E>
 hipError_t launch_stream(const ProductArgs& a, int blocks16, bool gated, bool vec, hipStream_t s);
 template <typename E>

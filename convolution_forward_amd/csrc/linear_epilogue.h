@@ -129,40 +129,111 @@ __device__ __forceinline__ void lin_act(float (&v)[N], int act, float alpha, flo
   }
 }
 
-// Activation and its derivative at v (for the backward passes, 16-bit or float32).
-__device__ __forceinline__ void act_and_slope(float v, int act, float alpha, float beta, float* a,
-                                              float* d) {
+// Activation and its derivative at v, for the backward passes.  FX (16-bit
+// gradients): the logistic function's two sides from one exponential of -|v| and one
+// reciprocal, each to a few ulps of its own size, and normal_tail_fast.
+template <bool FX>
+__device__ __forceinline__ void logistic_sides(float v, float* q, float* c) {
+  if constexpr (FX) {
+    const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * fabsf(v));
+    const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
+    *q = v < 0.0f ? small : big;
+    *c = v < 0.0f ? big : small;
+  } else {
+    *q = 1.0f / (1.0f + expf(-v));
+    *c = 1.0f / (1.0f + expf(v));
+  }
+}
+
+template <int ACT, bool FX>
+__device__ __forceinline__ void act_and_slope(float v, float alpha, float beta, float* a, float* d) {
+  if constexpr (ACT == 1) {
+    *a = v > 0.0f ? v : 0.0f;
+    *d = v > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (ACT == 2) {
+    if constexpr (FX) {
+      float q, c;
+      logistic_sides<true>(2.0f * v, &q, &c);
+      *a = tanh_fast(v);
+      *d = 4.0f * q * c;
+    } else {
+      const float t = tanhf(v);
+      *a = t;
+      *d = 1.0f - t * t;
+    }
+  } else if constexpr (ACT == 3) {
+    float q, c;
+    logistic_sides<FX>(v, &q, &c);
+    *a = q;
+    *d = q * c;
+  } else if constexpr (ACT == 4) {
+    float q, c;
+    logistic_sides<FX>(v, &q, &c);
+    *a = v * q;
+    *d = q * (1.0f + v * c);
+  } else if constexpr (ACT == 5) {
+    const float u = alpha * v + beta;
+    *a = fminf(fmaxf(u, 0.0f), 1.0f);
+    *d = u > 0.0f && u < 1.0f ? alpha : 0.0f;
+  } else if constexpr (ACT == 6) {
+    *a = v * fminf(fmaxf(v * (1.0f / 6.0f) + 0.5f, 0.0f), 1.0f);
+    *d = v >= 3.0f ? 1.0f : v <= -3.0f ? 0.0f : v * (1.0f / 3.0f) + 0.5f;
+  } else if constexpr (ACT == 7) {
+    *a = fminf(fmaxf(v, alpha), beta);
+    *d = v > alpha && v < beta ? 1.0f : 0.0f;
+  } else if constexpr (ACT == 8) {
+    *a = v >= 0.0f ? v : alpha * v;
+    *d = v >= 0.0f ? 1.0f : alpha;
+  } else if constexpr (ACT == 9) {
+    const float pdf = 0.39894228040143268f *
+                      (FX ? __builtin_amdgcn_exp2f(-0.72134752f * v * v) : expf(-0.5f * v * v));
+    float cdf;
+    if constexpr (FX) {
+      const float h = normal_tail_fast(v);
+      cdf = v < 0.0f ? h : 1.0f - h;
+    } else {
+      cdf = 0.5f * (1.0f + erff(v * 0.70710678118654752f));
+    }
+    *a = v * cdf;
+    *d = cdf + v * pdf;
+  } else if constexpr (ACT == 10) {
+    // with q = sigmoid(2u): gelu = v q, derivative q + v q (1 - q) 2u'
+    float q, c;
+    logistic_sides<FX>(1.5957691216057308f * (v + 0.044715f * v * v * v), &q, &c);
+    *a = v * q;
+    *d = q + v * q * c * 1.5957691216057308f * (1.0f + 0.134145f * v * v);
+  } else {
+    *a = v;
+    *d = 1.0f;
+  }
+}
+
+// Eight values behind one uniform branch: z becomes the derivative, f the activation.
+template <bool FX>
+__device__ __forceinline__ void acts_and_slopes(float (&z)[8], float (&f)[8], int act, float alpha,
+                                                float beta) {
   switch (act) {
-    case 1: *a = v > 0.0f ? v : 0.0f; *d = v > 0.0f ? 1.0f : 0.0f; return;
-    case 2: { const float t = tanhf(v); *a = t; *d = 1.0f - t * t; return; }
-    case 3: { const float q = 1.0f / (1.0f + expf(-v)); *a = q; *d = q / (1.0f + expf(v)); return; }
-    case 4: {
-      const float q = 1.0f / (1.0f + expf(-v)), c = 1.0f / (1.0f + expf(v));
-      *a = v * q; *d = q * (1.0f + v * c); return;
-    }
-    case 5: {
-      const float u = alpha * v + beta;
-      *a = fminf(fmaxf(u, 0.0f), 1.0f); *d = u > 0.0f && u < 1.0f ? alpha : 0.0f; return;
-    }
-    case 6:
-      *a = v * fminf(fmaxf(v * (1.0f / 6.0f) + 0.5f, 0.0f), 1.0f);
-      *d = v >= 3.0f ? 1.0f : v <= -3.0f ? 0.0f : v * (1.0f / 3.0f) + 0.5f;
-      return;
-    case 7: *a = fminf(fmaxf(v, alpha), beta); *d = v > alpha && v < beta ? 1.0f : 0.0f; return;
-    case 8: *a = v >= 0.0f ? v : alpha * v; *d = v >= 0.0f ? 1.0f : alpha; return;
-    case 9: {
-      const float cdf = 0.5f * (1.0f + erff(v * 0.70710678118654752f));
-      *a = v * cdf; *d = cdf + v * 0.39894228040143268f * expf(-0.5f * v * v); return;
-    }
-    case 10: {
-      // with s = sigmoid(2u): gelu = v s, derivative s + v s (1 - s) 2u'
-      const float u2 = 1.5957691216057308f * (v + 0.044715f * v * v * v);
-      const float s = 1.0f / (1.0f + expf(-u2)), c = 1.0f / (1.0f + expf(u2));
-      *a = v * s;
-      *d = s + v * s * c * 1.5957691216057308f * (1.0f + 0.134145f * v * v);
-      return;
-    }
-    default: *a = v; *d = 1.0f;
+#define CONVFWD_CASE(A)                                                              \
+  case A:                                                                            \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i) {                                  \
+      float d;                                                                       \
+      act_and_slope<A, FX>(z[i], alpha, beta, &f[i], &d);                            \
+      z[i] = d;                                                                      \
+    }                                                                                \
+    break;
+    CONVFWD_CASE(0)
+    CONVFWD_CASE(1)
+    CONVFWD_CASE(2)
+    CONVFWD_CASE(3)
+    CONVFWD_CASE(4)
+    CONVFWD_CASE(5)
+    CONVFWD_CASE(6)
+    CONVFWD_CASE(7)
+    CONVFWD_CASE(8)
+    CONVFWD_CASE(9)
+    CONVFWD_CASE(10)
+#undef CONVFWD_CASE
+    default: break;
   }
 }
 
@@ -223,6 +294,21 @@ __device__ __forceinline__ void finish_linear_runs(const LinEpilogue& e, int z, 
   if (in) {
     if (e.res_mode == 2) add(e.res, c * e.ldres);
     store(e.out[z], c * e.ldo);
+  }
+}
+
+// The sums as they are (gradients).
+template <typename E, int NR, typename Off>
+__device__ __forceinline__ void finish_plain_runs(const LinEpilogue& e, int z, long long c, int r,
+                                                  Off off, bool whole, const float (&v)[NR * 8]) {
+  E* p = static_cast<E*>(e.out[z]) + c * e.ldo + r;
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = v[n * 8 + i];
+    if (whole) store8(p + off(n), 8, true, t);
+    else store8(p + off(n), min(8, e.R - r - off(n)), e.vec, t);
   }
 }
 

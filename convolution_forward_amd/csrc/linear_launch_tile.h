@@ -59,4 +59,31 @@ hipError_t launch_product(const ProductArgs& a, int tile, int layout, bool gated
   return launch_layout<E, true, true>(a, tile, dma, s);
 }
 
+template <typename E>
+hipError_t launch_pair(const PairArgs& pair, int tile, bool dx_transposed, hipStream_t s) {
+  if constexpr (sizeof(E) == 2) {
+    PairArgs a = pair;
+    const int bc = tile == TILE_256 ? 256 : 128;
+    int grid[2], i = 0;
+    for (ProductArgs* p : {&a.dx, &a.dw}) {
+      p->ntr = (p->R + 255) / 256;
+      p->ntc = (p->C + bc - 1) / bc;
+      grid[i++] = p->ntr * p->ntc * p->nz;
+    }
+    // the longer contraction first: the shorter tiles then even out the last round
+    a.dw_first = a.dw.ktiles * a.dw.nseg > a.dx.ktiles * a.dx.nseg;
+    a.first = grid[a.dw_first];
+    const dim3 g(grid[0] + grid[1]), b(512);
+    if (dx_transposed) {
+      if (bc == 256) hipLaunchKernelGGL((linear_pair_kernel<E, true, 256>), g, b, 0, s, a);
+      else hipLaunchKernelGGL((linear_pair_kernel<E, true, 128>), g, b, 0, s, a);
+    } else {
+      if (bc == 256) hipLaunchKernelGGL((linear_pair_kernel<E, false, 256>), g, b, 0, s, a);
+      else hipLaunchKernelGGL((linear_pair_kernel<E, false, 128>), g, b, 0, s, a);
+    }
+    return hipGetLastError();
+  }
+  return hipErrorInvalidValue;  // 16-bit operands only
+}
+
 }  // namespace convfwd

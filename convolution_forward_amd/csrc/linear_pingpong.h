@@ -30,7 +30,7 @@ namespace lin {
 
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
-template <typename E, bool PT, bool QT, int BC, bool GATED>
+template <typename E, bool PT, bool QT, int BC, bool GATED, bool PLAIN = false>
 struct PingPong {
   static_assert(sizeof(E) == 2 && (BC == 256 || BC == 128), "16-bit operands");
   static constexpr int NT = 512, HR = 128, HC = BC / 2;
@@ -91,39 +91,65 @@ struct PingPong {
     }
     const unsigned lds0 = lds_addr(smem) + wave * 1024;
 
-    // The half at row `row` of an operand, step t: rows run along k, or are of
-    // constant k (T).  The descriptor ends with the last valid row (T: with the last
-    // valid k), so that everything past an end reads as zeros; it is empty past the
-    // last step and past the operand's rows.
-    auto issue = [&](auto transposed, const char* m0, const char* m1, long long ld, long long row,
-                     long long rows, int most, const int* off, int items, int kpiece, int t,
-                     unsigned lds) {
-      constexpr bool T = decltype(transposed)::value;
-      const int seg = t >= a.ktiles ? 1 : 0;
-      const int k0 = (t - (seg ? a.ktiles : 0)) * 64;
-      const int kk = min(a.K - k0, 64), ldb = (int)ld * 2;
-      const int n = (int)min(rows, (long long)most);
-      int bytes = T ? (kk - 1) * ldb + ((n + 7) & ~7) * 2 : (n - 1) * ldb + ((kk + 7) & ~7) * 2;
-      bytes = n <= 0 || t >= t1 ? 0 : bytes;
-      const char* p = (seg ? m1 : m0) + (T ? k0 * ld + row : row * ld + k0) * 2;
-      const i32x4 rs = make_rsrc(p, bytes);
+    // What the loads of a step need, moved on from step to step in small pieces
+    // between a phase's products: scalar code costs a wave 4 cycles an instruction,
+    // and the reading side of a turn has none to spare.  A descriptor ends with the
+    // last valid row (transposed: the last valid k), so that everything past an end
+    // reads as zeros; it is empty past the last step and past the operand's rows.
+    constexpr int kNone = -(1 << 30);
+    const int ldpb = (int)a.ldp * 2, ldqb = (int)a.ldq * 2;
+    const int seg0 = t0 >= a.ktiles ? 1 : 0, kt0 = t0 - (seg0 ? a.ktiles : 0);
+    const long long pstep = PT ? 64LL * ldpb : 128, qstep = QT ? 64LL * ldqb : 128;
+    const char *pb[2], *qb[2], *pseg[2], *qseg[2];  // present, and of the second segment
+    int pspan[2], qspan[2];
 #pragma unroll
-      for (int i = 0; i < items; ++i)
-        dma16(rs, !T && kpiece >= kk ? kOob : off[i], lds + i * NT * 16);
+    for (int h = 0; h < 2; ++h) {
+      const long long pr = r0 + (GATED ? 0 : h * HR), qr = c0 + h * HC;
+      const long long po = PT ? pr * 2 : pr * ldpb, qo = QT ? qr * 2 : qr * ldqb;
+      pseg[h] = static_cast<const char*>(a.P[1]) + po;
+      qseg[h] = static_cast<const char*>(a.Q[1]) + qo;
+      pb[h] = (GATED ? h : seg0) ? pseg[h] : static_cast<const char*>(a.P[0]) + po;
+      qb[h] = seg0 ? qseg[h] : static_cast<const char*>(a.Q[z]) + qo;
+      pb[h] += kt0 * pstep;
+      qb[h] += kt0 * qstep;
+      const int np = (int)min(a.R - pr, (long long)HR), nq = (int)min(a.C - qr, (long long)HC);
+      pspan[h] = np <= 0 ? kNone : PT ? ((np + 7) & ~7) * 2 : (np - 1) * ldpb;
+      qspan[h] = nq <= 0 ? kNone : QT ? ((nq + 7) & ~7) * 2 : (nq - 1) * ldqb;
+    }
+    int count = t0, left = a.K - kt0 * 64, kk, pbytes, qbytes;
+    const int ktail = a.K - (a.K - 1) / 64 * 64;  // k of a segment's last step
+    const bool ptail = PT || pk < ktail, qtail = QT || qk < ktail;
+    bool turn = false;
+    auto stage = [&](int n) {
+      if (n == 0) {
+        ++count;
+        turn = !GATED && count == a.ktiles;
+        left = turn ? a.K : left - 64;
+      } else if (n == 1) {
+        kk = count < t1 ? min(left, 64) : kNone;
+      } else if (n == 2) {
+        pbytes = kk < 0 ? kNone : PT ? (kk - 1) * ldpb : ((kk + 7) & ~7) * 2;
+      } else if (n == 3) {
+        qbytes = kk < 0 ? kNone : QT ? (kk - 1) * ldqb : ((kk + 7) & ~7) * 2;
+      } else if (n < 6) {
+        pb[n - 4] = turn ? pseg[n - 4] : pb[n - 4] + pstep;
+      } else {
+        qb[n - 6] = turn ? qseg[n - 6] : qb[n - 6] + qstep;
+      }
     };
-    const char* const P0 = static_cast<const char*>(a.P[0]);
-    const char* const P1 = static_cast<const char*>(a.P[1]);
-    const char* const Q0 = static_cast<const char*>(a.Q[z]);
-    const char* const Q1 = static_cast<const char*>(a.Q[1]);
-    auto issue_p = [&](int t, int half, int buf) {
-      const char* m = GATED && half ? P1 : P0;
-      const int h = GATED ? 0 : half * HR;
-      issue(std::integral_constant<bool, PT>(), m, GATED ? m : P1, a.ldp, r0 + h, nr - h, HR, poff,
-            TP::ITEMS, pk, t, lds0 + p_at(half, buf));
+    auto issue_p = [&](int half, int buf) {
+      const i32x4 rs = make_rsrc(pb[half], max(pspan[half] + pbytes, 0));
+      const bool all = kk >= 64 || ptail;
+#pragma unroll
+      for (int i = 0; i < TP::ITEMS; ++i)
+        dma16(rs, all ? poff[i] : kOob, lds0 + p_at(half, buf) + i * NT * 16);
     };
-    auto issue_q = [&](int t, int half, int buf) {
-      issue(std::integral_constant<bool, QT>(), Q0, Q1, a.ldq, c0 + half * HC, nc - half * HC, HC,
-            qoff, TQ::ITEMS, qk, t, lds0 + q_at(half, buf));
+    auto issue_q = [&](int half, int buf) {
+      const i32x4 rs = make_rsrc(qb[half], max(qspan[half] + qbytes, 0));
+      const bool all = kk >= 64 || qtail;
+#pragma unroll
+      for (int i = 0; i < TQ::ITEMS; ++i)
+        dma16(rs, all ? qoff[i] : kOob, lds0 + q_at(half, buf) + i * NT * 16);
     };
 
     typename TP::Frag p[NI][2];
@@ -144,56 +170,71 @@ struct PingPong {
     };
     // end of a phase's reads: they are in registers, and the half that the next
     // phase reads has arrived for every wave behind the barrier
-    auto turn = [&] {
+    auto turn_over = [&] {
       lds_wait();
       vm_wait<FLIGHT>();
       fence();
       barrier();
       fence();
     };
-    auto multiply_all = [&](int hp, int hq) {
+    // a quadrant's products; with MOVE the state of the loads moves on between them
+    auto multiply_all = [&](int hp, int hq, auto move) {
+      constexpr bool MOVE = decltype(move)::value;
+      constexpr int N = 2 * NI * NJ, EACH = N / 8;
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int j2 = 0; j2 < 2; ++j2)
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            acc[hp][hq][i][j] = multiply<E>(p[i][j2], q[hq][j][j2], acc[hp][hq][i][j]);
+      for (int n = 0; n < N; ++n) {
+        const int j2 = n / (NI * NJ), i = n / NJ % NI, j = n % NJ;
+        acc[hp][hq][i][j] = multiply<E>(p[i][j2], q[hq][j][j2], acc[hp][hq][i][j]);
+        if (MOVE && n % EACH == EACH - 1) {
+          fence();
+          stage(n / EACH);
+          fence();
+        }
+      }
       __builtin_amdgcn_s_setprio(0);
       fence();
       barrier();
       fence();
     };
-    // one contraction step in buffer F (its parity): halves f = F, s = 1 - F of Q
-    auto step = [&](int t, auto parity) {
+    constexpr std::integral_constant<bool, false> stay;
+    constexpr std::integral_constant<bool, true> move;
+    // one contraction step in buffer F (its parity): halves f = F, s = 1 - F of Q; the
+    // loads are those of two steps later
+    auto step = [&](auto parity) {
       constexpr int F = decltype(parity)::value, S = 1 - F;
       read_p(0, F);
-      issue_q(t + 2, F, F);
-      turn();
-      multiply_all(0, F);
+      issue_q(F, F);
+      turn_over();
+      multiply_all(0, F, stay);
       read_q(S, F);
-      issue_p(t + 2, 0, F);
-      turn();
-      multiply_all(0, S);
+      issue_p(0, F);
+      turn_over();
+      multiply_all(0, S, stay);
       read_p(1, F);
-      issue_q(t + 2, S, F);
-      turn();
-      multiply_all(1, S);
+      issue_q(S, F);
+      turn_over();
+      multiply_all(1, S, stay);
       read_q(S, S);  // the next step's first half
-      issue_p(t + 2, 1, F);
-      turn();
-      multiply_all(1, F);
+      issue_p(1, F);
+      turn_over();
+      multiply_all(1, F, move);
     };
 
-    issue_q(t0, 0, 0);
-    issue_p(t0, 0, 0);
-    issue_q(t0, 1, 0);
-    issue_p(t0, 1, 0);
-    issue_q(t0 + 1, 1, 1);
-    issue_p(t0 + 1, 0, 1);
-    issue_q(t0 + 1, 0, 1);
-    issue_p(t0 + 1, 1, 1);
+#pragma unroll
+    for (int n = 1; n < 4; ++n) {
+      if (n == 1) kk = min(left, 64);
+      else stage(n);
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      issue_q(b, b);
+      issue_p(0, b);
+      issue_q(1 - b, b);
+      issue_p(1, b);
+#pragma unroll
+      for (int n = 0; n < 8; ++n) stage(n);
+    }
     vm_wait<FLIGHT>();
     barrier();
     read_q(0, 0);
@@ -204,8 +245,8 @@ struct PingPong {
     if (late) barrier();
     fence();
     for (int t = t0; t < t1; t += 2) {  // an odd count ends with a step of zeros
-      step(t, std::integral_constant<int, 0>());
-      step(t + 1, std::integral_constant<int, 1>());
+      step(std::integral_constant<int, 0>());
+      step(std::integral_constant<int, 1>());
     }
     if (!late) barrier();
     vm_wait<0>();  // loads past the end (zeros) land before the workgroup's LDS is given up
@@ -231,7 +272,7 @@ struct PingPong {
         }
       const long long c = c0 + round / NJ * HC + wc * WC + round % NJ * 16 + (lane & 15);
       const bool in = c < a.C;
-      if (a.splits > 1) {
+      if (!PLAIN && a.splits > 1) {
         constexpr int KINDS = GATED ? 2 : 1;
         float* d = a.planes + (((long long)split * a.nz + z) * KINDS * a.C + c) * a.plane_ld + rl;
 #pragma unroll
@@ -243,6 +284,8 @@ struct PingPong {
               if constexpr (GATED) d[(long long)a.C * a.plane_ld + off(n) + e] = u[n * 8 + e];
             }
           }
+      } else if constexpr (PLAIN) {
+        if (in) finish_plain_runs<E, NR>(a.e, z, c, rl, off, whole, v);
       } else if constexpr (GATED) {
         finish_gated_runs<E, NR>(a.e, c, in, rl, off, whole, v, u);
       } else {
@@ -259,6 +302,23 @@ __global__ __launch_bounds__(512) void linear_pingpong_kernel(const ProductArgs 
   using K = lin::PingPong<E, PT, QT, BC, GATED>;
   __shared__ __attribute__((aligned(1024))) char smem[K::SMEM];
   K::run(a, xcd_logical(blockIdx.x, gridDim.x), smem);
+}
+
+// The two products of a backward pass in one launch, the one with the longer
+// contraction first: dx = dz w (DT: w transposed in the sense of linear_tile.h) and
+// dw = dz^T x.  Each alone often fills part of the card's last round of workgroups
+// only; together they fill one another's.
+template <typename E, bool DT, int BC>
+__global__ __launch_bounds__(512) void linear_pair_kernel(const PairArgs a) {
+  using DX = lin::PingPong<E, DT, false, BC, false, true>;
+  using DW = lin::PingPong<E, true, true, BC, false, true>;
+  static_assert(DX::SMEM == DW::SMEM, "one buffer for both");
+  __shared__ __attribute__((aligned(1024))) char smem[DX::SMEM];
+  const bool second = (int)blockIdx.x >= a.first;
+  const int id = second ? xcd_logical(blockIdx.x - a.first, gridDim.x - a.first)
+                        : xcd_logical(blockIdx.x, a.first);
+  if (second != a.dw_first) DW::run(a.dw, id, smem);
+  else DX::run(a.dx, id, smem);
 }
 
 }  // namespace convfwd

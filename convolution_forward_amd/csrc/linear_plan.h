@@ -31,6 +31,7 @@ struct ProductPlan {
   int stream_t;     // stream: 16-row blocks of Q
   int64_t plane_ld; // floats per plane row
   int64_t planes_bytes;
+  double time;      // estimated, us
 };
 
 struct LinearGeo {
@@ -67,6 +68,9 @@ int linear_validate(const linear_problem* p, int dtype, LinearGeo* g);
 int gated_validate(const gated_problem* p, int dtype, GatedGeo* g);
 
 ProductPlan plan_product(const ProductShape& s, int es);
+// The tile (TILE_256 or TILE_256X128) of one launch for both products of a backward
+// pass, or -1 where they run one after the other.
+int plan_pair(const ProductShape& dx, const ProductShape& dw, int es);
 ColsumPlan plan_colsum(int64_t m, int64_t n);
 
 // The products of each call, from the geometry and offsets alone.
