@@ -19,10 +19,10 @@ T* at(T* p, int64_t off, int es) {
   return p ? static_cast<T*>(static_cast<C*>(p) + off * es) : nullptr;
 }
 
-bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
-// An operand row stride of whole 16-byte pieces from an aligned base.
-bool rows16(const void* p, int64_t ld, int es) { return al16(p) && ld * es % 16 == 0; }
+// Rows that start on multiples of 4 bytes.
+bool rows4(const void* p, int64_t ld, int es) {
+  return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld * es % 4 == 0;
+}
 
 hipError_t product(int dtype, const ProductArgs& a, int tile, int layout, bool gated, bool dma,
                    hipStream_t s) {
@@ -31,11 +31,11 @@ hipError_t product(int dtype, const ProductArgs& a, int tile, int layout, bool g
   return launch_product<float>(a, tile, layout, gated, dma, s);
 }
 
-hipError_t stream_product(int dtype, const ProductArgs& a, int blocks16, bool gated, bool vec,
-                          hipStream_t s) {
-  if (dtype == CONV_F16) return launch_stream<_Float16>(a, blocks16, gated, vec, s);
-  if (dtype == CONV_BF16) return launch_stream<__bf16>(a, blocks16, gated, vec, s);
-  return launch_stream<float>(a, blocks16, gated, vec, s);
+hipError_t stream_product(int dtype, const ProductArgs& a, int blocks16, int rows, bool gated,
+                          bool vec, hipStream_t s) {
+  if (dtype == CONV_F16) return launch_stream<_Float16>(a, blocks16, rows, gated, vec, s);
+  if (dtype == CONV_BF16) return launch_stream<__bf16>(a, blocks16, rows, gated, vec, s);
+  return launch_stream<float>(a, blocks16, rows, gated, vec, s);
 }
 
 hipError_t join(int dtype, const JoinArgs& a, bool gated, hipStream_t s) {
@@ -56,12 +56,12 @@ hipError_t sums_pass(int dtype, const SumsArgs& a, hipStream_t s) {
   return launch_sums<float>(a, s);
 }
 
-// Whether the operands can go to LDS directly: aligned bases, row strides and
-// contiguous extents of whole 16-byte pieces, or rows padded to that with zeros.
+// Whether the operands can go to LDS directly: rows from multiples of 4 bytes, of
+// whole 16-byte pieces or padded to that with zeros.
 bool direct(const ProductShape& s, const ProductArgs& a, int es, bool p_padded, bool q_padded) {
   for (int i = 0; i < 2; ++i) {
-    if (a.P[i] && !rows16(a.P[i], a.ldp, es)) return false;
-    if (a.Q[i] && !rows16(a.Q[i], a.ldq, es)) return false;
+    if (a.P[i] && !rows4(a.P[i], a.ldp, es)) return false;
+    if (a.Q[i] && !rows4(a.Q[i], a.ldq, es)) return false;
   }
   if (!p_padded && (s.pt ? s.R : s.K) * es % 16 != 0) return false;
   return q_padded || (s.qt ? s.C : s.K) * es % 16 == 0;
@@ -79,7 +79,7 @@ hipError_t run_product(const ProductShape& s, int dtype, ProductArgs& a, bool p_
   a.plane_ld = pl.plane_ld;
   a.e.R = a.R;
   const bool dma = direct(s, a, es, p_padded, q_padded);
-  if (pl.tile == TILE_STREAM) return stream_product(dtype, a, pl.stream_t, s.gated, dma, st);
+  if (pl.tile == TILE_STREAM) return stream_product(dtype, a, pl.stream_t, pl.stream_rows, s.gated, dma, st);
   const int layout = s.pt ? (s.qt ? 2 : 1) : 0;
   hipError_t e = product(dtype, a, pl.tile, layout, s.gated, dma, st);
   if (e != hipSuccess || pl.splits == 1) return e;
@@ -105,7 +105,7 @@ hipError_t run_both(const ProductShape& sx, const ProductShape& sw, int dtype, P
                     ProductArgs& dw, bool dx_p_padded, bool dx_q_padded, bool dw_p_padded,
                     bool dw_q_padded, void* planes, hipStream_t st) {
   const int es = (int)dtype_size(dtype);
-  const int tile = plan_pair(sx, sw, es);
+  const int tile = plan_pair(sx, sw, es).tile;
   if (tile >= 0 && direct(sx, dx, es, dx_p_padded, dx_q_padded) &&
       direct(sw, dw, es, dw_p_padded, dw_q_padded)) {
     PairArgs a{};
@@ -127,6 +127,32 @@ hipError_t run_both(const ProductShape& sx, const ProductShape& sw, int dtype, P
   return e != hipSuccess ? e : run_product(sw, dtype, dw, dw_p_padded, dw_q_padded, planes, st);
 }
 
+// Copies the operands that the plan packs and points to the copies.  src[i] and ld[i]:
+// the i-th item's operand (null: not wanted by this call).
+hipError_t run_pack(const Packing& k, int dtype, const void** src, int64_t* ld, void* scratch,
+                    hipStream_t s) {
+  PackArgs a{};
+  const int es = (int)dtype_size(dtype);
+  for (int i = 0; i < k.n; ++i) {
+    const PackItem& q = k.item[i];
+    if (!k.on || !q.need || !src[i] || q.rows == 0) continue;
+    a.src[a.n] = src[i];
+    a.dst[a.n] = static_cast<char*>(scratch) + q.off;
+    a.ld[a.n] = ld[i];
+    a.packed_ld[a.n] = q.packed_ld;
+    a.pieces[a.n] = q.rows * (q.packed_ld * es / 16);
+    a.cols[a.n] = (int)q.cols;
+    a.first[a.n + 1] = a.first[a.n] + (int)ceil_div(a.pieces[a.n], 1024);
+    src[i] = a.dst[a.n];
+    ld[i] = q.packed_ld;
+    ++a.n;
+  }
+  if (a.n == 0) return hipSuccess;
+  if (dtype == CONV_F16) return launch_pack<_Float16>(a, s);
+  if (dtype == CONV_BF16) return launch_pack<__bf16>(a, s);
+  return launch_pack<float>(a, s);
+}
+
 int status(hipError_t e) { return e == hipSuccess ? CONV_OK : CONV_ERR_DEVICE; }
 
 }  // namespace
@@ -141,10 +167,16 @@ int linear_forward(const linear_problem* p, int dtype, const void* x, const void
   LinearGeo g;
   linear_validate(p, dtype, &g);
   if (g.m == 0) return CONV_OK;
+  const LinearPlan pl = plan_linear(p, g);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const void* src[3] = {at(x, p->x_off, g.es), at(w, p->w_off, g.es)};
+  int64_t ld[3] = {g.ldx, g.ldw};
+  const hipError_t packed = run_pack(pl.pack, dtype, src, ld, scratch, s);
+  if (packed != hipSuccess) return status(packed);
   ProductArgs a{};
-  a.P[0] = at(w, p->w_off, g.es);
-  a.Q[0] = at(x, p->x_off, g.es);
-  a.ldp = g.ldw; a.ldq = g.ldx;
+  a.P[0] = src[1];
+  a.Q[0] = src[0];
+  a.ldp = ld[1]; a.ldq = ld[0];
   LinEpilogue& e = a.e;
   e.bias[0] = p->has_bias ? at(b, p->b_off, g.es) : nullptr;
   e.res = p->has_residual ? at(r, p->r_off, g.es) : nullptr;
@@ -153,10 +185,7 @@ int linear_forward(const linear_problem* p, int dtype, const void* x, const void
   e.save[0] = p->save_z ? at(z, p->z_off, g.es) : nullptr;
   e.ldo = g.ldy; e.ldres = g.ldr; e.ldsave = g.ldz;
   e.act = p->activation; e.alpha = p->act_alpha; e.beta = p->act_beta;
-  e.vec = rows16(e.out[0], g.ldy, g.es) && (!e.bias[0] || al16(e.bias[0])) &&
-          (!e.res || rows16(e.res, g.ldr, g.es)) && (!e.save[0] || rows16(e.save[0], g.ldz, g.es));
-  return status(run_product(linear_product(p, g), dtype, a, false, false, scratch,
-                            static_cast<hipStream_t>(stream)));
+  return status(run_product(pl.product, dtype, a, pl.pack.on, pl.pack.on, scratch, s));
 }
 
 int gated_forward(const gated_problem* p, int dtype, const void* x, const void* wg, const void* wu,
@@ -167,11 +196,17 @@ int gated_forward(const gated_problem* p, int dtype, const void* x, const void* 
   GatedGeo g;
   gated_validate(p, dtype, &g);
   if (g.m == 0) return CONV_OK;
+  const GatedPlan pl = plan_gated(p, g);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const void* src[3] = {at(x, p->x_off, g.es), at(wg, p->wg_off, g.es), at(wu, p->wu_off, g.es)};
+  int64_t ld[3] = {g.ldx, g.ldw, g.ldw};
+  const hipError_t packed = run_pack(pl.pack, dtype, src, ld, scratch, s);
+  if (packed != hipSuccess) return status(packed);
   ProductArgs a{};
-  a.P[0] = at(wg, p->wg_off, g.es);
-  a.P[1] = at(wu, p->wu_off, g.es);
-  a.Q[0] = at(x, p->x_off, g.es);
-  a.ldp = g.ldw; a.ldq = g.ldx;
+  a.P[0] = src[1];
+  a.P[1] = src[2];
+  a.Q[0] = src[0];
+  a.ldp = ld[1]; a.ldq = ld[0];
   LinEpilogue& e = a.e;
   if (p->has_bias) {
     e.bias[0] = at(bg, p->bg_off, g.es);
@@ -184,11 +219,7 @@ int gated_forward(const gated_problem* p, int dtype, const void* x, const void* 
   }
   e.ldo = g.ldh; e.ldsave = g.ldp;
   e.act = p->activation; e.alpha = p->act_alpha; e.beta = p->act_beta;
-  e.vec = rows16(e.out[0], g.ldh, g.es) &&
-          (!e.bias[0] || (al16(e.bias[0]) && al16(e.bias[1]))) &&
-          (!e.save[0] || (rows16(e.save[0], g.ldp, g.es) && al16(e.save[1])));
-  return status(run_product(gated_product(p, g), dtype, a, false, false, scratch,
-                            static_cast<hipStream_t>(stream)));
+  return status(run_product(pl.product, dtype, a, pl.pack.on, pl.pack.on, scratch, s));
 }
 
 int linear_backward(const linear_problem* p, int dtype, const void* x, const void* w, const void* z,
@@ -198,7 +229,8 @@ int linear_backward(const linear_problem* p, int dtype, const void* x, const voi
   if (st) return st;
   LinearGeo g;
   linear_validate(p, dtype, &g);
-  const BackwardScratch sc = linear_backward_scratch(p, g);
+  const BackwardPlan pl = plan_linear_backward(p, g);
+  const BackwardScratch& sc = pl.scratch;
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* sb = static_cast<char*>(scratch);
   const bool act = p->activation != CONV_ACT_IDENTITY;
@@ -222,8 +254,6 @@ int linear_backward(const linear_problem* p, int dtype, const void* x, const voi
     a.m = g.m; a.rows = cp.rows;
     a.n = (int)g.n; a.np = (int)round_up(g.n, 8);
     a.alpha = p->act_alpha; a.beta = p->act_beta;
-    a.vec = rows16(dy, g.ldy, g.es) && (!a.z[0] || rows16(a.z[0], g.ldz, g.es)) &&
-            (!dr || rows16(dr, g.lddr, g.es));
     e = dz_pass(dtype, a, false, (int)cp.chunks, s);
     if (e == hipSuccess && db) {
       SumsArgs q{};
@@ -233,35 +263,36 @@ int linear_backward(const linear_problem* p, int dtype, const void* x, const voi
       e = sums_pass(dtype, q, s);
     }
   }
-  const void* d = act ? static_cast<const void*>(sb + sc.dz) : dy;
-  const int64_t ldd = act ? sc.dz_ld : g.ldy;
   const bool want_dx = dx && g.m > 0;
+  const void* src[3] = {dw ? at(x, p->x_off, g.es) : nullptr, want_dx ? at(w, p->w_off, g.es) : nullptr,
+                        act ? static_cast<const void*>(sb + sc.dz) : dx || dw ? dy : nullptr};
+  int64_t ld[3] = {g.ldx, g.ldw, act ? sc.dz_ld : g.ldy};
+  if (e == hipSuccess) e = run_pack(pl.pack, dtype, src, ld, scratch, s);
+  const bool on = pl.pack.on;
   ProductArgs ax{}, aw{};
   if (want_dx) {
-    ax.P[0] = at(w, p->w_off, g.es);
-    ax.Q[0] = d;
-    ax.ldp = g.ldw; ax.ldq = ldd;
+    ax.P[0] = src[1];
+    ax.Q[0] = src[2];
+    ax.ldp = ld[1]; ax.ldq = ld[2];
     ax.e.out[0] = at(dx, p->dx_off, g.es);
     ax.e.ldo = g.lddx;
-    ax.e.vec = rows16(ax.e.out[0], g.lddx, g.es);
   }
   if (dw) {
-    const void* xb = at(x, p->x_off, g.es);
-    aw.P[0] = g.kn ? d : xb;
-    aw.Q[0] = g.kn ? xb : d;
-    aw.ldp = g.kn ? ldd : g.ldx;
-    aw.ldq = g.kn ? g.ldx : ldd;
+    aw.P[0] = g.kn ? src[2] : src[0];
+    aw.Q[0] = g.kn ? src[0] : src[2];
+    aw.ldp = g.kn ? ld[2] : ld[0];
+    aw.ldq = g.kn ? ld[0] : ld[2];
     aw.e.out[0] = at(dw, p->dw_off, g.es);
     aw.e.ldo = g.lddw;
-    aw.e.vec = rows16(aw.e.out[0], g.lddw, g.es);
   }
-  const ProductShape sx = linear_dx_product(p, g), sw = linear_dw_product(p, g);
+  // rows padded with zeros: packed ones, and dz
+  const bool dpad = on || act, wp = g.kn ? dpad : on, wq = g.kn ? on : dpad;
   if (e == hipSuccess && want_dx && dw)
-    e = run_both(sx, sw, dtype, ax, aw, false, act, act && g.kn, act && !g.kn, sb + sc.planes, s);
+    e = run_both(pl.dx, pl.dw, dtype, ax, aw, on, dpad, wp, wq, sb + sc.planes, s);
   else if (e == hipSuccess && want_dx)
-    e = run_product(sx, dtype, ax, false, act, sb + sc.planes, s);
+    e = run_product(pl.dx, dtype, ax, on, dpad, sb + sc.planes, s);
   else if (e == hipSuccess && dw)
-    e = run_product(sw, dtype, aw, act && g.kn, act && !g.kn, sb + sc.planes, s);
+    e = run_product(pl.dw, dtype, aw, wp, wq, sb + sc.planes, s);
   return status(e);
 }
 
@@ -273,7 +304,8 @@ int gated_backward(const gated_problem* p, int dtype, const void* x, const void*
   if (st) return st;
   GatedGeo g;
   gated_validate(p, dtype, &g);
-  const BackwardScratch sc = gated_backward_scratch(p, g);
+  const BackwardPlan pl = plan_gated_backward(p, g);
+  const BackwardScratch& sc = pl.scratch;
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* sb = static_cast<char*>(scratch);
   const ColsumPlan cp = plan_colsum(g.m, g.f);
@@ -287,7 +319,6 @@ int gated_backward(const gated_problem* p, int dtype, const void* x, const void*
   a.m = g.m; a.rows = cp.rows;
   a.n = (int)g.f; a.np = (int)round_up(g.f, 8);
   a.act = p->activation; a.alpha = p->act_alpha; a.beta = p->act_beta;
-  a.vec = rows16(a.dy, g.ldh, g.es) && rows16(a.z[0], g.ldp, g.es) && al16(a.z[1]);
   hipError_t e = dz_pass(dtype, a, true, (int)cp.chunks, s);
   if (e == hipSuccess && dbg) {
     SumsArgs q{};
@@ -300,34 +331,37 @@ int gated_backward(const gated_problem* p, int dtype, const void* x, const void*
   const char* dg = sb + sc.dz;
   const char* du = dg + (int64_t)a.np * g.es;
   const bool want_dx = dx && g.m > 0;
+  const void* src[3] = {dwg ? at(x, p->x_off, g.es) : nullptr,
+                        want_dx ? at(wg, p->wg_off, g.es) : nullptr,
+                        want_dx ? at(wu, p->wu_off, g.es) : nullptr};
+  int64_t ld[3] = {g.ldx, g.ldw, g.ldw};
+  if (e == hipSuccess) e = run_pack(pl.pack, dtype, src, ld, scratch, s);
+  const bool on = pl.pack.on;
   ProductArgs ax{}, aw{};
   if (want_dx) {
-    ax.P[0] = at(wg, p->wg_off, g.es);
-    ax.P[1] = at(wu, p->wu_off, g.es);
+    ax.P[0] = src[1];
+    ax.P[1] = src[2];
     ax.Q[0] = dg;
     ax.Q[1] = du;
-    ax.ldp = g.ldw; ax.ldq = sc.dz_ld;
+    ax.ldp = ld[1]; ax.ldq = sc.dz_ld;
     ax.e.out[0] = at(dx, p->dx_off, g.es);
     ax.e.ldo = g.lddx;
-    ax.e.vec = rows16(ax.e.out[0], g.lddx, g.es);
   }
   if (dwg) {
-    aw.P[0] = at(x, p->x_off, g.es);
+    aw.P[0] = src[0];
     aw.Q[0] = dg;
     aw.Q[1] = du;
-    aw.ldp = g.ldx; aw.ldq = sc.dz_ld;
+    aw.ldp = ld[0]; aw.ldq = sc.dz_ld;
     aw.e.out[0] = at(dwg, p->dwg_off, g.es);
     aw.e.out[1] = at(dwu, p->dwu_off, g.es);
     aw.e.ldo = g.lddw;
-    aw.e.vec = rows16(aw.e.out[0], g.lddw, g.es) && al16(aw.e.out[1]);
   }
-  const ProductShape sx = gated_dx_product(p, g), sw = gated_dw_product(p, g);
   if (e == hipSuccess && want_dx && dwg)
-    e = run_both(sx, sw, dtype, ax, aw, false, true, false, true, sb + sc.planes, s);
+    e = run_both(pl.dx, pl.dw, dtype, ax, aw, on, true, on, true, sb + sc.planes, s);
   else if (e == hipSuccess && want_dx)
-    e = run_product(sx, dtype, ax, false, true, sb + sc.planes, s);
+    e = run_product(pl.dx, dtype, ax, on, true, sb + sc.planes, s);
   else if (e == hipSuccess && dwg)
-    e = run_product(sw, dtype, aw, false, true, sb + sc.planes, s);
+    e = run_product(pl.dw, dtype, aw, on, true, sb + sc.planes, s);
   return status(e);
 }
 

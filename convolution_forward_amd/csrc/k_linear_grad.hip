@@ -8,7 +8,7 @@
 // the unrounded float32 values: each thread 8 columns of every 8th row of a chunk,
 // the 8 row groups joined in order through LDS, one float32 row per chunk, and the
 // chunks joined in order by a second kernel.
-#include "linear_epilogue.h"
+#include "linear_tile.h"
 
 namespace convfwd {
 
@@ -40,9 +40,9 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const DzArgs a) {
       for (int k = 0; k < 2; ++k) {
         if (k == 1 && !two) break;
         const long long row = m + 8 * k;
-        load8(gy + row * a.ldy, nv, a.vec, dy[k]);
-        if (GATED || a.act != 0) load8(gz + row * a.ldz, nv, a.vec, z[k]);
-        if constexpr (GATED) load8(gu + row * a.ldz, nv, a.vec, t[k]);
+        load8(gy + row * a.ldy, nv, dy[k]);
+        if (GATED || a.act != 0) load8(gz + row * a.ldz, nv, z[k]);
+        if constexpr (GATED) load8(gu + row * a.ldz, nv, t[k]);
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -59,8 +59,8 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const DzArgs a) {
             sum[KINDS - 1][i] += t[k][i];
           }
           E* o = static_cast<E*>(a.dz) + row * a.lddz + col;
-          store8(o, 8, true, z[k]);
-          store8(o + a.np, 8, true, t[k]);
+          store8(o, 8, z[k]);
+          store8(o + a.np, 8, t[k]);
         } else {
           if (a.act != 0) {
             acts_and_slopes<FX>(z[k], f, a.act, a.alpha, a.beta);
@@ -72,9 +72,9 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const DzArgs a) {
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum[0][i] += t[k][i];
-          if (a.dz) store8(static_cast<E*>(a.dz) + row * a.lddz + col, 8, true, t[k]);
+          if (a.dz) store8(static_cast<E*>(a.dz) + row * a.lddz + col, 8, t[k]);
           if (a.dr)
-            store8(static_cast<E*>(a.dr) + row * a.lddr + col, nv, a.vec, a.dr_is_dy ? dy[k] : t[k]);
+            store8(static_cast<E*>(a.dr) + row * a.lddr + col, nv, a.dr_is_dy ? dy[k] : t[k]);
         }
       }
     }
@@ -121,7 +121,43 @@ __global__ __launch_bounds__(256) void linear_sums_kernel(const SumsArgs a) {
   }
 }
 
+// Operands with odd rows, copied so that the products can load them to LDS directly:
+// a thread moves 16-byte pieces, the last one of a row loaded from further back and
+// shifted.  Bound by memory: every element is read and written once.
+template <typename E>
+__global__ __launch_bounds__(256) void linear_pack_kernel(const PackArgs a) {
+  constexpr int EPC = 16 / (int)sizeof(E), PER = 4;
+  using R = lin::Ragged<E, false>;
+  int q = 0;
+  while (q + 1 < a.n && (int)blockIdx.x >= a.first[q + 1]) ++q;
+  const int cols = a.cols[q], ppr = (int)(a.packed_ld[q] / EPC);
+  const long long at = (long long)((int)blockIdx.x - a.first[q]) * 256 * PER + threadIdx.x;
+  lin::i32x4 v[PER];
+  int piece[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const long long id = min(at + i * 256, a.pieces[q] - 1);
+    const long long row = a.pieces[q] < (1LL << 31) ? (unsigned)id / (unsigned)ppr : id / ppr;
+    piece[i] = (int)(id - row * ppr);
+    const E* p = static_cast<const E*>(a.src[q]) + row * a.ld[q];
+    if (cols >= EPC)
+      v[i] = lin::load_piece<E>(reinterpret_cast<const char*>(p), min(piece[i] * EPC, cols - EPC) * (int)sizeof(E));
+    else
+      v[i] = R::raw(p, 0, 0, 0, 1, cols, true);
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (at + i * 256 < a.pieces[q])
+      static_cast<lin::i32x4*>(a.dst[q])[at + i * 256] = cols >= EPC ? R::shift(v[i], piece[i], cols) : v[i];
+}
+
 }  // namespace
+
+template <typename E>
+hipError_t launch_pack(const PackArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((linear_pack_kernel<E>), dim3(a.first[a.n]), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
 
 template <typename E>
 hipError_t launch_dz(const DzArgs& a, bool gated, int chunks, hipStream_t s) {
@@ -139,7 +175,8 @@ hipError_t launch_sums(const SumsArgs& a, hipStream_t s) {
 
 #define CONVFWD_INST(E)                                                          \
   template hipError_t launch_dz<E>(const DzArgs&, bool, int, hipStream_t);      \
-  template hipError_t launch_sums<E>(const SumsArgs&, hipStream_t);
+  template hipError_t launch_sums<E>(const SumsArgs&, hipStream_t);             \
+  template hipError_t launch_pack<E>(const PackArgs&, hipStream_t);
 CONVFWD_INST(_Float16)
 CONVFWD_INST(__bf16)
 CONVFWD_INST(float)

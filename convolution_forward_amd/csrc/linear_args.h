@@ -21,7 +21,6 @@ struct LinEpilogue {
   int res_mode;   // LINEAR_RES_*
   int act;
   float alpha, beta;
-  int vec;        // every row of every operand starts on a 16-byte boundary
 };
 
 // out[c][r] = sum_k P(r, k) Q(c, k), see linear_plan.h.
@@ -54,6 +53,16 @@ struct JoinArgs {
   LinEpilogue e;
 };
 
+// Up to three matrices copied into rows of whole 16-byte pieces, zeros past the end.
+struct PackArgs {
+  const void* src[3];
+  void* dst[3];
+  long long ld[3], packed_ld[3], pieces[3];  // strides in elements; 16-byte pieces of all rows
+  int cols[3];
+  int first[4];  // first workgroup of each; the last entry is the grid
+  int n;
+};
+
 // dz and its column sums (see k_linear_grad.hip).
 struct DzArgs {
   const void* dy;
@@ -67,7 +76,6 @@ struct DzArgs {
   int dr_is_dy;
   int act;
   float alpha, beta;
-  int vec;
 };
 
 struct SumsArgs {
@@ -81,11 +89,14 @@ struct SumsArgs {
 template <typename E>
 hipError_t launch_product(const ProductArgs& a, int tile, int layout, bool gated, bool dma,
                           hipStream_t s);
+template <typename E>
+hipError_t launch_pack(const PackArgs& a, hipStream_t s);
 // tile: TILE_256 or TILE_256X128; both products' operands go to LDS directly.
 template <typename E>
 hipError_t launch_pair(const PairArgs& a, int tile, bool dx_transposed, hipStream_t s);
 template <typename E>
-hipError_t launch_stream(const ProductArgs& a, int blocks16, bool gated, bool vec, hipStream_t s);
+hipError_t launch_stream(const ProductArgs& a, int blocks16, int rows, bool gated, bool vec,
+                         hipStream_t s);
 template <typename E>
 hipError_t launch_join(const JoinArgs& a, bool gated, hipStream_t s);
 template <typename E>

@@ -10,25 +10,22 @@
 
 namespace convfwd {
 
+// Eight elements at p, whatever its alignment (the card reads and writes 16 bytes at
+// any element's address): two pieces of float32, one of 16 bits.  The last run of a
+// row, nv < 8 of them, goes element by element.
 template <typename E>
-struct Vec8 {
-  static constexpr int N = (int)sizeof(E) / 2;  // 16-byte pieces
-  typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+struct __attribute__((packed, aligned(sizeof(E)))) Eight {
   typedef E piece __attribute__((ext_vector_type(16 / sizeof(E))));
-  static constexpr int W = 16 / (int)sizeof(E);
+  piece q[sizeof(E) / 2];
 };
 
-// Eight elements at p: two 16-byte pieces of float32, one of 16 bits.
 template <typename E>
-__device__ __forceinline__ void load8(const E* p, int nv, bool vec, float (&v)[8]) {
-  using V = Vec8<E>;
-  if (vec && nv == 8) {
+__device__ __forceinline__ void load8(const E* p, int nv, float (&v)[8]) {
+  constexpr int W = 16 / (int)sizeof(E);
+  if (nv >= 8) {
+    const Eight<E> u = *reinterpret_cast<const Eight<E>*>(p);
 #pragma unroll
-    for (int i = 0; i < V::N; ++i) {
-      const typename V::piece q = *reinterpret_cast<const typename V::piece*>(p + i * V::W);
-#pragma unroll
-      for (int e = 0; e < V::W; ++e) v[i * V::W + e] = (float)q[e];
-    }
+    for (int e = 0; e < 8; ++e) v[e] = (float)u.q[e / W][e % W];
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = e < nv ? (float)p[e] : 0.0f;
@@ -36,16 +33,18 @@ __device__ __forceinline__ void load8(const E* p, int nv, bool vec, float (&v)[8
 }
 
 template <typename E>
-__device__ __forceinline__ void store8(E* p, int nv, bool vec, const float (&v)[8]) {
-  using V = Vec8<E>;
-  if (vec && nv == 8) {
+__device__ __forceinline__ void store8(E* p, int nv, const float (&v)[8]) {
+  constexpr int W = 16 / (int)sizeof(E);
+  if (nv >= 8) {
+    Eight<E> u;
 #pragma unroll
-    for (int i = 0; i < V::N; ++i) {
-      typename V::piece q;
+    for (int i = 0; i < (int)sizeof(E) / 2; ++i) {
+      typename Eight<E>::piece q;
 #pragma unroll
-      for (int e = 0; e < V::W; ++e) q[e] = (E)v[i * V::W + e];
-      *reinterpret_cast<typename V::piece*>(p + i * V::W) = q;
+      for (int e = 0; e < W; ++e) q[e] = (E)v[i * W + e];
+      u.q[i] = q;
     }
+    *reinterpret_cast<Eight<E>*>(p) = u;
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -259,8 +258,8 @@ __device__ __forceinline__ int run_offset(int lane) {
 }
 
 // Linear: v holds the sums of one row c, NR runs of 8 outputs at r + off(n).  whole
-// (uniform): every run is inside and every operand vectorised; in: c is a row.  The
-// runs' loads are in flight together and one branch picks the activation for all.
+// (uniform): every run is inside; in: c is a row.  The runs' loads are in flight
+// together and one branch picks the activation for all.
 template <typename E, int NR, typename Off>
 __device__ __forceinline__ void finish_linear_runs(const LinEpilogue& e, int z, long long c,
                                                    bool in, int r, Off off, bool whole,
@@ -270,8 +269,7 @@ __device__ __forceinline__ void finish_linear_runs(const LinEpilogue& e, int z, 
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       float t[8];
-      if (whole) load8(p + off(n), 8, true, t);
-      else load8(p + off(n), min(8, e.R - r - off(n)), e.vec, t);
+      load8(p + off(n), whole ? 8 : e.R - r - off(n), t);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[n * 8 + i] += t[i];
     }
@@ -283,8 +281,7 @@ __device__ __forceinline__ void finish_linear_runs(const LinEpilogue& e, int z, 
       float t[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) t[i] = v[n * 8 + i];
-      if (whole) store8(p + off(n), 8, true, t);
-      else store8(p + off(n), min(8, e.R - r - off(n)), e.vec, t);
+      store8(p + off(n), whole ? 8 : e.R - r - off(n), t);
     }
   };
   if (e.bias[0]) add(e.bias[0], 0);
@@ -307,8 +304,7 @@ __device__ __forceinline__ void finish_plain_runs(const LinEpilogue& e, int z, l
     float t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = v[n * 8 + i];
-    if (whole) store8(p + off(n), 8, true, t);
-    else store8(p + off(n), min(8, e.R - r - off(n)), e.vec, t);
+    store8(p + off(n), whole ? 8 : e.R - r - off(n), t);
   }
 }
 
@@ -327,8 +323,7 @@ __device__ __forceinline__ void finish_gated_runs(const LinEpilogue& e, long lon
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       float t[8];
-      if (whole) load8(p + r + off(n), 8, true, t);
-      else load8(p + r + off(n), min(8, e.R - r - off(n)), e.vec, t);
+      load8(p + r + off(n), whole ? 8 : e.R - r - off(n), t);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[n * 8 + i] += t[i];
     }
@@ -340,8 +335,7 @@ __device__ __forceinline__ void finish_gated_runs(const LinEpilogue& e, long lon
       float t[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) t[i] = v[n * 8 + i];
-      if (whole) store8(p + r + off(n), 8, true, t);
-      else store8(p + r + off(n), min(8, e.R - r - off(n)), e.vec, t);
+      store8(p + r + off(n), whole ? 8 : e.R - r - off(n), t);
     }
   };
   if (e.bias[0]) {

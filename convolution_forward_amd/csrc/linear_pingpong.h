@@ -255,7 +255,7 @@ struct PingPong {
     constexpr int NR = GATED ? NI / 2 : NI;
     auto off = [](int n) { return n % (NI / 2) * 32 + n / (NI / 2) * HR; };
     const int rl = r0 + wr * WR + run_offset(lane);
-    const bool whole = a.e.vec && nr >= (GATED ? HR : 2 * HR);
+    const bool whole = nr >= (GATED ? HR : 2 * HR);
 #pragma unroll 1
     for (int round = 0; round < 2 * NJ; ++round) {
       float v[NR * 8], u[GATED ? NR * 8 : 1];

@@ -76,7 +76,11 @@ const char* dtype_name(int dtype) {
   return dtype == CONV_F16 ? "f16" : dtype == CONV_BF16 ? "bf16" : "f32";
 }
 
-bool vec16(int64_t elems, int es) { return elems * es % 16 == 0; }
+// rows of cols elements (0: padded with zeros), ld apart from element off on, as
+// whole 16-byte pieces at multiples of 4 bytes
+bool whole_rows(int64_t cols, int64_t ld, int64_t off, int es) {
+  return cols * es % 16 == 0 && ld * es % 4 == 0 && off * es % 4 == 0;
+}
 
 }  // namespace
 
@@ -202,12 +206,6 @@ ProductPlan plan_product(const ProductShape& s, int es) {
   pl.splits = 1;
   const int64_t all = std::max<int64_t>(pl.ktiles * s.nseg, 1);  // no k: one step of zeros
   pl.per_split = all;
-  if (!s.pt && !s.qt && s.nseg == 1 && s.nz == 1 && s.C <= 32) {
-    pl.tile = TILE_STREAM;
-    pl.stream_t = s.C <= 16 ? 1 : 2;
-    pl.time = 0.0;
-    return pl;
-  }
   // the cheapest tile and split count by the model of the measured times
   const Tiling* table = es == 4 ? kTiles32 : s.aligned ? kTiles16 : kTiles16Gather;
   const int count = es == 2 && s.aligned ? 4 : 2;
@@ -231,6 +229,25 @@ ProductPlan plan_product(const ProductShape& s, int es) {
       }
     }
   }
+  if (!s.pt && !s.qt && s.nseg == 1 && s.nz == 1 && s.C <= 32 && s.K * es >= 16) {
+    // the streamed kernel: on every compute unit the bytes of its weight rows, of Q
+    // (from L2, 0.4 of a weight row's time) and a workgroup's start (4 rows' time), at
+    // 24 KB a us (float32, bound by its products: 18)
+    for (int rows = s.C > 16 ? 32 : 16; rows >= 4; rows /= 2) {
+      const int64_t groups = ceil_div(s.R, rows);
+      const double cost = (double)ceil_div(groups, kCus) *
+                          ((s.gated ? 2 : 1) * rows + 0.4 * (double)s.C + 4.0);
+      const double t = 3.0 + cost * (double)(s.K * es) / (es == 4 ? 18e3 : 24e3);
+      if (t < best) {
+        best = t;
+        pl.tile = TILE_STREAM;
+        pl.stream_t = s.C <= 16 ? 1 : 2;
+        pl.stream_rows = rows;
+        pl.splits = 1;
+        pl.per_split = all;
+      }
+    }
+  }
   pl.time = best;
   if (pl.splits > 1) {
     pl.plane_ld = plane_ld;
@@ -239,12 +256,11 @@ ProductPlan plan_product(const ProductShape& s, int es) {
   return pl;
 }
 
-int plan_pair(const ProductShape& dx, const ProductShape& dw, int es) {
-  if (es != 2 || !dx.aligned || !dw.aligned) return -1;
+PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es) {
+  PairPlan out{-1, plan_product(dx, es).time + plan_product(dw, es).time};
+  if (es != 2 || !dx.aligned || !dw.aligned) return out;
   const bool dw_first = dw.K * dw.nseg > dx.K * dx.nseg;
   const ProductShape &f = dw_first ? dw : dx, &l = dw_first ? dx : dw;
-  double best = plan_product(dx, es).time + plan_product(dw, es).time;
-  int tile = -1;
   for (int i = 0; i < 2; ++i) {
     const Tiling& t = kTiles16[i];
     const int64_t nf = tile_count(f, t), nl = tile_count(l, t);
@@ -262,12 +278,9 @@ int plan_pair(const ProductShape& dx, const ProductShape& dw, int es) {
                            rest * std::floor(std::max(0.0, mid - (full + 1) * lf) / ll);
       (taken >= (double)nl ? hi : lo) = mid;
     }
-    if (t.fixed + hi < best) {
-      best = t.fixed + hi;
-      tile = t.tile;
-    }
+    if (t.fixed + hi < out.time) out = {t.tile, t.fixed + hi};
   }
-  return tile;
+  return out;
 }
 
 ColsumPlan plan_colsum(int64_t m, int64_t n) {
@@ -281,78 +294,138 @@ ColsumPlan plan_colsum(int64_t m, int64_t n) {
   return c;
 }
 
-ProductShape linear_product(const linear_problem* p, const LinearGeo& g) {
-  ProductShape s{g.n, g.m, g.k, 1, 1, g.kn, false, false, false};
-  s.aligned = vec16(g.k, g.es) && vec16(g.ldx, g.es) && vec16(p->x_off, g.es) &&
-              vec16(g.ldw, g.es) && vec16(p->w_off, g.es) && (!g.kn || vec16(g.n, g.es));
-  return s;
+namespace {
+
+PackItem item_of(int64_t rows, int64_t cols, int64_t ld, int64_t off, int es) {
+  return {rows, cols, ld, !whole_rows(cols, ld, off, es), 0, 0};
 }
 
-ProductShape linear_dx_product(const linear_problem* p, const LinearGeo& g) {
-  // P = w with n contracted; Q = dz, whose rows the scratch pads with zeros
-  ProductShape s{g.k, g.m, g.n, 1, 1, !g.kn, false, false, false};
-  s.aligned = vec16(g.ldw, g.es) && vec16(p->w_off, g.es) && vec16(g.kn ? g.n : g.k, g.es);
-  if (p->activation == CONV_ACT_IDENTITY)
-    s.aligned = s.aligned && vec16(g.n, g.es) && vec16(g.ldy, g.es) && vec16(p->dy_off, g.es);
-  return s;
+// Lays the needed copies out from byte `at` on; returns their time, us.
+double lay_out(Packing* k, int64_t at, int es) {
+  double bytes = 0.0;
+  k->bytes = 0;
+  for (int i = 0; i < k->n; ++i) {
+    PackItem& q = k->item[i];
+    if (!q.need) continue;
+    q.packed_ld = round_up(q.cols, 16 / es);
+    q.off = at + k->bytes;
+    k->bytes += round_up(q.rows * q.packed_ld * es, 256);
+    bytes += 2.0 * (double)(q.rows * q.cols * es);
+  }
+  return 4.0 + bytes / 4e6;  // a launch, 4 TB/s
 }
 
-ProductShape linear_dw_product(const linear_problem* p, const LinearGeo& g) {
-  ProductShape s{g.kn ? g.n : g.k, g.kn ? g.k : g.n, g.m, 1, 1, true, true, false, false};
-  s.aligned = vec16(g.k, g.es) && vec16(g.ldx, g.es) && vec16(p->x_off, g.es);
-  if (p->activation == CONV_ACT_IDENTITY)
-    s.aligned = s.aligned && vec16(g.n, g.es) && vec16(g.ldy, g.es) && vec16(p->dy_off, g.es);
-  return s;
+bool any_needed(const Packing& k) {
+  for (int i = 0; i < k.n; ++i)
+    if (k.item[i].need) return true;
+  return false;
 }
 
-ProductShape gated_product(const gated_problem* p, const GatedGeo& g) {
-  ProductShape s{g.f, g.m, g.k, 1, 1, false, false, true, false};
-  s.aligned = vec16(g.k, g.es) && vec16(g.ldx, g.es) && vec16(p->x_off, g.es) &&
-              vec16(g.ldw, g.es) && vec16(p->wg_off, g.es) && vec16(p->wu_off, g.es);
-  return s;
+// One product: packs if that is estimated to pay; returns the planes' bytes.
+int64_t settle(ProductShape* s, Packing* k, int es, int64_t* total) {
+  ProductPlan pl = plan_product(*s, es);
+  if (!s->aligned && s->C > 0 && pl.tile != TILE_STREAM) {
+    ProductShape t = *s;
+    t.aligned = true;
+    const ProductPlan packed = plan_product(t, es);
+    if (packed.tile != TILE_STREAM && packed.time + lay_out(k, 0, es) < pl.time) {
+      k->on = true;
+      *s = t;
+      pl = packed;
+    }
+  }
+  const int64_t planes = round_up(pl.planes_bytes, 256);
+  if (k->on) lay_out(k, planes, es);
+  *total = planes + (k->on ? k->bytes : 0);
+  return planes;
 }
 
-ProductShape gated_dx_product(const gated_problem* p, const GatedGeo& g) {
-  ProductShape s{g.k, g.m, g.f, 2, 1, true, false, false, false};
-  s.aligned = vec16(g.k, g.es) && vec16(g.ldw, g.es) && vec16(p->wg_off, g.es) &&
-              vec16(p->wu_off, g.es);
-  return s;
+// Both products of a backward pass, the same way.
+void settle_backward(BackwardPlan* b, int es, int64_t at) {
+  if (b->dx.C > 0 && (!b->dx.aligned || !b->dw.aligned)) {
+    ProductShape x = b->dx, w = b->dw;
+    x.aligned = w.aligned = true;
+    if (plan_pair(x, w, es).time + lay_out(&b->pack, 0, es) < plan_pair(b->dx, b->dw, es).time) {
+      b->pack.on = true;
+      b->dx = x;
+      b->dw = w;
+    }
+  }
+  b->scratch.planes = at;
+  at += round_up(std::max(plan_product(b->dx, es).planes_bytes, plan_product(b->dw, es).planes_bytes), 256);
+  b->scratch.pack = at;
+  if (b->pack.on) {
+    lay_out(&b->pack, at, es);
+    at += b->pack.bytes;
+  }
+  b->scratch.total = at;
 }
 
-ProductShape gated_dw_product(const gated_problem* p, const GatedGeo& g) {
-  ProductShape s{g.k, g.f, g.m, 1, 2, true, true, false, false};
-  s.aligned = vec16(g.k, g.es) && vec16(g.ldx, g.es) && vec16(p->x_off, g.es);
-  return s;
+}  // namespace
+
+LinearPlan plan_linear(const linear_problem* p, const LinearGeo& g) {
+  LinearPlan o{};
+  o.pack.n = 2;
+  o.pack.item[0] = item_of(g.m, g.k, g.ldx, p->x_off, g.es);
+  o.pack.item[1] = item_of(g.kn ? g.k : g.n, g.kn ? g.n : g.k, g.ldw, p->w_off, g.es);
+  o.product = {g.n, g.m, g.k, 1, 1, g.kn, false, false, !any_needed(o.pack)};
+  o.planes = settle(&o.product, &o.pack, g.es, &o.total);
+  return o;
 }
 
-BackwardScratch linear_backward_scratch(const linear_problem* p, const LinearGeo& g) {
-  BackwardScratch b{};
+GatedPlan plan_gated(const gated_problem* p, const GatedGeo& g) {
+  GatedPlan o{};
+  o.pack.n = 3;
+  o.pack.item[0] = item_of(g.m, g.k, g.ldx, p->x_off, g.es);
+  o.pack.item[1] = item_of(g.f, g.k, g.ldw, p->wg_off, g.es);
+  o.pack.item[2] = item_of(g.f, g.k, g.ldw, p->wu_off, g.es);
+  // both weights have one stride
+  o.pack.item[1].need = o.pack.item[2].need = o.pack.item[1].need || o.pack.item[2].need;
+  o.product = {g.f, g.m, g.k, 1, 1, false, false, true, !any_needed(o.pack)};
+  o.planes = settle(&o.product, &o.pack, g.es, &o.total);
+  return o;
+}
+
+BackwardPlan plan_linear_backward(const linear_problem* p, const LinearGeo& g) {
+  BackwardPlan o{};
+  const bool act = p->activation != CONV_ACT_IDENTITY;
+  o.pack.n = act ? 2 : 3;  // dz is laid out in scratch already
+  o.pack.item[0] = item_of(g.m, g.k, g.ldx, p->x_off, g.es);
+  o.pack.item[1] = item_of(g.kn ? g.k : g.n, g.kn ? g.n : g.k, g.ldw, p->w_off, g.es);
+  if (!act) o.pack.item[2] = item_of(g.m, g.n, g.ldy, p->dy_off, g.es);
+  const bool d = !act && o.pack.item[2].need;
+  // dx: P = w with n contracted, Q = dz; dw: P and Q = x and dz, rows contracted
+  o.dx = {g.k, g.m, g.n, 1, 1, !g.kn, false, false, !o.pack.item[1].need && !d};
+  o.dw = {g.kn ? g.n : g.k, g.kn ? g.k : g.n, g.m, 1, 1, true, true, false, !o.pack.item[0].need && !d};
+  BackwardScratch& b = o.scratch;
   int64_t at = 0;
   b.dz = 0;
   b.dz_ld = round_up(g.n, 8);
-  if (p->activation != CONV_ACT_IDENTITY) at += round_up(g.m * b.dz_ld * g.es, 256);
+  if (act) at += round_up(g.m * b.dz_ld * g.es, 256);
   b.sums = at;
   at += round_up(plan_colsum(g.m, g.n).chunks * round_up(g.n, 8) * 4, 256);
-  b.planes = at;
-  at += round_up(std::max(plan_product(linear_dx_product(p, g), g.es).planes_bytes,
-                          plan_product(linear_dw_product(p, g), g.es).planes_bytes), 256);
-  b.total = at;
-  return b;
+  settle_backward(&o, g.es, at);
+  return o;
 }
 
-BackwardScratch gated_backward_scratch(const gated_problem* p, const GatedGeo& g) {
-  BackwardScratch b{};
+BackwardPlan plan_gated_backward(const gated_problem* p, const GatedGeo& g) {
+  BackwardPlan o{};
+  o.pack.n = 3;
+  o.pack.item[0] = item_of(g.m, g.k, g.ldx, p->x_off, g.es);
+  o.pack.item[1] = item_of(g.f, g.k, g.ldw, p->wg_off, g.es);
+  o.pack.item[2] = item_of(g.f, g.k, g.ldw, p->wu_off, g.es);
+  o.pack.item[1].need = o.pack.item[2].need = o.pack.item[1].need || o.pack.item[2].need;
+  o.dx = {g.k, g.m, g.f, 2, 1, true, false, false, !o.pack.item[1].need};
+  o.dw = {g.k, g.f, g.m, 1, 2, true, true, false, !o.pack.item[0].need};
+  BackwardScratch& b = o.scratch;
   int64_t at = 0;
   b.dz = 0;
   b.dz_ld = 2 * round_up(g.f, 8);
   at += round_up(g.m * b.dz_ld * g.es, 256);
   b.sums = at;
   at += round_up(plan_colsum(g.m, g.f).chunks * 2 * round_up(g.f, 8) * 4, 256);
-  b.planes = at;
-  at += round_up(std::max(plan_product(gated_dx_product(p, g), g.es).planes_bytes,
-                          plan_product(gated_dw_product(p, g), g.es).planes_bytes), 256);
-  b.total = at;
-  return b;
+  settle_backward(&o, g.es, at);
+  return o;
 }
 
 namespace {
@@ -373,16 +446,16 @@ void product_name(const ProductPlan& pl, char* buf, size_t len) {
 }
 
 void backward_name(const char* call, int dtype, const ProductShape& sx, const ProductShape& sw,
-                   int es, char* buf, size_t len) {
-  const int tile = plan_pair(sx, sw, es);
+                   const char* pack, int es, char* buf, size_t len) {
+  const int tile = plan_pair(sx, sw, es).tile;
   if (tile >= 0) {
-    snprintf(buf, len, "%s.%s.both.tile256x%d", call, dtype_name(dtype), tile == TILE_256 ? 256 : 128);
+    snprintf(buf, len, "%s.%s.both.tile256x%d%s", call, dtype_name(dtype), tile == TILE_256 ? 256 : 128, pack);
     return;
   }
   char dx[48], dw[48];
   product_name(plan_product(sx, es), dx, sizeof dx);
   product_name(plan_product(sw, es), dw, sizeof dw);
-  snprintf(buf, len, "%s.%s.dx.%s.dw.%s", call, dtype_name(dtype), dx, dw);
+  snprintf(buf, len, "%s.%s.dx.%s.dw.%s%s", call, dtype_name(dtype), dx, dw, pack);
 }
 
 int put(const char* text, char* buf, uint64_t len) {
@@ -433,7 +506,7 @@ int linear_scratch_size(const linear_problem* p, int dtype, uint64_t* bytes) {
   LinearGeo g;
   const int st = linear_validate(p, dtype, &g);
   if (st) return st;
-  *bytes = (uint64_t)round_up(plan_product(linear_product(p, g), g.es).planes_bytes, 256);
+  *bytes = (uint64_t)plan_linear(p, g).total;
   return CONV_OK;
 }
 
@@ -442,7 +515,7 @@ int linear_backward_scratch_size(const linear_problem* p, int dtype, uint64_t* b
   LinearGeo g;
   const int st = linear_validate(p, dtype, &g);
   if (st) return st;
-  *bytes = (uint64_t)linear_backward_scratch(p, g).total;
+  *bytes = (uint64_t)plan_linear_backward(p, g).scratch.total;
   return CONV_OK;
 }
 
@@ -451,7 +524,7 @@ int gated_scratch_size(const gated_problem* p, int dtype, uint64_t* bytes) {
   GatedGeo g;
   const int st = gated_validate(p, dtype, &g);
   if (st) return st;
-  *bytes = (uint64_t)round_up(plan_product(gated_product(p, g), g.es).planes_bytes, 256);
+  *bytes = (uint64_t)plan_gated(p, g).total;
   return CONV_OK;
 }
 
@@ -460,7 +533,7 @@ int gated_backward_scratch_size(const gated_problem* p, int dtype, uint64_t* byt
   GatedGeo g;
   const int st = gated_validate(p, dtype, &g);
   if (st) return st;
-  *bytes = (uint64_t)gated_backward_scratch(p, g).total;
+  *bytes = (uint64_t)plan_gated_backward(p, g).scratch.total;
   return CONV_OK;
 }
 
@@ -469,8 +542,9 @@ int linear_describe_variant(const linear_problem* p, int dtype, char* buf, uint6
   const int st = linear_validate(p, dtype, &g);
   if (st) return st;
   char name[48], text[96];
-  product_name(plan_product(linear_product(p, g), g.es), name, sizeof name);
-  snprintf(text, sizeof text, "linear.%s.%s", dtype_name(dtype), name);
+  const LinearPlan pl = plan_linear(p, g);
+  product_name(plan_product(pl.product, g.es), name, sizeof name);
+  snprintf(text, sizeof text, "linear.%s.%s%s", dtype_name(dtype), name, pl.pack.on ? ".pack" : "");
   return put(text, buf, len);
 }
 
@@ -479,7 +553,8 @@ int linear_backward_describe_variant(const linear_problem* p, int dtype, char* b
   const int st = linear_validate(p, dtype, &g);
   if (st) return st;
   char text[160];
-  backward_name("linear_backward", dtype, linear_dx_product(p, g), linear_dw_product(p, g), g.es,
+  const BackwardPlan pl = plan_linear_backward(p, g);
+  backward_name("linear_backward", dtype, pl.dx, pl.dw, pl.pack.on ? ".pack" : "", g.es,
                 text, sizeof text);
   return put(text, buf, len);
 }
@@ -489,8 +564,9 @@ int gated_describe_variant(const gated_problem* p, int dtype, char* buf, uint64_
   const int st = gated_validate(p, dtype, &g);
   if (st) return st;
   char name[48], text[96];
-  product_name(plan_product(gated_product(p, g), g.es), name, sizeof name);
-  snprintf(text, sizeof text, "gated.%s.%s", dtype_name(dtype), name);
+  const GatedPlan pl = plan_gated(p, g);
+  product_name(plan_product(pl.product, g.es), name, sizeof name);
+  snprintf(text, sizeof text, "gated.%s.%s%s", dtype_name(dtype), name, pl.pack.on ? ".pack" : "");
   return put(text, buf, len);
 }
 
@@ -499,7 +575,8 @@ int gated_backward_describe_variant(const gated_problem* p, int dtype, char* buf
   const int st = gated_validate(p, dtype, &g);
   if (st) return st;
   char text[160];
-  backward_name("gated_backward", dtype, gated_dx_product(p, g), gated_dw_product(p, g), g.es, text,
+  const BackwardPlan pl = plan_gated_backward(p, g);
+  backward_name("gated_backward", dtype, pl.dx, pl.dw, pl.pack.on ? ".pack" : "", g.es, text,
                 sizeof text);
   return put(text, buf, len);
 }
@@ -526,7 +603,7 @@ int linear_check(const linear_problem* p, int dtype, const void* x, const void* 
     if (!elem_aligned((const void*)ins[i].base, g.es)) return CONV_ERR_ARG;
   for (int i = 0; i < no; ++i)
     if (!elem_aligned((const void*)outs[i].base, g.es)) return CONV_ERR_ARG;
-  const int64_t need = plan_product(linear_product(p, g), g.es).planes_bytes;
+  const int64_t need = plan_linear(p, g).total;
   st = scratch_ok(scratch, scratch_bytes, need);
   if (st) return st;
   return overlaps(outs, no, ins, ni, 0, res_at, g.es, scratch, need);
@@ -564,7 +641,7 @@ int linear_backward_check(const linear_problem* p, int dtype, const void* x, con
     if (!elem_aligned((const void*)ins[i].base, g.es)) return CONV_ERR_ARG;
   for (int i = 0; i < no; ++i)
     if (!elem_aligned((const void*)outs[i].base, g.es)) return CONV_ERR_ARG;
-  const int64_t need = linear_backward_scratch(p, g).total;
+  const int64_t need = plan_linear_backward(p, g).scratch.total;
   st = scratch_ok(scratch, scratch_bytes, need);
   if (st) return st;
   // dr = dy in place is exact only where every later reader has its own copy of
@@ -599,7 +676,7 @@ int gated_check(const gated_problem* p, int dtype, const void* x, const void* wg
     if (!elem_aligned((const void*)ins[i].base, g.es)) return CONV_ERR_ARG;
   for (int i = 0; i < no; ++i)
     if (!elem_aligned((const void*)outs[i].base, g.es)) return CONV_ERR_ARG;
-  const int64_t need = plan_product(gated_product(p, g), g.es).planes_bytes;
+  const int64_t need = plan_gated(p, g).total;
   st = scratch_ok(scratch, scratch_bytes, need);
   if (st) return st;
   return overlaps(outs, no, ins, ni, -1, -1, g.es, scratch, need);
@@ -639,7 +716,7 @@ int gated_backward_check(const gated_problem* p, int dtype, const void* x, const
     if (!elem_aligned((const void*)ins[i].base, g.es)) return CONV_ERR_ARG;
   for (int i = 0; i < no; ++i)
     if (!elem_aligned((const void*)outs[i].base, g.es)) return CONV_ERR_ARG;
-  const int64_t need = gated_backward_scratch(p, g).total;
+  const int64_t need = plan_gated_backward(p, g).scratch.total;
   st = scratch_ok(scratch, scratch_bytes, need);
   if (st) return st;
   return overlaps(outs, no, ins, ni, -1, -1, g.es, scratch, need);

@@ -18,7 +18,7 @@ struct ProductShape {
   int nz;           // products of one shape in a launch (gated weight gradients: 2)
   bool pt, qt;      // operand transposed
   bool gated;       // P is two matrices of R rows (gate and up), joined in the epilogue
-  bool aligned;     // rows of whole 16-byte vectors (strides, extents, offsets)
+  bool aligned;     // rows of whole 16-byte pieces at multiples of 4 bytes (strides, extents, offsets)
 };
 
 enum ProductTile { TILE_256 = 0, TILE_128 = 1, TILE_64 = 2, TILE_STREAM = 3, TILE_256X128 = 4 };
@@ -29,6 +29,7 @@ struct ProductPlan {
   int64_t ktiles;   // 128-byte contraction steps of one segment
   int64_t per_split;
   int stream_t;     // stream: 16-row blocks of Q
+  int stream_rows;  // stream: weight rows of a workgroup
   int64_t plane_ld; // floats per plane row
   int64_t planes_bytes;
   double time;      // estimated, us
@@ -53,12 +54,29 @@ struct ColsumPlan {
   int64_t chunks;  // <= 256
 };
 
+// Operands whose rows do not start on multiples of 4 bytes or are no whole 16-byte
+// pieces can be copied to scratch first, rows padded with zeros, which lets the
+// products load them to LDS directly.  Planned where the model finds it cheaper than
+// products that gather through registers.
+struct PackItem {
+  int64_t rows, cols, ld;
+  bool need;
+  int64_t off, packed_ld;  // in the call's scratch (bytes), elements
+};
+struct Packing {
+  bool on;
+  int n;
+  PackItem item[3];
+  int64_t bytes;
+};
+
 // Scratch layout of a backward call (byte offsets; every part 256-byte aligned).
 struct BackwardScratch {
   int64_t dz;      // dz [m, dz_ld] (gated: dg and du side by side)
   int64_t dz_ld;   // elements
   int64_t sums;    // column-sum partials
   int64_t planes;  // split planes (the two products run one after the other)
+  int64_t pack;    // packed operands
   int64_t total;
 };
 
@@ -68,21 +86,35 @@ int linear_validate(const linear_problem* p, int dtype, LinearGeo* g);
 int gated_validate(const gated_problem* p, int dtype, GatedGeo* g);
 
 ProductPlan plan_product(const ProductShape& s, int es);
-// The tile (TILE_256 or TILE_256X128) of one launch for both products of a backward
-// pass, or -1 where they run one after the other.
-int plan_pair(const ProductShape& dx, const ProductShape& dw, int es);
+// Both products of a backward pass: in one launch of a tile (TILE_256 or
+// TILE_256X128), or one after the other (tile -1).
+struct PairPlan {
+  int tile;
+  double time;  // estimated, us
+};
+PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es);
 ColsumPlan plan_colsum(int64_t m, int64_t n);
 
-// The products of each call, from the geometry and offsets alone.
-ProductShape linear_product(const linear_problem* p, const LinearGeo& g);
-ProductShape linear_dx_product(const linear_problem* p, const LinearGeo& g);
-ProductShape linear_dw_product(const linear_problem* p, const LinearGeo& g);
-ProductShape gated_product(const gated_problem* p, const GatedGeo& g);
-ProductShape gated_dx_product(const gated_problem* p, const GatedGeo& g);
-ProductShape gated_dw_product(const gated_problem* p, const GatedGeo& g);
-
-BackwardScratch linear_backward_scratch(const linear_problem* p, const LinearGeo& g);
-BackwardScratch gated_backward_scratch(const gated_problem* p, const GatedGeo& g);
+// A call's plan: its products as they will run, and its scratch.
+struct LinearPlan {
+  ProductShape product;
+  Packing pack;  // x, w
+  int64_t planes, total;
+};
+struct GatedPlan {
+  ProductShape product;
+  Packing pack;  // x, wg, wu
+  int64_t planes, total;
+};
+struct BackwardPlan {
+  ProductShape dx, dw;
+  Packing pack;  // linear: x, w, dy (identity); gated: x, wg, wu
+  BackwardScratch scratch;
+};
+LinearPlan plan_linear(const linear_problem* p, const LinearGeo& g);
+GatedPlan plan_gated(const gated_problem* p, const GatedGeo& g);
+BackwardPlan plan_linear_backward(const linear_problem* p, const LinearGeo& g);
+BackwardPlan plan_gated_backward(const gated_problem* p, const GatedGeo& g);
 
 inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 

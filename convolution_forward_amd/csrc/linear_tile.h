@@ -145,26 +145,66 @@ __device__ __forceinline__ mfma_f32x4 multiply(const F& p, const F& q, mfma_f32x
   }
 }
 
-// One 16-byte piece gathered element by element where it crosses an end.
-template <typename E, bool T>
-__device__ __forceinline__ i32x4 gather(const E* base, long long ld, int row, int piece,
-                                        long long nrow, long long nk) {
-  constexpr int EPC = 16 / (int)sizeof(E);
-  struct __attribute__((packed, aligned(sizeof(E)))) U { i32x4 v; };
-  const long long at = (long long)piece * EPC;
-  const long long have = (T ? nrow : nk) - at;  // valid elements of the row from here
-  const bool ok = T ? row < nk : row < nrow;
-  const E* p = base + (long long)row * ld + at;
-  if (ok && have >= EPC) return reinterpret_cast<const U*>(p)->v;
-  union { E e[EPC]; i32x4 v; } u;
-  u.v = i32x4{0, 0, 0, 0};
-  if (ok) {
+// 16 bytes at base + off, aligned to their elements.  The card reads 16 bytes at a
+// multiple of 4 at full speed, at an odd multiple of 2 at less than half: those come
+// as the five words around them (a word that holds an element is on its page).
+template <typename E>
+__device__ __forceinline__ i32x4 load_piece(const char* base, int off) {
+  typedef i32x4 A4 __attribute__((aligned(4)));
+  if constexpr (sizeof(E) == 4) {
+    return *reinterpret_cast<const A4*>(base + off);
+  } else {
+    const int odd = ((int)reinterpret_cast<unsigned long long>(base) + off) & 2;
+    const i32x4 v = *reinterpret_cast<const A4*>(base + (off - odd));
+    const int w = *reinterpret_cast<const int*>(base + (off + odd + 12));
+    i32x4 o;
 #pragma unroll
-    for (int i = 0; i < EPC; ++i)
-      if (i < have) u.e[i] = p[i];
+    for (int i = 0; i < 4; ++i)
+      o[i] = (int)__builtin_amdgcn_alignbyte((unsigned)(i < 3 ? v[i < 3 ? i + 1 : 3] : w), (unsigned)v[i], odd);
+    return o;
   }
-  return u.v;
 }
+
+// Pieces of operands whose rows start anywhere (odd strides, sizes or bases), loaded
+// into registers.  raw: the 16 bytes at the piece, moved back where it would pass the
+// end of its row and to the last row where there is no such row, so that every load
+// is inside the operand and none waits for a branch.  fix: those bytes as the piece:
+// elements past an end are zeros.  (A row past the last r or c is whatever raw gave:
+// its outputs are not stored.)  Rows shorter than a piece go element by element.
+template <typename E, bool T>
+struct Ragged {
+  static constexpr int EPC = 16 / (int)sizeof(E);
+  struct __attribute__((packed, aligned(sizeof(E)))) P { i32x4 v; };
+
+  static __device__ __forceinline__ i32x4 raw(const E* base, long long ld, int row, int piece,
+                                              long long nrow, long long nk, bool tiny) {
+    const int len = (int)min(T ? nrow : nk, 1LL << 20), rows = (int)min(T ? nk : nrow, 256LL);
+    const int at = piece * EPC;
+    const E* p = base + (long long)min(row, rows - 1) * ld;
+    if (!tiny) return reinterpret_cast<const P*>(p + min(at, len - EPC))->v;
+    union { E e[EPC]; i32x4 v; } u;
+#pragma unroll
+    for (int i = 0; i < EPC; ++i) u.e[i] = at + i < len ? p[at + i] : (E)0.0f;
+    return u.v;
+  }
+  // The elements of a piece that lies partly past len, loaded so that it ends there.
+  template <typename V>
+  static __device__ __forceinline__ V shift(V v, int piece, int len) {
+    const int past = min(max(piece * EPC + EPC - len, 0), EPC), s = past * (int)sizeof(E) * 8;
+    typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+    const u64x2 u = __builtin_bit_cast(u64x2, v);
+    const unsigned long long a = u[0], b = u[1];
+    u64x2 o;
+    o[0] = s == 0 ? a : s < 64 ? (a >> s) | (b << (64 - s)) : s < 128 ? b >> (s - 64) : 0;
+    o[1] = s < 64 ? b >> s : 0;
+    return __builtin_bit_cast(V, o);
+  }
+  static __device__ __forceinline__ i32x4 fix(i32x4 v, int row, int piece, long long nrow,
+                                              long long nk, bool tiny) {
+    if (!tiny) v = shift(v, piece, (int)min(T ? nrow : nk, 1LL << 20));
+    return T && row >= nk ? i32x4{0, 0, 0, 0} : v;
+  }
+};
 
 }  // namespace lin
 
@@ -303,6 +343,9 @@ __global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const Produ
     }
   } else {
     i32x4 pv[TP::ITEMS], qv[TQ::ITEMS];
+    using RP = Ragged<E, PT>;
+    using RQ = Ragged<E, QT>;
+    const bool ptiny = (PT ? a.R : a.K) < TP::EPC, qtiny = (QT ? a.C : a.K) < TQ::EPC;
     auto fetch = [&](int t) {
       const char *p0, *p1, *q;
       int kk;
@@ -316,16 +359,33 @@ __global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const Produ
           if (row % WR >= HW) base = p1;
           row = (row / WR) * HW + row % HW;
         }
-        pv[i] = gather<E, PT>(reinterpret_cast<const E*>(base), a.ldp, row, piece, nr, kk);
+        pv[i] = RP::raw(reinterpret_cast<const E*>(base), a.ldp, row, piece, nr, kk, ptiny);
       }
 #pragma unroll
       for (int i = 0; i < TQ::ITEMS; ++i) {
         int row, piece;
         TQ::item(i, tid, &row, &piece);
-        qv[i] = gather<E, QT>(reinterpret_cast<const E*>(q), a.ldq, row, piece, nc, kk);
+        qv[i] = RQ::raw(reinterpret_cast<const E*>(q), a.ldq, row, piece, nc, kk, qtiny);
       }
     };
-    auto put = [&](int b) {
+    auto put = [&](int t, int b) {
+      const int kk = a.K - (t - (t >= a.ktiles ? a.ktiles : 0)) * TP::BKE;
+      if (kk < TP::BKE || (PT && nr < BR)) {
+#pragma unroll
+        for (int i = 0; i < TP::ITEMS; ++i) {
+          int row, piece;
+          TP::item(i, tid, &row, &piece);
+          pv[i] = RP::fix(pv[i], row, piece, nr, kk, ptiny);
+        }
+      }
+      if (kk < TP::BKE || (QT && nc < BC)) {
+#pragma unroll
+        for (int i = 0; i < TQ::ITEMS; ++i) {
+          int row, piece;
+          TQ::item(i, tid, &row, &piece);
+          qv[i] = RQ::fix(qv[i], row, piece, nc, kk, qtiny);
+        }
+      }
       char* d = smem + b * STAGE;
 #pragma unroll
       for (int i = 0; i < TP::ITEMS; ++i) *reinterpret_cast<i32x4*>(d + (i * NT + tid) * 16) = pv[i];
@@ -336,14 +396,14 @@ __global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const Produ
     int b = 0;
     if (t0 < t1) {
       fetch(t0);
-      put(0);
+      put(t0, 0);
     }
     for (int t = t0; t < t1; ++t) {
       if (t + 1 < t1) fetch(t + 1);
       lds_wait();
       barrier();  // step t is staged; buffer b ^ 1 was last read before this
       compute(smem + b * STAGE);
-      if (t + 1 < t1) put(b ^ 1);
+      if (t + 1 < t1) put(t + 1, b ^ 1);
       b ^= 1;
     }
   }
@@ -353,7 +413,7 @@ __global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const Produ
   constexpr int NR = RUN / 32;
   auto off = [](int n) { return n * 32; };
   const int rl = r0 + wr * RUN + run_offset(lane);
-  const bool whole = a.e.vec && nr >= WVR * RUN;
+  const bool whole = nr >= WVR * RUN;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     float v[NR * 8], u[GATED ? NR * 8 : 1];
