@@ -439,8 +439,10 @@ def _describe(name, p, dtype):
 
 
 def _run(name, p, dtype, operands, scratch, scratch_bytes, stream, check):
-    st = getattr(lib(), name)(ctypes.byref(p), _dt(dtype), *map(_ptr, operands), _ptr(scratch),
-                              int(scratch_bytes), stream or None)
+    st = getattr(_lib or lib(), name)(
+        ctypes.byref(p), DTYPES[dtype] if isinstance(dtype, str) else int(dtype),
+        *[t if t is None or isinstance(t, int) else t.data_ptr() for t in operands], _ptr(scratch),
+        int(scratch_bytes), stream or None)
     if check and st:
         raise ConvError(st, name)
     return st

@@ -10,6 +10,7 @@
 namespace convfwd {
 
 constexpr int kClipTable = 112;      // tensors per launch (their table is a kernel argument)
+constexpr int kClipSmall = 16;       // or of a launch with a small table, if they are that few
 constexpr int kClipPartials = 1024;  // partial norms per launch
 
 struct ClipPlan {

@@ -29,6 +29,9 @@ struct ClipEntry {
   int first;  // its first chunk in this launch
 };
 
+// N: tensors in the table.  The table travels with the launch (32 bytes a tensor);
+// the few tensors of a small model do not pay for a large one.
+template <int N>
 struct ClipArgs {
   double* partials;
   float* norm;        // written by workgroup 0 where not null
@@ -38,7 +41,7 @@ struct ClipArgs {
   int shift;          // log2 of the chunk
   int kind;
   float max_norm, eps;
-  ClipEntry t[kClipTable];
+  ClipEntry t[N];
 };
 
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
@@ -82,7 +85,8 @@ __device__ __forceinline__ double reduce256(double s, int kind, double* lds) {
   return combine(combine(lds[0], lds[1], kind), combine(lds[2], lds[3], kind), kind);
 }
 
-__device__ __forceinline__ int entry_of(const ClipArgs& a, int chunk) {
+template <int N>
+__device__ __forceinline__ int entry_of(const ClipArgs<N>& a, int chunk) {
   int lo = 0, hi = a.n - 1;  // the last entry whose first chunk is <= chunk
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -119,8 +123,8 @@ __device__ __forceinline__ void chunk_power(const E* g, int n, double (&s)[4]) {
   for (int i = done + threadIdx.x; i < n; i += 256) add_power(s[0], (float)g[i], KIND);
 }
 
-template <int KIND>
-__global__ __launch_bounds__(256) void clip_norm_kernel(const ClipArgs a) {
+template <int KIND, int N>
+__global__ __launch_bounds__(256) void clip_norm_kernel(const ClipArgs<N> a) {
   __shared__ double lds[4];
   double s[4] = {0, 0, 0, 0};
   for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
@@ -177,7 +181,8 @@ __device__ __forceinline__ void chunk_scale(const E* g, E* out, int n, float c) 
   for (int i = done + threadIdx.x; i < n; i += 256) out[i] = (E)((float)g[i] * c);
 }
 
-__global__ __launch_bounds__(256) void clip_scale_kernel(const ClipArgs a) {
+template <int N>
+__global__ __launch_bounds__(256) void clip_scale_kernel(const ClipArgs<N> a) {
   __shared__ double lds[4];
   double s = 0;
   for (long long i = threadIdx.x; i < a.count; i += 256) s = combine(s, a.partials[i], a.kind);
@@ -186,7 +191,9 @@ __global__ __launch_bounds__(256) void clip_scale_kernel(const ClipArgs a) {
   const double q = (double)a.max_norm / (norm + (double)a.eps);
   const float c = q >= 1.0 ? 1.0f : (float)q;  // NaN stays NaN
   if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
-  for (int k = blockIdx.x; k < a.chunks; k += gridDim.x) {
+  // from the last chunk back: what the norm read last is what the last-level cache
+  // still holds
+  for (int k = a.chunks - 1 - (int)blockIdx.x; k >= 0; k -= gridDim.x) {
     const ClipEntry& t = a.t[entry_of(a, k)];
     if (c == 1.0f && t.out == t.g) continue;
     const long long at = (long long)(k - t.first) << a.shift;
@@ -200,11 +207,12 @@ __global__ __launch_bounds__(256) void clip_scale_kernel(const ClipArgs a) {
   }
 }
 
-// The launch's table: tensors [i0, i0 + kClipTable) that hold elements.
-void fill(const grad_clip_problem* p, const ClipPlan& pl, int64_t i0, ClipArgs* a) {
+// The launch's table: tensors [i0, i0 + N) that hold elements.
+template <int N>
+void fill(const grad_clip_problem* p, const ClipPlan& pl, int64_t i0, ClipArgs<N>* a) {
   a->n = 0;
   int64_t chunks = 0;
-  for (int64_t i = i0; i < std::min<int64_t>(p->count, i0 + kClipTable); ++i) {
+  for (int64_t i = i0; i < std::min<int64_t>(p->count, i0 + N); ++i) {
     const grad_tensor& t = p->tensors[i];
     if (t.elems == 0) continue;
     a->t[a->n++] = {t.g, t.out, (long long)t.elems, t.dtype, (int)chunks};
@@ -213,37 +221,27 @@ void fill(const grad_clip_problem* p, const ClipPlan& pl, int64_t i0, ClipArgs* 
   a->chunks = (int)chunks;
 }
 
-}  // namespace
-
-}  // namespace convfwd
-
-using namespace convfwd;
-
-extern "C" int grad_clip(const grad_clip_problem* p, float* norm, void* scratch,
-                         uint64_t scratch_bytes, void* stream) {
-  const int st = grad_clip_check(p, norm, scratch, scratch_bytes);
-  if (st) return st;
-  ClipPlan pl;
-  clip_validate(p, &pl);
+template <int N>
+int clip(const grad_clip_problem* p, const ClipPlan& pl, float* norm, void* scratch, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   double* partials = static_cast<double*>(scratch);
-  ClipArgs a{};
+  ClipArgs<N> a{};
   a.kind = p->kind;
   a.max_norm = p->max_norm;
   a.eps = p->eps;
   a.shift = 63 - __builtin_clzll((unsigned long long)pl.chunk);
   int64_t count = 0;
   for (int64_t l = 0; l < pl.launches; ++l) {
-    fill(p, pl, l * kClipTable, &a);
+    fill(p, pl, l * N, &a);
     if (a.chunks == 0) continue;
     const int grid = std::min(a.chunks, kClipPartials);
     a.partials = partials + count;
     if (a.kind == GRAD_NORM_2)
-      hipLaunchKernelGGL((clip_norm_kernel<GRAD_NORM_2>), dim3(grid), dim3(256), 0, s, a);
+      hipLaunchKernelGGL((clip_norm_kernel<GRAD_NORM_2, N>), dim3(grid), dim3(256), 0, s, a);
     else if (a.kind == GRAD_NORM_1)
-      hipLaunchKernelGGL((clip_norm_kernel<GRAD_NORM_1>), dim3(grid), dim3(256), 0, s, a);
+      hipLaunchKernelGGL((clip_norm_kernel<GRAD_NORM_1, N>), dim3(grid), dim3(256), 0, s, a);
     else
-      hipLaunchKernelGGL((clip_norm_kernel<GRAD_NORM_INF>), dim3(grid), dim3(256), 0, s, a);
+      hipLaunchKernelGGL((clip_norm_kernel<GRAD_NORM_INF, N>), dim3(grid), dim3(256), 0, s, a);
     if (hipGetLastError() != hipSuccess) return CONV_ERR_DEVICE;
     count += grid;
   }
@@ -260,13 +258,29 @@ extern "C" int grad_clip(const grad_clip_problem* p, float* norm, void* scratch,
   bool out = false;
   for (int64_t i = 0; i < p->count && !out; ++i) out = p->tensors[i].elems > 0 && p->tensors[i].out;
   for (int64_t l = 0; l < (out ? pl.launches : 1); ++l) {
-    if (pl.launches > 1 || l > 0) fill(p, pl, l * kClipTable, &a);
+    if (pl.launches > 1 || l > 0) fill(p, pl, l * N, &a);
     if (!out) a.chunks = 0;
     if (a.chunks == 0 && !a.norm) continue;
     const int grid = std::max(1, std::min(a.chunks, 2048));
-    hipLaunchKernelGGL(clip_scale_kernel, dim3(grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((clip_scale_kernel<N>), dim3(grid), dim3(256), 0, s, a);
     if (hipGetLastError() != hipSuccess) return CONV_ERR_DEVICE;
     a.norm = nullptr;
   }
   return CONV_OK;
+}
+
+}  // namespace
+
+}  // namespace convfwd
+
+using namespace convfwd;
+
+extern "C" int grad_clip(const grad_clip_problem* p, float* norm, void* scratch,
+                         uint64_t scratch_bytes, void* stream) {
+  const int st = grad_clip_check(p, norm, scratch, scratch_bytes);
+  if (st) return st;
+  ClipPlan pl;
+  clip_validate(p, &pl);
+  return p->count <= kClipSmall ? clip<kClipSmall>(p, pl, norm, scratch, stream)
+                                : clip<kClipTable>(p, pl, norm, scratch, stream);
 }

@@ -68,10 +68,9 @@ bool direct(const ProductShape& s, const ProductArgs& a, int es, bool p_padded, 
 }
 
 // Runs one planned product; a's operands and epilogue are set.
-hipError_t run_product(const ProductShape& s, int dtype, ProductArgs& a, bool p_padded,
-                       bool q_padded, void* planes, hipStream_t st) {
+hipError_t run_product(const ProductShape& s, const ProductPlan& pl, int dtype, ProductArgs& a,
+                       bool p_padded, bool q_padded, void* planes, hipStream_t st) {
   const int es = (int)dtype_size(dtype);
-  const ProductPlan pl = plan_product(s, es);
   a.R = (int)s.R; a.C = (int)s.C; a.K = (int)s.K;
   a.nseg = s.nseg; a.nz = s.nz;
   a.ktiles = (int)pl.ktiles; a.splits = pl.splits; a.per_split = (int)pl.per_split;
@@ -79,7 +78,8 @@ hipError_t run_product(const ProductShape& s, int dtype, ProductArgs& a, bool p_
   a.plane_ld = pl.plane_ld;
   a.e.R = a.R;
   const bool dma = direct(s, a, es, p_padded, q_padded);
-  if (pl.tile == TILE_STREAM) return stream_product(dtype, a, pl.stream_t, pl.stream_rows, s.gated, dma, st);
+  if (pl.tile == TILE_STREAM)
+    return stream_product(dtype, a, pl.stream_t, pl.stream_rows, s.gated, dma, st);
   const int layout = s.pt ? (s.qt ? 2 : 1) : 0;
   hipError_t e = product(dtype, a, pl.tile, layout, s.gated, dma, st);
   if (e != hipSuccess || pl.splits == 1) return e;
@@ -101,11 +101,12 @@ hipError_t pair(int dtype, const PairArgs& a, int tile, bool dx_transposed, hipS
 
 // Both products of a backward pass: in one launch where the plan pairs them and the
 // operands allow it, one after the other otherwise.
-hipError_t run_both(const ProductShape& sx, const ProductShape& sw, int dtype, ProductArgs& dx,
-                    ProductArgs& dw, bool dx_p_padded, bool dx_q_padded, bool dw_p_padded,
+hipError_t run_both(const BackwardPlan& pl, int dtype, ProductArgs& dx, ProductArgs& dw,
+                    bool dx_p_padded, bool dx_q_padded, bool dw_p_padded,
                     bool dw_q_padded, void* planes, hipStream_t st) {
   const int es = (int)dtype_size(dtype);
-  const int tile = plan_pair(sx, sw, es).tile;
+  const ProductShape &sx = pl.dx, &sw = pl.dw;
+  const int tile = pl.both.tile;
   if (tile >= 0 && direct(sx, dx, es, dx_p_padded, dx_q_padded) &&
       direct(sw, dw, es, dw_p_padded, dw_q_padded)) {
     PairArgs a{};
@@ -123,8 +124,9 @@ hipError_t run_both(const ProductShape& sx, const ProductShape& sw, int dtype, P
     a.dw = dw;
     return pair(dtype, a, tile, sx.pt, st);
   }
-  const hipError_t e = run_product(sx, dtype, dx, dx_p_padded, dx_q_padded, planes, st);
-  return e != hipSuccess ? e : run_product(sw, dtype, dw, dw_p_padded, dw_q_padded, planes, st);
+  const hipError_t e = run_product(sx, pl.both.dx, dtype, dx, dx_p_padded, dx_q_padded, planes, st);
+  if (e != hipSuccess) return e;
+  return run_product(sw, pl.both.dw, dtype, dw, dw_p_padded, dw_q_padded, planes, st);
 }
 
 // Copies the operands that the plan packs and points to the copies.  src[i] and ld[i]:
@@ -162,12 +164,11 @@ extern "C" {
 int linear_forward(const linear_problem* p, int dtype, const void* x, const void* w, const void* b,
                    const void* r, void* y, void* z, void* scratch, uint64_t scratch_bytes,
                    void* stream) {
-  const int st = linear_check(p, dtype, x, w, b, r, y, z, scratch, scratch_bytes);
-  if (st) return st;
   LinearGeo g;
-  linear_validate(p, dtype, &g);
+  LinearPlan pl;
+  const int st = linear_checked(p, dtype, x, w, b, r, y, z, scratch, scratch_bytes, &g, &pl);
+  if (st) return st;
   if (g.m == 0) return CONV_OK;
-  const LinearPlan pl = plan_linear(p, g);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const void* src[3] = {at(x, p->x_off, g.es), at(w, p->w_off, g.es)};
   int64_t ld[3] = {g.ldx, g.ldw};
@@ -185,18 +186,18 @@ int linear_forward(const linear_problem* p, int dtype, const void* x, const void
   e.save[0] = p->save_z ? at(z, p->z_off, g.es) : nullptr;
   e.ldo = g.ldy; e.ldres = g.ldr; e.ldsave = g.ldz;
   e.act = p->activation; e.alpha = p->act_alpha; e.beta = p->act_beta;
-  return status(run_product(pl.product, dtype, a, pl.pack.on, pl.pack.on, scratch, s));
+  return status(run_product(pl.product, pl.run, dtype, a, pl.pack.on, pl.pack.on, scratch, s));
 }
 
 int gated_forward(const gated_problem* p, int dtype, const void* x, const void* wg, const void* wu,
                   const void* bg, const void* bu, void* h, void* pg, void* pu, void* scratch,
                   uint64_t scratch_bytes, void* stream) {
-  const int st = gated_check(p, dtype, x, wg, wu, bg, bu, h, pg, pu, scratch, scratch_bytes);
-  if (st) return st;
   GatedGeo g;
-  gated_validate(p, dtype, &g);
+  GatedPlan pl;
+  const int st = gated_checked(p, dtype, x, wg, wu, bg, bu, h, pg, pu,
+                               scratch, scratch_bytes, &g, &pl);
+  if (st) return st;
   if (g.m == 0) return CONV_OK;
-  const GatedPlan pl = plan_gated(p, g);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const void* src[3] = {at(x, p->x_off, g.es), at(wg, p->wg_off, g.es), at(wu, p->wu_off, g.es)};
   int64_t ld[3] = {g.ldx, g.ldw, g.ldw};
@@ -219,17 +220,17 @@ int gated_forward(const gated_problem* p, int dtype, const void* x, const void* 
   }
   e.ldo = g.ldh; e.ldsave = g.ldp;
   e.act = p->activation; e.alpha = p->act_alpha; e.beta = p->act_beta;
-  return status(run_product(pl.product, dtype, a, pl.pack.on, pl.pack.on, scratch, s));
+  return status(run_product(pl.product, pl.run, dtype, a, pl.pack.on, pl.pack.on, scratch, s));
 }
 
 int linear_backward(const linear_problem* p, int dtype, const void* x, const void* w, const void* z,
                     const void* dy, void* dx, void* dw, void* db, void* dr, void* scratch,
                     uint64_t scratch_bytes, void* stream) {
-  const int st = linear_backward_check(p, dtype, x, w, z, dy, dx, dw, db, dr, scratch, scratch_bytes);
-  if (st) return st;
   LinearGeo g;
-  linear_validate(p, dtype, &g);
-  const BackwardPlan pl = plan_linear_backward(p, g);
+  BackwardPlan pl;
+  const int st = linear_backward_checked(p, dtype, x, w, z, dy, dx, dw, db, dr,
+                                         scratch, scratch_bytes, &g, &pl);
+  if (st) return st;
   const BackwardScratch& sc = pl.scratch;
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* sb = static_cast<char*>(scratch);
@@ -264,7 +265,8 @@ int linear_backward(const linear_problem* p, int dtype, const void* x, const voi
     }
   }
   const bool want_dx = dx && g.m > 0;
-  const void* src[3] = {dw ? at(x, p->x_off, g.es) : nullptr, want_dx ? at(w, p->w_off, g.es) : nullptr,
+  const void* src[3] = {dw ? at(x, p->x_off, g.es) : nullptr,
+                        want_dx ? at(w, p->w_off, g.es) : nullptr,
                         act ? static_cast<const void*>(sb + sc.dz) : dx || dw ? dy : nullptr};
   int64_t ld[3] = {g.ldx, g.ldw, act ? sc.dz_ld : g.ldy};
   if (e == hipSuccess) e = run_pack(pl.pack, dtype, src, ld, scratch, s);
@@ -288,23 +290,22 @@ int linear_backward(const linear_problem* p, int dtype, const void* x, const voi
   // rows padded with zeros: packed ones, and dz
   const bool dpad = on || act, wp = g.kn ? dpad : on, wq = g.kn ? on : dpad;
   if (e == hipSuccess && want_dx && dw)
-    e = run_both(pl.dx, pl.dw, dtype, ax, aw, on, dpad, wp, wq, sb + sc.planes, s);
+    e = run_both(pl, dtype, ax, aw, on, dpad, wp, wq, sb + sc.planes, s);
   else if (e == hipSuccess && want_dx)
-    e = run_product(pl.dx, dtype, ax, on, dpad, sb + sc.planes, s);
+    e = run_product(pl.dx, pl.both.dx, dtype, ax, on, dpad, sb + sc.planes, s);
   else if (e == hipSuccess && dw)
-    e = run_product(pl.dw, dtype, aw, wp, wq, sb + sc.planes, s);
+    e = run_product(pl.dw, pl.both.dw, dtype, aw, wp, wq, sb + sc.planes, s);
   return status(e);
 }
 
 int gated_backward(const gated_problem* p, int dtype, const void* x, const void* wg, const void* wu,
                    const void* pg, const void* pu, const void* dh, void* dx, void* dwg, void* dwu,
                    void* dbg, void* dbu, void* scratch, uint64_t scratch_bytes, void* stream) {
-  const int st = gated_backward_check(p, dtype, x, wg, wu, pg, pu, dh, dx, dwg, dwu, dbg, dbu,
-                                      scratch, scratch_bytes);
-  if (st) return st;
   GatedGeo g;
-  gated_validate(p, dtype, &g);
-  const BackwardPlan pl = plan_gated_backward(p, g);
+  BackwardPlan pl;
+  const int st = gated_backward_checked(p, dtype, x, wg, wu, pg, pu, dh, dx, dwg, dwu, dbg, dbu,
+                                        scratch, scratch_bytes, &g, &pl);
+  if (st) return st;
   const BackwardScratch& sc = pl.scratch;
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* sb = static_cast<char*>(scratch);
@@ -357,11 +358,11 @@ int gated_backward(const gated_problem* p, int dtype, const void* x, const void*
     aw.e.ldo = g.lddw;
   }
   if (e == hipSuccess && want_dx && dwg)
-    e = run_both(pl.dx, pl.dw, dtype, ax, aw, on, true, on, true, sb + sc.planes, s);
+    e = run_both(pl, dtype, ax, aw, on, true, on, true, sb + sc.planes, s);
   else if (e == hipSuccess && want_dx)
-    e = run_product(pl.dx, dtype, ax, on, true, sb + sc.planes, s);
+    e = run_product(pl.dx, pl.both.dx, dtype, ax, on, true, sb + sc.planes, s);
   else if (e == hipSuccess && dwg)
-    e = run_product(pl.dw, dtype, aw, on, true, sb + sc.planes, s);
+    e = run_product(pl.dw, pl.both.dw, dtype, aw, on, true, sb + sc.planes, s);
   return status(e);
 }
 

@@ -141,14 +141,16 @@ __global__ __launch_bounds__(256) void linear_pack_kernel(const PackArgs a) {
     piece[i] = (int)(id - row * ppr);
     const E* p = static_cast<const E*>(a.src[q]) + row * a.ld[q];
     if (cols >= EPC)
-      v[i] = lin::load_piece<E>(reinterpret_cast<const char*>(p), min(piece[i] * EPC, cols - EPC) * (int)sizeof(E));
+      v[i] = lin::load_piece<E>(reinterpret_cast<const char*>(p),
+                                min(piece[i] * EPC, cols - EPC) * (int)sizeof(E));
     else
       v[i] = R::raw(p, 0, 0, 0, 1, cols, true);
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i)
     if (at + i * 256 < a.pieces[q])
-      static_cast<lin::i32x4*>(a.dst[q])[at + i * 256] = cols >= EPC ? R::shift(v[i], piece[i], cols) : v[i];
+      static_cast<lin::i32x4*>(a.dst[q])[at + i * 256] =
+          cols >= EPC ? R::shift(v[i], piece[i], cols) : v[i];
 }
 
 }  // namespace

@@ -30,8 +30,9 @@ __global__ __launch_bounds__(kStreamWaves * 64) void linear_stream_kernel(const 
   using namespace lin;
   constexpr int EB = (int)sizeof(E), EPC = 16 / EB, UE = 64 / EB, WAVES = kStreamWaves;
   constexpr int KINDS = GATED ? 2 : 1, RG = 16 / G, RB = RG * M;
-  constexpr int N = G > 1 || M > 1 || TC * KINDS >= 4 ? 2 : 4;  // weight loads of a batch, each G units
-  constexpr int BU = N * G;                                      // units of a batch
+  // weight loads of a batch, each of G units
+  constexpr int N = G > 1 || M > 1 || TC * KINDS >= 4 ? 2 : 4;
+  constexpr int BU = N * G;  // units of a batch
   typedef std::conditional_t<EB == 2, s16x8, f32x4> Frag;
   using R = Ragged<E, false>;
   constexpr int PARTS = WAVES * G;
@@ -95,7 +96,8 @@ __global__ __launch_bounds__(kStreamWaves * 64) void linear_stream_kernel(const 
       for (int m = 0; m < M; ++m)
 #pragma unroll
         for (int d = 0; d < KINDS; ++d)
-          b.p[m][d][i] = __builtin_bit_cast(Frag, piece(pr[d], pb[d], prow[m], (u + i * G + pu) * 64 + g * 16));
+          b.p[m][d][i] = __builtin_bit_cast(
+              Frag, piece(pr[d], pb[d], prow[m], (u + i * G + pu) * 64 + g * 16));
 #pragma unroll
     for (int i = 0; i < BU; ++i)
 #pragma unroll
@@ -201,6 +203,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const JoinArgs a) {
   float v[8], u[8];
 #pragma unroll
   for (int q = 0; q < 8; ++q) v[q] = u[q] = 0.0f;
+#pragma unroll 4
   for (int i = 0; i < a.splits; ++i) {
     const lin::f32x4 lo = *reinterpret_cast<const lin::f32x4*>(s);
     const lin::f32x4 hi = *reinterpret_cast<const lin::f32x4*>(s + 4);

@@ -166,21 +166,21 @@ namespace {
 // step (128 bytes of k): step, plus busy by the share of the units at work (the card
 // lowers its clock as they fill), plus more for every further workgroup on a unit,
 // up to units of them.  Fitted to 1300 timings of m 48 .. 8192, n and k 256 .. 4096
-// with 1 to 16 splits: off by 9% (root mean square), and the choice by it costs 1.6%
-// more than the best on average, 15% at most.
+// with 1 to 16 splits: off by 10% (root mean square), and the choice by it costs 1.8%
+// more than the best on average, 16% at most.
 struct Tiling {
   int tile, r, c, units;
   double fixed, round, step, busy, more;
 };
-const Tiling kTiles16[] = {{TILE_256, 256, 256, 1, 10.3, 7.3, 0.908, 0.314, 0.0},
-                           {TILE_256X128, 256, 128, 1, 8.0, 3.3, 0.555, 0.231, 0.0},
-                           {TILE_128, 128, 128, 2, 5.4, 0.7, 0.650, 0.114, 0.277},
-                           {TILE_64, 64, 64, 4, 4.2, 1.6, 0.400, 0.011, 0.160}};
-const Tiling kTiles16Gather[] = {{TILE_128, 128, 128, 2, 5.5, 0.0, 0.930, 0.166, 0.200},
-                                 {TILE_64, 64, 64, 4, 3.8, 0.0, 0.489, 0.081, 0.251}};
-const Tiling kTiles32[] = {{TILE_128, 128, 128, 2, 5.9, 0.0, 2.100, 0.294, 1.560},
-                           {TILE_64, 64, 64, 4, 4.2, 0.0, 0.753, 0.059, 0.525}};
-constexpr double kJoin = 3.6, kJoinByte = 3.4e-7;  // the second pass of a split: launch, plane bytes
+const Tiling kTiles16[] = {{TILE_256, 256, 256, 1, 10.1, 7.3, 0.912, 0.317, 0.0},
+                           {TILE_256X128, 256, 128, 1, 7.8, 3.1, 0.558, 0.227, 0.0},
+                           {TILE_128, 128, 128, 2, 5.2, 0.5, 0.547, 0.096, 0.326},
+                           {TILE_64, 64, 64, 4, 3.9, 2.1, 0.314, 0.0, 0.160}};
+const Tiling kTiles16Gather[] = {{TILE_128, 128, 128, 2, 5.6, 0.0, 0.883, 0.123, 0.281},
+                                 {TILE_64, 64, 64, 4, 3.8, 0.0, 0.465, 0.083, 0.250}};
+const Tiling kTiles32[] = {{TILE_128, 128, 128, 2, 5.9, 0.0, 1.990, 0.284, 1.410},
+                           {TILE_64, 64, 64, 4, 4.3, 0.0, 0.651, 0.048, 0.494}};
+constexpr double kJoin = 3.6, kJoinByte = 3.3e-7;  // the second pass of a split: launch, plane bytes
 
 int64_t tile_count(const ProductShape& s, const Tiling& t) {
   return ceil_div(s.gated ? 2 * s.R : s.R, t.r) * ceil_div(s.C, t.c) * s.nz;
@@ -257,7 +257,8 @@ ProductPlan plan_product(const ProductShape& s, int es) {
 }
 
 PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es) {
-  PairPlan out{-1, plan_product(dx, es).time + plan_product(dw, es).time};
+  PairPlan out{-1, 0.0, plan_product(dx, es), plan_product(dw, es)};
+  out.time = out.dx.time + out.dw.time;
   if (es != 2 || !dx.aligned || !dw.aligned) return out;
   const bool dw_first = dw.K * dw.nseg > dx.K * dx.nseg;
   const ProductShape &f = dw_first ? dw : dx, &l = dw_first ? dx : dw;
@@ -278,7 +279,10 @@ PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es) {
                            rest * std::floor(std::max(0.0, mid - (full + 1) * lf) / ll);
       (taken >= (double)nl ? hi : lo) = mid;
     }
-    if (t.fixed + hi < out.time) out = {t.tile, t.fixed + hi};
+    if (t.fixed + hi < out.time) {
+      out.tile = t.tile;
+      out.time = t.fixed + hi;
+    }
   }
   return out;
 }
@@ -322,8 +326,9 @@ bool any_needed(const Packing& k) {
 }
 
 // One product: packs if that is estimated to pay; returns the planes' bytes.
-int64_t settle(ProductShape* s, Packing* k, int es, int64_t* total) {
-  ProductPlan pl = plan_product(*s, es);
+int64_t settle(ProductShape* s, ProductPlan* run, Packing* k, int es, int64_t* total) {
+  ProductPlan& pl = *run;
+  pl = plan_product(*s, es);
   if (!s->aligned && s->C > 0 && pl.tile != TILE_STREAM) {
     ProductShape t = *s;
     t.aligned = true;
@@ -342,17 +347,20 @@ int64_t settle(ProductShape* s, Packing* k, int es, int64_t* total) {
 
 // Both products of a backward pass, the same way.
 void settle_backward(BackwardPlan* b, int es, int64_t at) {
+  b->both = plan_pair(b->dx, b->dw, es);
   if (b->dx.C > 0 && (!b->dx.aligned || !b->dw.aligned)) {
     ProductShape x = b->dx, w = b->dw;
     x.aligned = w.aligned = true;
-    if (plan_pair(x, w, es).time + lay_out(&b->pack, 0, es) < plan_pair(b->dx, b->dw, es).time) {
+    const PairPlan packed = plan_pair(x, w, es);
+    if (packed.time + lay_out(&b->pack, 0, es) < b->both.time) {
       b->pack.on = true;
       b->dx = x;
       b->dw = w;
+      b->both = packed;
     }
   }
   b->scratch.planes = at;
-  at += round_up(std::max(plan_product(b->dx, es).planes_bytes, plan_product(b->dw, es).planes_bytes), 256);
+  at += round_up(std::max(b->both.dx.planes_bytes, b->both.dw.planes_bytes), 256);
   b->scratch.pack = at;
   if (b->pack.on) {
     lay_out(&b->pack, at, es);
@@ -369,7 +377,7 @@ LinearPlan plan_linear(const linear_problem* p, const LinearGeo& g) {
   o.pack.item[0] = item_of(g.m, g.k, g.ldx, p->x_off, g.es);
   o.pack.item[1] = item_of(g.kn ? g.k : g.n, g.kn ? g.n : g.k, g.ldw, p->w_off, g.es);
   o.product = {g.n, g.m, g.k, 1, 1, g.kn, false, false, !any_needed(o.pack)};
-  o.planes = settle(&o.product, &o.pack, g.es, &o.total);
+  o.planes = settle(&o.product, &o.run, &o.pack, g.es, &o.total);
   return o;
 }
 
@@ -382,7 +390,7 @@ GatedPlan plan_gated(const gated_problem* p, const GatedGeo& g) {
   // both weights have one stride
   o.pack.item[1].need = o.pack.item[2].need = o.pack.item[1].need || o.pack.item[2].need;
   o.product = {g.f, g.m, g.k, 1, 1, false, false, true, !any_needed(o.pack)};
-  o.planes = settle(&o.product, &o.pack, g.es, &o.total);
+  o.planes = settle(&o.product, &o.run, &o.pack, g.es, &o.total);
   return o;
 }
 
@@ -445,16 +453,16 @@ void product_name(const ProductPlan& pl, char* buf, size_t len) {
     snprintf(buf, len, "%s", tile);
 }
 
-void backward_name(const char* call, int dtype, const ProductShape& sx, const ProductShape& sw,
-                   const char* pack, int es, char* buf, size_t len) {
-  const int tile = plan_pair(sx, sw, es).tile;
-  if (tile >= 0) {
-    snprintf(buf, len, "%s.%s.both.tile256x%d%s", call, dtype_name(dtype), tile == TILE_256 ? 256 : 128, pack);
+void backward_name(const char* call, int dtype, const BackwardPlan& pl, char* buf, size_t len) {
+  const char* pack = pl.pack.on ? ".pack" : "";
+  if (pl.both.tile >= 0) {
+    snprintf(buf, len, "%s.%s.both.tile256x%d%s", call, dtype_name(dtype),
+             pl.both.tile == TILE_256 ? 256 : 128, pack);
     return;
   }
   char dx[48], dw[48];
-  product_name(plan_product(sx, es), dx, sizeof dx);
-  product_name(plan_product(sw, es), dw, sizeof dw);
+  product_name(pl.both.dx, dx, sizeof dx);
+  product_name(pl.both.dw, dw, sizeof dw);
   snprintf(buf, len, "%s.%s.dx.%s.dw.%s%s", call, dtype_name(dtype), dx, dw, pack);
 }
 
@@ -543,7 +551,7 @@ int linear_describe_variant(const linear_problem* p, int dtype, char* buf, uint6
   if (st) return st;
   char name[48], text[96];
   const LinearPlan pl = plan_linear(p, g);
-  product_name(plan_product(pl.product, g.es), name, sizeof name);
+  product_name(pl.run, name, sizeof name);
   snprintf(text, sizeof text, "linear.%s.%s%s", dtype_name(dtype), name, pl.pack.on ? ".pack" : "");
   return put(text, buf, len);
 }
@@ -553,9 +561,7 @@ int linear_backward_describe_variant(const linear_problem* p, int dtype, char* b
   const int st = linear_validate(p, dtype, &g);
   if (st) return st;
   char text[160];
-  const BackwardPlan pl = plan_linear_backward(p, g);
-  backward_name("linear_backward", dtype, pl.dx, pl.dw, pl.pack.on ? ".pack" : "", g.es,
-                text, sizeof text);
+  backward_name("linear_backward", dtype, plan_linear_backward(p, g), text, sizeof text);
   return put(text, buf, len);
 }
 
@@ -565,7 +571,7 @@ int gated_describe_variant(const gated_problem* p, int dtype, char* buf, uint64_
   if (st) return st;
   char name[48], text[96];
   const GatedPlan pl = plan_gated(p, g);
-  product_name(plan_product(pl.product, g.es), name, sizeof name);
+  product_name(pl.run, name, sizeof name);
   snprintf(text, sizeof text, "gated.%s.%s%s", dtype_name(dtype), name, pl.pack.on ? ".pack" : "");
   return put(text, buf, len);
 }
@@ -575,16 +581,19 @@ int gated_backward_describe_variant(const gated_problem* p, int dtype, char* buf
   const int st = gated_validate(p, dtype, &g);
   if (st) return st;
   char text[160];
-  const BackwardPlan pl = plan_gated_backward(p, g);
-  backward_name("gated_backward", dtype, pl.dx, pl.dw, pl.pack.on ? ".pack" : "", g.es, text,
-                sizeof text);
+  backward_name("gated_backward", dtype, plan_gated_backward(p, g), text, sizeof text);
   return put(text, buf, len);
 }
 
-int linear_check(const linear_problem* p, int dtype, const void* x, const void* w, const void* b,
-                 const void* r, const void* y, const void* z, const void* scratch,
-                 uint64_t scratch_bytes) {
-  LinearGeo g;
+}  // extern "C"
+
+namespace convfwd {
+
+int linear_checked(const linear_problem* p, int dtype, const void* x, const void* w, const void* b,
+                   const void* r, const void* y, const void* z, const void* scratch,
+                   uint64_t scratch_bytes,
+                   LinearGeo* go, LinearPlan* plan) {
+  LinearGeo& g = *go;
   int st = linear_validate(p, dtype, &g);
   if (st) return st;
   if (!w || (p->has_bias && !b)) return CONV_ERR_ARG;
@@ -603,17 +612,19 @@ int linear_check(const linear_problem* p, int dtype, const void* x, const void* 
     if (!elem_aligned((const void*)ins[i].base, g.es)) return CONV_ERR_ARG;
   for (int i = 0; i < no; ++i)
     if (!elem_aligned((const void*)outs[i].base, g.es)) return CONV_ERR_ARG;
-  const int64_t need = plan_linear(p, g).total;
+  *plan = plan_linear(p, g);
+  const int64_t need = plan->total;
   st = scratch_ok(scratch, scratch_bytes, need);
   if (st) return st;
   return overlaps(outs, no, ins, ni, 0, res_at, g.es, scratch, need);
 }
 
-int linear_backward_check(const linear_problem* p, int dtype, const void* x, const void* w,
-                          const void* z, const void* dy, const void* dx, const void* dw,
-                          const void* db, const void* dr, const void* scratch,
-                          uint64_t scratch_bytes) {
-  LinearGeo g;
+int linear_backward_checked(const linear_problem* p, int dtype, const void* x, const void* w,
+                            const void* z, const void* dy, const void* dx, const void* dw,
+                            const void* db, const void* dr, const void* scratch,
+                            uint64_t scratch_bytes,
+                            LinearGeo* go, BackwardPlan* plan) {
+  LinearGeo& g = *go;
   int st = linear_validate(p, dtype, &g);
   if (st) return st;
   const bool rows = g.m > 0;  // operands of m rows may be null where there is no row
@@ -641,7 +652,8 @@ int linear_backward_check(const linear_problem* p, int dtype, const void* x, con
     if (!elem_aligned((const void*)ins[i].base, g.es)) return CONV_ERR_ARG;
   for (int i = 0; i < no; ++i)
     if (!elem_aligned((const void*)outs[i].base, g.es)) return CONV_ERR_ARG;
-  const int64_t need = plan_linear_backward(p, g).scratch.total;
+  *plan = plan_linear_backward(p, g);
+  const int64_t need = plan->scratch.total;
   st = scratch_ok(scratch, scratch_bytes, need);
   if (st) return st;
   // dr = dy in place is exact only where every later reader has its own copy of
@@ -650,10 +662,11 @@ int linear_backward_check(const linear_problem* p, int dtype, const void* x, con
   return overlaps(outs, no, ins, ni, dr_at, 0, g.es, scratch, need);
 }
 
-int gated_check(const gated_problem* p, int dtype, const void* x, const void* wg, const void* wu,
-                const void* bg, const void* bu, const void* h, const void* pg, const void* pu,
-                const void* scratch, uint64_t scratch_bytes) {
-  GatedGeo g;
+int gated_checked(const gated_problem* p, int dtype, const void* x, const void* wg, const void* wu,
+                  const void* bg, const void* bu, const void* h, const void* pg, const void* pu,
+                  const void* scratch, uint64_t scratch_bytes,
+                  GatedGeo* go, GatedPlan* plan) {
+  GatedGeo& g = *go;
   int st = gated_validate(p, dtype, &g);
   if (st) return st;
   if (!wg || !wu || (p->has_bias && (!bg || !bu))) return CONV_ERR_ARG;
@@ -676,17 +689,19 @@ int gated_check(const gated_problem* p, int dtype, const void* x, const void* wg
     if (!elem_aligned((const void*)ins[i].base, g.es)) return CONV_ERR_ARG;
   for (int i = 0; i < no; ++i)
     if (!elem_aligned((const void*)outs[i].base, g.es)) return CONV_ERR_ARG;
-  const int64_t need = plan_gated(p, g).total;
+  *plan = plan_gated(p, g);
+  const int64_t need = plan->total;
   st = scratch_ok(scratch, scratch_bytes, need);
   if (st) return st;
   return overlaps(outs, no, ins, ni, -1, -1, g.es, scratch, need);
 }
 
-int gated_backward_check(const gated_problem* p, int dtype, const void* x, const void* wg,
-                         const void* wu, const void* pg, const void* pu, const void* dh,
-                         const void* dx, const void* dwg, const void* dwu, const void* dbg,
-                         const void* dbu, const void* scratch, uint64_t scratch_bytes) {
-  GatedGeo g;
+int gated_backward_checked(const gated_problem* p, int dtype, const void* x, const void* wg,
+                           const void* wu, const void* pg, const void* pu, const void* dh,
+                           const void* dx, const void* dwg, const void* dwu, const void* dbg,
+                           const void* dbu, const void* scratch, uint64_t scratch_bytes,
+                           GatedGeo* go, BackwardPlan* plan) {
+  GatedGeo& g = *go;
   int st = gated_validate(p, dtype, &g);
   if (st) return st;
   const bool rows = g.m > 0;
@@ -716,10 +731,49 @@ int gated_backward_check(const gated_problem* p, int dtype, const void* x, const
     if (!elem_aligned((const void*)ins[i].base, g.es)) return CONV_ERR_ARG;
   for (int i = 0; i < no; ++i)
     if (!elem_aligned((const void*)outs[i].base, g.es)) return CONV_ERR_ARG;
-  const int64_t need = plan_gated_backward(p, g).scratch.total;
+  *plan = plan_gated_backward(p, g);
+  const int64_t need = plan->scratch.total;
   st = scratch_ok(scratch, scratch_bytes, need);
   if (st) return st;
   return overlaps(outs, no, ins, ni, -1, -1, g.es, scratch, need);
+}
+
+}  // namespace convfwd
+
+extern "C" {
+
+int linear_check(const linear_problem* p, int dtype, const void* x, const void* w, const void* b,
+                 const void* r, const void* y, const void* z, const void* scratch,
+                 uint64_t scratch_bytes) {
+  LinearGeo g;
+  LinearPlan plan;
+  return linear_checked(p, dtype, x, w, b, r, y, z, scratch, scratch_bytes, &g, &plan);
+}
+
+int linear_backward_check(const linear_problem* p, int dtype, const void* x, const void* w,
+                          const void* z, const void* dy, const void* dx, const void* dw,
+                          const void* db, const void* dr, const void* scratch,
+                          uint64_t scratch_bytes) {
+  LinearGeo g;
+  BackwardPlan plan;
+  return linear_backward_checked(p, dtype, x, w, z, dy, dx, dw, db, dr, scratch, scratch_bytes, &g, &plan);
+}
+
+int gated_check(const gated_problem* p, int dtype, const void* x, const void* wg, const void* wu,
+                const void* bg, const void* bu, const void* h, const void* pg, const void* pu,
+                const void* scratch, uint64_t scratch_bytes) {
+  GatedGeo g;
+  GatedPlan plan;
+  return gated_checked(p, dtype, x, wg, wu, bg, bu, h, pg, pu, scratch, scratch_bytes, &g, &plan);
+}
+
+int gated_backward_check(const gated_problem* p, int dtype, const void* x, const void* wg,
+                         const void* wu, const void* pg, const void* pu, const void* dh,
+                         const void* dx, const void* dwg, const void* dwu, const void* dbg,
+                         const void* dbu, const void* scratch, uint64_t scratch_bytes) {
+  GatedGeo g;
+  BackwardPlan plan;
+  return gated_backward_checked(p, dtype, x, wg, wu, pg, pu, dh, dx, dwg, dwu, dbg, dbu, scratch, scratch_bytes, &g, &plan);
 }
 
 }  // extern "C"

@@ -90,7 +90,8 @@ ProductPlan plan_product(const ProductShape& s, int es);
 // TILE_256X128), or one after the other (tile -1).
 struct PairPlan {
   int tile;
-  double time;  // estimated, us
+  double time;         // estimated, us
+  ProductPlan dx, dw;  // of each alone
 };
 PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es);
 ColsumPlan plan_colsum(int64_t m, int64_t n);
@@ -98,16 +99,19 @@ ColsumPlan plan_colsum(int64_t m, int64_t n);
 // A call's plan: its products as they will run, and its scratch.
 struct LinearPlan {
   ProductShape product;
+  ProductPlan run;
   Packing pack;  // x, w
   int64_t planes, total;
 };
 struct GatedPlan {
   ProductShape product;
+  ProductPlan run;
   Packing pack;  // x, wg, wu
   int64_t planes, total;
 };
 struct BackwardPlan {
   ProductShape dx, dw;
+  PairPlan both;
   Packing pack;  // linear: x, w, dy (identity); gated: x, wg, wu
   BackwardScratch scratch;
 };
@@ -115,6 +119,26 @@ LinearPlan plan_linear(const linear_problem* p, const LinearGeo& g);
 GatedPlan plan_gated(const gated_problem* p, const GatedGeo& g);
 BackwardPlan plan_linear_backward(const linear_problem* p, const LinearGeo& g);
 BackwardPlan plan_gated_backward(const gated_problem* p, const GatedGeo& g);
+
+// The checks of include/linear.h; a call that passes gets its geometry and plan.
+int linear_checked(const linear_problem* p, int dtype, const void* x, const void* w, const void* b,
+                   const void* r, const void* y, const void* z, const void* scratch,
+                   uint64_t scratch_bytes,
+                   LinearGeo* g, LinearPlan* plan);
+int linear_backward_checked(const linear_problem* p, int dtype, const void* x, const void* w,
+                            const void* z, const void* dy, const void* dx, const void* dw,
+                            const void* db, const void* dr, const void* scratch,
+                            uint64_t scratch_bytes,
+                            LinearGeo* g, BackwardPlan* plan);
+int gated_checked(const gated_problem* p, int dtype, const void* x, const void* wg, const void* wu,
+                  const void* bg, const void* bu, const void* h, const void* pg, const void* pu,
+                  const void* scratch, uint64_t scratch_bytes,
+                  GatedGeo* g, GatedPlan* plan);
+int gated_backward_checked(const gated_problem* p, int dtype, const void* x, const void* wg,
+                           const void* wu, const void* pg, const void* pu, const void* dh,
+                           const void* dx, const void* dwg, const void* dwu, const void* dbg,
+                           const void* dbu, const void* scratch, uint64_t scratch_bytes,
+                           GatedGeo* g, BackwardPlan* plan);
 
 inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 

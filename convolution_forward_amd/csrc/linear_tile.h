@@ -6,7 +6,8 @@
 //  * A workgroup owns BR x BC outputs; P rows feed MFMA's A operand and Q rows
 //    its B operand, so a lane ends with 4 consecutive r of one c.
 //  * Contraction step: 128 bytes of k (64 halves, 32 floats).  Both operands are
-//    staged in LDS, two buffers; step t + 1 is in flight while t is multiplied.
+//    staged in LDS, in two buffers (small tiles: three); the next step (two) is in
+//    flight while one is multiplied.
 //  * DMA: global to LDS directly (16 bytes a lane, no registers), for rows of
 //    whole aligned 16-byte vectors; descriptor range checks give zeros past the
 //    last row and, per lane, past the end of k.  Otherwise (odd strides, sizes or
@@ -219,8 +220,11 @@ __global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const Produ
   using TP = Tile<E, BR, PT, NT>;
   using TQ = Tile<E, BC, QT, NT>;
   constexpr int STAGE = TP::BYTES + TQ::BYTES;
+  // small tiles: buffers for two steps ahead (a step's products are shorter than a
+  // load's way); large ones: two buffers, so that two workgroups fit on a compute unit
+  constexpr int STAGES = DMA && BR * BC <= 64 * 64 ? 3 : 2;
   static_assert(!GATED || (!PT && !QT), "gated weights are k-major");
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  __shared__ __attribute__((aligned(1024))) char smem[STAGES * STAGE];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -249,22 +253,23 @@ __global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const Produ
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_f32x4{0, 0, 0, 0};
 
-  // per-item offsets: constant over the contraction
-  int poff[TP::ITEMS], qoff[TQ::ITEMS], pk[TP::ITEMS], qk[TQ::ITEMS];
+  // byte offsets of this thread's pieces, constant over the contraction; the piece's
+  // k, alike for all
+  int poff[TP::ITEMS], qoff[TQ::ITEMS], pk, qk;
 #pragma unroll
-  for (int i = 0; i < TP::ITEMS; ++i) {
+  for (int i = TP::ITEMS - 1; i >= 0; --i) {
     int row, piece;
     TP::item(i, tid, &row, &piece);
     if constexpr (GATED) row = (row / WR) * HW + row % HW;
     poff[i] = (int)(row * a.ldp * TP::EB) + piece * 16;
-    pk[i] = piece * TP::EPC;
+    pk = piece * TP::EPC;
   }
 #pragma unroll
-  for (int i = 0; i < TQ::ITEMS; ++i) {
+  for (int i = TQ::ITEMS - 1; i >= 0; --i) {
     int row, piece;
     TQ::item(i, tid, &row, &piece);
     qoff[i] = (int)(row * a.ldq * TQ::EB) + piece * 16;
-    qk[i] = piece * TQ::EPC;
+    qk = piece * TQ::EPC;
   }
   const unsigned lds0 = lds_addr(smem);
 
@@ -298,48 +303,76 @@ __global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const Produ
   };
 
   if constexpr (DMA) {
-    auto issue = [&](int t, int b) {
-      const char *p0, *p1, *q;
-      int kk;
-      bases(t, &p0, &p1, &q, &kk);
-      const int kv = min(kk, TP::BKE);
-      // bytes from the base to the end of the last valid row's last piece (which a
-      // padded operand fills with zeros)
-      auto range = [&](bool tr_, long long rows, long long ld) {
-        const long long n = tr_ ? rows : kk, up = (n + TP::EPC - 1) / TP::EPC * TP::EPC;
-        return ((tr_ ? kv - 1 : min(rows, 256LL) - 1) * ld + up) * TP::EB;
-      };
-      const long long pr = range(PT, nr, a.ldp), qr = range(QT, nc, a.ldq);
-      const i32x4 rp0 = make_rsrc(p0, pr), rp1 = GATED ? make_rsrc(p1, pr) : rp0;
-      const i32x4 rq = make_rsrc(q, qr);
+    // What the next step's loads need, moved on by additions after each.  A descriptor
+    // ends with the last valid row (transposed: the last valid k; a padded operand's
+    // last piece is filled with zeros), so that everything past an end reads as zeros.
+    constexpr int EB = TP::EB, EPC = TP::EPC, BKE = TP::BKE;
+    const int ldpb = (int)a.ldp * EB, ldqb = (int)a.ldq * EB;
+    const long long pstep = PT ? (long long)BKE * ldpb : 128, qstep = QT ? (long long)BKE * ldqb : 128;
+    auto up = [](int n) { return (n + EPC - 1) / EPC * EPC * EB; };
+    const int np = (int)min(nr, (long long)(GATED ? BR / 2 : BR)), nq = (int)min(nc, (long long)BC);
+    const int pspan = PT ? up(np) : (np - 1) * ldpb, qspan = QT ? up(nq) : (nq - 1) * ldqb;
+    const char *pp, *pu, *qq;
+    int left;
+    auto start = [&](int t) {
+      bases(t, &pp, &pu, &qq, &left);
+    };
+    int at = t0;
+    start(t0);
+    const int ktail = a.K - (a.K - 1) / BKE * BKE;  // k of a segment's last step
+    const bool ptail = PT || pk < ktail, qtail = QT || qk < ktail;
+    auto issue = [&](int b) {
+      const int kv = min(left, BKE);
+      const i32x4 rp0 = make_rsrc(pp, pspan + (PT ? (kv - 1) * ldpb : up(kv)));
+      const i32x4 rp1 = GATED ? make_rsrc(pu, pspan + up(kv)) : rp0;
+      const i32x4 rq = make_rsrc(qq, qspan + (QT ? (kv - 1) * ldqb : up(kv)));
       const unsigned lp = lds0 + b * STAGE + wave * 1024, lq = lp + TP::BYTES;
-      const bool tail = kk < TP::BKE;
+      const bool pall = left >= BKE || ptail, qall = left >= BKE || qtail;
 #pragma unroll
       for (int i = 0; i < TP::ITEMS; ++i) {
-        const int off = !PT && tail && pk[i] >= kk ? kOob : poff[i];
-        const bool up = GATED && ((i * (NT / 8) + wave * 8) % WR) >= HW;
-        dma16(up ? rp1 : rp0, off, lp + i * NT * 16);
+        const bool up_row = GATED && ((i * (NT / 8) + wave * 8) % WR) >= HW;
+        dma16(up_row ? rp1 : rp0, pall ? poff[i] : kOob, lp + i * NT * 16);
       }
 #pragma unroll
-      for (int i = 0; i < TQ::ITEMS; ++i) {
-        const int off = !QT && tail && qk[i] >= kk ? kOob : qoff[i];
-        dma16(rq, off, lq + i * NT * 16);
-      }
+      for (int i = 0; i < TQ::ITEMS; ++i) dma16(rq, qall ? qoff[i] : kOob, lq + i * NT * 16);
+      ++at;
+      pp += pstep;
+      pu += pstep;
+      qq += qstep;
+      left -= BKE;
+      if (a.nseg > 1 && at == a.ktiles) start(at);  // the second segment
     };
-    int b = 0;
-    if (t0 < t1) issue(t0, 0);
-    for (int t = t0; t < t1; ++t) {
-      if (t + 1 < t1) {
-        issue(t + 1, b ^ 1);
-        vm_wait<TP::ITEMS + TQ::ITEMS>();
-      } else {
-        vm_wait<0>();
+    constexpr int LOADS = TP::ITEMS + TQ::ITEMS;
+    if constexpr (STAGES > 2) {
+#pragma unroll
+      for (int i = 0; i < STAGES - 1; ++i)
+        if (t0 + i < t1) issue(i);
+      int b = 0;
+      for (int t = t0; t < t1; ++t) {
+        if (t + STAGES - 2 < t1) vm_wait<(STAGES - 2) * LOADS>();
+        else vm_wait<0>();
+        lds_wait();
+        barrier();  // step t is staged, and every wave is done with step t - 1's buffer
+        if (t + STAGES - 1 < t1) issue(b == 0 ? STAGES - 1 : b - 1);
+        compute(smem + b * STAGE);
+        b = b == STAGES - 1 ? 0 : b + 1;
       }
-      barrier();
-      compute(smem + b * STAGE);
-      lds_wait();
-      barrier();
-      b ^= 1;
+    } else {
+      int b = 0;
+      if (t0 < t1) issue(0);
+      for (int t = t0; t < t1; ++t) {
+        if (t + 1 < t1) {
+          issue(b ^ 1);
+          vm_wait<LOADS>();
+        } else {
+          vm_wait<0>();
+        }
+        barrier();
+        compute(smem + b * STAGE);
+        lds_wait();
+        barrier();
+        b ^= 1;
+      }
     }
   } else {
     i32x4 pv[TP::ITEMS], qv[TQ::ITEMS];
