@@ -231,13 +231,15 @@ ProductPlan plan_product(const ProductShape& s, int es) {
   }
   if (!s.pt && !s.qt && s.nseg == 1 && s.nz == 1 && s.C <= 32 && s.K * es >= 16) {
     // the streamed kernel: on every compute unit the bytes of its weight rows, of Q
-    // (from L2, 0.4 of a weight row's time) and a workgroup's start (4 rows' time), at
-    // 24 KB a us (float32, bound by its products: 18)
+    // (from L2, 0.8 of a weight row's time) and a workgroup's start (4 rows' time), at
+    // 30 KB a us (float32, bound by its products as well: 26; 16-bit rows from odd
+    // elements on: 21); within 15% of 8 timings from 4 to 180 MB of weights
+    const double rate = es == 4 ? 26e3 : s.aligned ? 30e3 : 21e3;
     for (int rows = s.C > 16 ? 32 : 16; rows >= 4; rows /= 2) {
       const int64_t groups = ceil_div(s.R, rows);
       const double cost = (double)ceil_div(groups, kCus) *
-                          ((s.gated ? 2 : 1) * rows + 0.4 * (double)s.C + 4.0);
-      const double t = 3.0 + cost * (double)(s.K * es) / (es == 4 ? 18e3 : 24e3);
+                          ((s.gated ? 2 : 1) * rows + 0.8 * (double)s.C + 4.0);
+      const double t = 3.0 + cost * (double)(s.K * es) / rate;
       if (t < best) {
         best = t;
         pl.tile = TILE_STREAM;
@@ -288,10 +290,10 @@ PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es) {
 }
 
 ColsumPlan plan_colsum(int64_t m, int64_t n) {
-  // one workgroup per chunk and 256 columns: about four per compute unit,
+  // one workgroup per chunk and 256 columns: about eight per compute unit,
   // at least 32 rows each, at most 256 chunks to join
   const int64_t cols = ceil_div(n, 256);
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(256, 4 * kCus / cols));
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(256, 8 * kCus / cols));
   ColsumPlan c;
   c.rows = std::max<int64_t>(32, round_up(ceil_div(std::max<int64_t>(m, 1), want), 8));
   c.chunks = ceil_div(std::max<int64_t>(m, 1), c.rows);

@@ -177,6 +177,12 @@ struct Ragged {
   static constexpr int EPC = 16 / (int)sizeof(E);
   struct __attribute__((packed, aligned(sizeof(E)))) P { i32x4 v; };
 
+  // The byte offset of a piece's load where the step has all its k.
+  static __device__ __forceinline__ int at(long long ld, int row, int piece, long long nrow) {
+    const int r = T ? row : (int)min((long long)row, nrow - 1);
+    const int c = T ? (int)min((long long)piece * EPC, nrow - EPC) : piece * EPC;
+    return (int)(r * ld + c) * (int)sizeof(E);
+  }
   static __device__ __forceinline__ i32x4 raw(const E* base, long long ld, int row, int piece,
                                               long long nrow, long long nk, bool tiny) {
     const int len = (int)min(T ? nrow : nk, 1LL << 20), rows = (int)min(T ? nk : nrow, 256LL);
@@ -379,10 +385,36 @@ __global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const Produ
     using RP = Ragged<E, PT>;
     using RQ = Ragged<E, QT>;
     const bool ptiny = (PT ? a.R : a.K) < TP::EPC, qtiny = (QT ? a.C : a.K) < TQ::EPC;
+    // byte offsets from a step's first element, alike for all steps of whole k
+    int pat[TP::ITEMS], qat[TQ::ITEMS];
+#pragma unroll
+    for (int i = 0; i < TP::ITEMS; ++i) {
+      int row, piece;
+      TP::item(i, tid, &row, &piece);
+      if constexpr (GATED) row = (row / WR) * HW + row % HW;
+      pat[i] = RP::at(a.ldp, row, piece, nr);
+    }
+#pragma unroll
+    for (int i = 0; i < TQ::ITEMS; ++i) {
+      int row, piece;
+      TQ::item(i, tid, &row, &piece);
+      qat[i] = RQ::at(a.ldq, row, piece, nc);
+    }
     auto fetch = [&](int t) {
       const char *p0, *p1, *q;
       int kk;
       bases(t, &p0, &p1, &q, &kk);
+      if (kk >= TP::BKE && !ptiny && !qtiny) {
+#pragma unroll
+        for (int i = 0; i < TP::ITEMS; ++i) {
+          const bool up = GATED && ((i * (NT / 8) + wave * 8) % WR) >= HW;
+          pv[i] = reinterpret_cast<const typename RP::P*>((up ? p1 : p0) + pat[i])->v;
+        }
+#pragma unroll
+        for (int i = 0; i < TQ::ITEMS; ++i)
+          qv[i] = reinterpret_cast<const typename RQ::P*>(q + qat[i])->v;
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < TP::ITEMS; ++i) {
         int row, piece;
