@@ -44,6 +44,12 @@ hipError_t join(int dtype, const JoinArgs& a, bool gated, hipStream_t s) {
   return launch_join<float>(a, gated, s);
 }
 
+hipError_t join_pair(int dtype, const JoinArgs& a, const JoinArgs& b, hipStream_t s) {
+  if (dtype == CONV_F16) return launch_join_pair<_Float16>(a, b, s);
+  if (dtype == CONV_BF16) return launch_join_pair<__bf16>(a, b, s);
+  return launch_join_pair<float>(a, b, s);
+}
+
 hipError_t dz_pass(int dtype, const DzArgs& a, bool gated, int chunks, hipStream_t s) {
   if (dtype == CONV_F16) return launch_dz<_Float16>(a, gated, chunks, s);
   if (dtype == CONV_BF16) return launch_dz<__bf16>(a, gated, chunks, s);
@@ -67,66 +73,77 @@ bool direct(const ProductShape& s, const ProductArgs& a, int es, bool p_padded, 
   return q_padded || (s.qt ? s.C : s.K) * es % 16 == 0;
 }
 
+// The plan into a product's arguments; its operands and epilogue are set.
+void set_plan(const ProductShape& s, const ProductPlan& pl, void* planes, ProductArgs* a) {
+  a->R = (int)s.R; a->C = (int)s.C; a->K = (int)s.K;
+  a->nseg = s.nseg; a->nz = s.nz;
+  a->ktiles = (int)pl.ktiles; a->splits = pl.splits; a->per_split = (int)pl.per_split;
+  a->planes = static_cast<float*>(planes);
+  a->plane_ld = pl.plane_ld;
+  a->e.R = a->R;
+}
+
+JoinArgs join_of(const ProductShape& s, const ProductArgs& a) {
+  JoinArgs j{};
+  j.planes = a.planes;
+  j.plane_ld = a.plane_ld;
+  j.plane_stride = a.plane_ld * s.C * s.nz * (s.gated ? 2 : 1);
+  j.splits = a.splits;
+  j.C = a.C;
+  j.nz = s.nz;
+  j.e = a.e;
+  return j;
+}
+
 // Runs one planned product; a's operands and epilogue are set.
 hipError_t run_product(const ProductShape& s, const ProductPlan& pl, int dtype, ProductArgs& a,
                        bool p_padded, bool q_padded, void* planes, hipStream_t st) {
   const int es = (int)dtype_size(dtype);
-  a.R = (int)s.R; a.C = (int)s.C; a.K = (int)s.K;
-  a.nseg = s.nseg; a.nz = s.nz;
-  a.ktiles = (int)pl.ktiles; a.splits = pl.splits; a.per_split = (int)pl.per_split;
-  a.planes = static_cast<float*>(planes);
-  a.plane_ld = pl.plane_ld;
-  a.e.R = a.R;
+  set_plan(s, pl, planes, &a);
   const bool dma = direct(s, a, es, p_padded, q_padded);
   if (pl.tile == TILE_STREAM)
     return stream_product(dtype, a, pl.stream_t, pl.stream_rows, s.gated, dma, st);
   const int layout = s.pt ? (s.qt ? 2 : 1) : 0;
   hipError_t e = product(dtype, a, pl.tile, layout, s.gated, dma, st);
   if (e != hipSuccess || pl.splits == 1) return e;
-  JoinArgs j{};
-  j.planes = a.planes;
-  j.plane_ld = pl.plane_ld;
-  j.plane_stride = pl.plane_ld * s.C * s.nz * (s.gated ? 2 : 1);
-  j.splits = pl.splits;
-  j.C = a.C;
-  j.nz = s.nz;
-  j.e = a.e;
-  return join(dtype, j, s.gated, st);
+  return join(dtype, join_of(s, a), s.gated, st);
 }
 
 hipError_t pair(int dtype, const PairArgs& a, int tile, bool dx_transposed, hipStream_t s) {
   if (dtype == CONV_F16) return launch_pair<_Float16>(a, tile, dx_transposed, s);
-  return launch_pair<__bf16>(a, tile, dx_transposed, s);
+  if (dtype == CONV_BF16) return launch_pair<__bf16>(a, tile, dx_transposed, s);
+  return launch_pair<float>(a, tile, dx_transposed, s);
 }
 
 // Both products of a backward pass: in one launch where the plan pairs them and the
 // operands allow it, one after the other otherwise.
 hipError_t run_both(const BackwardPlan& pl, int dtype, ProductArgs& dx, ProductArgs& dw,
-                    bool dx_p_padded, bool dx_q_padded, bool dw_p_padded,
-                    bool dw_q_padded, void* planes, hipStream_t st) {
+                    bool dx_p_padded, bool dx_q_padded, bool dw_p_padded, bool dw_q_padded,
+                    char* scratch, hipStream_t st) {
   const int es = (int)dtype_size(dtype);
-  const ProductShape &sx = pl.dx, &sw = pl.dw;
-  const int tile = pl.both.tile;
-  if (tile >= 0 && direct(sx, dx, es, dx_p_padded, dx_q_padded) &&
-      direct(sw, dw, es, dw_p_padded, dw_q_padded)) {
-    PairArgs a{};
-    const ProductShape* shapes[2] = {&sx, &sw};
-    ProductArgs* args[2] = {&dx, &dw};
-    for (int i = 0; i < 2; ++i) {
-      ProductArgs& q = *args[i];
-      q.R = (int)shapes[i]->R; q.C = (int)shapes[i]->C; q.K = (int)shapes[i]->K;
-      q.nseg = shapes[i]->nseg; q.nz = shapes[i]->nz;
-      q.ktiles = (int)ceil_div(shapes[i]->K, 64);
-      q.splits = 1; q.per_split = q.ktiles * q.nseg;
-      q.e.R = q.R;
-    }
-    a.dx = dx;
-    a.dw = dw;
-    return pair(dtype, a, tile, sx.pt, st);
+  void *planes = scratch + pl.scratch.planes, *planes_dw = scratch + pl.scratch.planes_dw;
+  if (pl.both.tile < 0 || !direct(pl.dx, dx, es, dx_p_padded, dx_q_padded) ||
+      !direct(pl.dw, dw, es, dw_p_padded, dw_q_padded)) {
+    const hipError_t e = run_product(pl.dx, pl.both.dx, dtype, dx, dx_p_padded, dx_q_padded, planes, st);
+    if (e != hipSuccess) return e;
+    return run_product(pl.dw, pl.both.dw, dtype, dw, dw_p_padded, dw_q_padded, planes_dw, st);
   }
-  const hipError_t e = run_product(sx, pl.both.dx, dtype, dx, dx_p_padded, dx_q_padded, planes, st);
-  if (e != hipSuccess) return e;
-  return run_product(sw, pl.both.dw, dtype, dw, dw_p_padded, dw_q_padded, planes, st);
+  PairArgs a{};
+  set_plan(pl.dx, pl.both.dx, planes, &dx);
+  set_plan(pl.dw, pl.both.dw, planes_dw, &dw);
+  if (pl.both.tile != TILE_64) {  // the large tiles' launch splits neither
+    dx.splits = dw.splits = 1;
+    dx.per_split = dx.ktiles * dx.nseg;
+    dw.per_split = dw.ktiles * dw.nseg;
+  }
+  a.dx = dx;
+  a.dw = dw;
+  const hipError_t e = pair(dtype, a, pl.both.tile, pl.dx.pt, st);
+  if (e != hipSuccess || (dx.splits == 1 && dw.splits == 1)) return e;
+  if (dx.splits > 1 && dw.splits > 1)
+    return join_pair(dtype, join_of(pl.dx, dx), join_of(pl.dw, dw), st);
+  return dx.splits > 1 ? join(dtype, join_of(pl.dx, dx), false, st)
+                       : join(dtype, join_of(pl.dw, dw), false, st);
 }
 
 // Copies the operands that the plan packs and points to the copies.  src[i] and ld[i]:
@@ -290,11 +307,11 @@ int linear_backward(const linear_problem* p, int dtype, const void* x, const voi
   // rows padded with zeros: packed ones, and dz
   const bool dpad = on || act, wp = g.kn ? dpad : on, wq = g.kn ? on : dpad;
   if (e == hipSuccess && want_dx && dw)
-    e = run_both(pl, dtype, ax, aw, on, dpad, wp, wq, sb + sc.planes, s);
+    e = run_both(pl, dtype, ax, aw, on, dpad, wp, wq, sb, s);
   else if (e == hipSuccess && want_dx)
     e = run_product(pl.dx, pl.both.dx, dtype, ax, on, dpad, sb + sc.planes, s);
   else if (e == hipSuccess && dw)
-    e = run_product(pl.dw, pl.both.dw, dtype, aw, wp, wq, sb + sc.planes, s);
+    e = run_product(pl.dw, pl.both.dw, dtype, aw, wp, wq, sb + sc.planes_dw, s);
   return status(e);
 }
 
@@ -358,11 +375,11 @@ int gated_backward(const gated_problem* p, int dtype, const void* x, const void*
     aw.e.ldo = g.lddw;
   }
   if (e == hipSuccess && want_dx && dwg)
-    e = run_both(pl, dtype, ax, aw, on, true, on, true, sb + sc.planes, s);
+    e = run_both(pl, dtype, ax, aw, on, true, on, true, sb, s);
   else if (e == hipSuccess && want_dx)
     e = run_product(pl.dx, pl.both.dx, dtype, ax, on, true, sb + sc.planes, s);
   else if (e == hipSuccess && dwg)
-    e = run_product(pl.dw, pl.both.dw, dtype, aw, on, true, sb + sc.planes, s);
+    e = run_product(pl.dw, pl.both.dw, dtype, aw, on, true, sb + sc.planes_dw, s);
   return status(e);
 }
 

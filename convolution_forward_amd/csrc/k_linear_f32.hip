@@ -4,5 +4,6 @@
 namespace convfwd {
 
 template hipError_t launch_product<float>(const ProductArgs&, int, int, bool, bool, hipStream_t);
+template hipError_t launch_pair<float>(const PairArgs&, int, bool, hipStream_t);
 
 }  // namespace convfwd

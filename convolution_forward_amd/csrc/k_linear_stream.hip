@@ -191,9 +191,9 @@ __global__ __launch_bounds__(kStreamWaves * 64) void linear_stream_kernel(const 
 
 // Joins the planes of a split contraction in split order: 8 outputs a thread.
 template <typename E, bool GATED>
-__global__ __launch_bounds__(256) void linear_join_kernel(const JoinArgs a) {
+__device__ __forceinline__ void join(const JoinArgs& a, long long block) {
   const int per_row = (int)(a.plane_ld / 8);
-  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long id = block * 256 + threadIdx.x;
   const long long row = id / per_row;  // z * C + c
   if (row >= (long long)a.nz * a.C) return;
   const int r = (int)(id - row * per_row) * 8;
@@ -221,6 +221,23 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const JoinArgs a) {
   if (r >= a.e.R) return;
   if constexpr (GATED) finish_gated<E>(a.e, c, r, v, u);
   else finish_linear<E>(a.e, z, c, r, v);
+}
+
+template <typename E, bool GATED>
+__global__ __launch_bounds__(256) void linear_join_kernel(const JoinArgs a) {
+  join<E, GATED>(a, blockIdx.x);
+}
+
+template <typename E>
+__global__ __launch_bounds__(256) void linear_join_pair_kernel(const JoinArgs a, const JoinArgs b,
+                                                               int first) {
+  if ((int)blockIdx.x < first) join<E, false>(a, blockIdx.x);
+  else join<E, false>(b, (int)blockIdx.x - first);
+}
+
+unsigned join_blocks(const JoinArgs& a) {
+  const long long items = (long long)a.nz * a.C * (a.plane_ld / 8);
+  return (unsigned)((items + 255) / 256);
 }
 
 template <typename E, int TC, bool GATED, int G, int M>
@@ -254,16 +271,24 @@ hipError_t launch_stream(const ProductArgs& a, int blocks16, int rows, bool gate
 
 template <typename E>
 hipError_t launch_join(const JoinArgs& a, bool gated, hipStream_t s) {
-  const long long items = (long long)a.nz * a.C * (a.plane_ld / 8);
-  const dim3 grid((unsigned)((items + 255) / 256));
+  const dim3 grid(join_blocks(a));
   if (gated) hipLaunchKernelGGL((linear_join_kernel<E, true>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((linear_join_kernel<E, false>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
+template <typename E>
+hipError_t launch_join_pair(const JoinArgs& a, const JoinArgs& b, hipStream_t s) {
+  const unsigned first = join_blocks(a);
+  hipLaunchKernelGGL((linear_join_pair_kernel<E>), dim3(first + join_blocks(b)), dim3(256), 0, s, a, b,
+                     (int)first);
+  return hipGetLastError();
+}
+
 #define CONVFWD_INST(E)                                                                      \
   template hipError_t launch_stream<E>(const ProductArgs&, int, int, bool, bool, hipStream_t); \
-  template hipError_t launch_join<E>(const JoinArgs&, bool, hipStream_t);
+  template hipError_t launch_join<E>(const JoinArgs&, bool, hipStream_t);                   \
+  template hipError_t launch_join_pair<E>(const JoinArgs&, const JoinArgs&, hipStream_t);
 CONVFWD_INST(_Float16)
 CONVFWD_INST(__bf16)
 CONVFWD_INST(float)

@@ -38,7 +38,7 @@ struct ProductArgs {
   LinEpilogue e;
 };
 
-// Two products of one launch (neither split).
+// Two products of one launch (split on small tiles only).
 struct PairArgs {
   ProductArgs dx, dw;
   int first;     // workgroups of the one that comes first
@@ -91,7 +91,7 @@ hipError_t launch_product(const ProductArgs& a, int tile, int layout, bool gated
                           hipStream_t s);
 template <typename E>
 hipError_t launch_pack(const PackArgs& a, hipStream_t s);
-// tile: TILE_256 or TILE_256X128; both products' operands go to LDS directly.
+// tile: TILE_256, TILE_256X128 (16 bits) or TILE_64; operands that go to LDS directly.
 template <typename E>
 hipError_t launch_pair(const PairArgs& a, int tile, bool dx_transposed, hipStream_t s);
 template <typename E>
@@ -99,6 +99,8 @@ hipError_t launch_stream(const ProductArgs& a, int blocks16, int rows, bool gate
                          hipStream_t s);
 template <typename E>
 hipError_t launch_join(const JoinArgs& a, bool gated, hipStream_t s);
+template <typename E>
+hipError_t launch_join_pair(const JoinArgs& a, const JoinArgs& b, hipStream_t s);
 template <typename E>
 hipError_t launch_dz(const DzArgs& a, bool gated, int chunks, hipStream_t s);
 template <typename E>

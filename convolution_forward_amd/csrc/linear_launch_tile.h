@@ -61,19 +61,26 @@ hipError_t launch_product(const ProductArgs& a, int tile, int layout, bool gated
 
 template <typename E>
 hipError_t launch_pair(const PairArgs& pair, int tile, bool dx_transposed, hipStream_t s) {
+  PairArgs a = pair;
+  const int br = tile == TILE_64 ? 64 : 256;
+  const int bc = tile == TILE_64 ? 64 : tile == TILE_256 ? 256 : 128;
+  int grid[2], i = 0;
+  for (ProductArgs* p : {&a.dx, &a.dw}) {
+    p->ntr = (p->R + br - 1) / br;
+    p->ntc = (p->C + bc - 1) / bc;
+    grid[i++] = p->ntr * p->ntc * p->nz * p->splits;
+  }
+  // the longer contraction first: the shorter tiles then even out the last round
+  a.dw_first = a.dw.per_split > a.dx.per_split;
+  a.first = grid[a.dw_first];
+  const dim3 g(grid[0] + grid[1]);
+  if (tile == TILE_64) {
+    if (dx_transposed) hipLaunchKernelGGL((linear_tile_pair_kernel<E, true>), g, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((linear_tile_pair_kernel<E, false>), g, dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
   if constexpr (sizeof(E) == 2) {
-    PairArgs a = pair;
-    const int bc = tile == TILE_256 ? 256 : 128;
-    int grid[2], i = 0;
-    for (ProductArgs* p : {&a.dx, &a.dw}) {
-      p->ntr = (p->R + 255) / 256;
-      p->ntc = (p->C + bc - 1) / bc;
-      grid[i++] = p->ntr * p->ntc * p->nz;
-    }
-    // the longer contraction first: the shorter tiles then even out the last round
-    a.dw_first = a.dw.ktiles * a.dw.nseg > a.dx.ktiles * a.dx.nseg;
-    a.first = grid[a.dw_first];
-    const dim3 g(grid[0] + grid[1]), b(512);
+    const dim3 b(512);
     if (dx_transposed) {
       if (bc == 256) hipLaunchKernelGGL((linear_pair_kernel<E, true, 256>), g, b, 0, s, a);
       else hipLaunchKernelGGL((linear_pair_kernel<E, true, 128>), g, b, 0, s, a);
@@ -83,7 +90,7 @@ hipError_t launch_pair(const PairArgs& pair, int tile, bool dx_transposed, hipSt
     }
     return hipGetLastError();
   }
-  return hipErrorInvalidValue;  // 16-bit operands only
+  return hipErrorInvalidValue;  // the large tiles take 16-bit operands
 }
 
 }  // namespace convfwd

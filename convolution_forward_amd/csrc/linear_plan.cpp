@@ -180,6 +180,7 @@ const Tiling kTiles16Gather[] = {{TILE_128, 128, 128, 2, 5.6, 0.0, 0.883, 0.123,
                                  {TILE_64, 64, 64, 4, 3.8, 0.0, 0.465, 0.083, 0.250}};
 const Tiling kTiles32[] = {{TILE_128, 128, 128, 2, 5.9, 0.0, 1.990, 0.284, 1.410},
                            {TILE_64, 64, 64, 4, 4.3, 0.0, 0.651, 0.048, 0.494}};
+const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
 constexpr double kJoin = 3.6, kJoinByte = 3.3e-7;  // the second pass of a split: launch, plane bytes
 
 int64_t tile_count(const ProductShape& s, const Tiling& t) {
@@ -209,7 +210,6 @@ ProductPlan plan_product(const ProductShape& s, int es) {
   // the cheapest tile and split count by the model of the measured times
   const Tiling* table = es == 4 ? kTiles32 : s.aligned ? kTiles16 : kTiles16Gather;
   const int count = es == 2 && s.aligned ? 4 : 2;
-  static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
   const int64_t plane_ld = round_up(s.R, 8);
   const int64_t plane = plane_ld * s.C * 4 * (s.gated ? 2 : 1) * s.nz;  // bytes of one
   double best = 0.0;
@@ -219,7 +219,10 @@ ProductPlan plan_product(const ProductShape& s, int es) {
     for (int want : kSplits) {
       if (want > 1 && (all / want < 2 || tiles >= 2 * kCus || plane * want > (1LL << 30))) break;
       const int64_t per = ceil_div(all, want), n = ceil_div(all, per);
-      double t = time_of(table[i], tiles * n, per);
+      // a transposed operand that is gathered costs a third more (777 x 1001 x 1531: 21
+      // us for 16)
+      const double slow = s.pt && es == 2 && !s.aligned ? 1.35 : 1.0;
+      double t = slow * time_of(table[i], tiles * n, per);
       if (n > 1) t += kJoin + kJoinByte * (double)(plane * n);
       if (pl.tile < 0 || t < best) {
         best = t;
@@ -261,7 +264,36 @@ ProductPlan plan_product(const ProductShape& s, int es) {
 PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es) {
   PairPlan out{-1, 0.0, plan_product(dx, es), plan_product(dw, es)};
   out.time = out.dx.time + out.dw.time;
-  if (es != 2 || !dx.aligned || !dw.aligned) return out;
+  if (!dx.aligned || !dw.aligned) return out;
+  // small tiles: the contractions of both cut into pieces of one length
+  const Tiling& small = es == 4 ? kTiles32[1] : kTiles16[3];
+  const int64_t bk = 128 / es, ax = ceil_div(dx.K, bk) * dx.nseg, aw = ceil_div(dw.K, bk) * dw.nseg;
+  const int64_t tx = tile_count(dx, small), tw = tile_count(dw, small);
+  for (int want : kSplits) {
+    const int64_t per = ceil_div(std::max(ax, aw), want);
+    if (ax < 1 || aw < 1 || tx + tw >= 8 * kCus || (want > 1 && per < 2)) break;
+    ProductPlan p[2] = {out.dx, out.dw};
+    const ProductShape* shapes[2] = {&dx, &dw};
+    const int64_t steps[2] = {ax, aw};
+    int64_t bytes = 0;
+    for (int i = 0; i < 2; ++i) {
+      p[i].tile = TILE_64;
+      p[i].ktiles = ceil_div(shapes[i]->K, bk);
+      p[i].per_split = std::min(per, steps[i]);
+      p[i].splits = (int)ceil_div(steps[i], per);
+      p[i].plane_ld = p[i].planes_bytes = 0;
+      if (p[i].splits > 1) {
+        p[i].plane_ld = round_up(shapes[i]->R, 8);
+        p[i].planes_bytes = p[i].plane_ld * shapes[i]->C * 4 * shapes[i]->nz * p[i].splits;
+        bytes += p[i].planes_bytes;
+      }
+    }
+    if (bytes > (1LL << 30)) break;
+    double t = time_of(small, tx * p[0].splits + tw * p[1].splits, per);
+    if (bytes > 0) t += kJoin + kJoinByte * (double)bytes;
+    if (t < out.time) out = {TILE_64, t, p[0], p[1]};
+  }
+  if (es != 2) return out;
   const bool dw_first = dw.K * dw.nseg > dx.K * dx.nseg;
   const ProductShape &f = dw_first ? dw : dx, &l = dw_first ? dx : dw;
   for (int i = 0; i < 2; ++i) {
@@ -362,7 +394,13 @@ void settle_backward(BackwardPlan* b, int es, int64_t at) {
     }
   }
   b->scratch.planes = at;
-  at += round_up(std::max(b->both.dx.planes_bytes, b->both.dw.planes_bytes), 256);
+  b->scratch.planes_dw = at;
+  if (b->both.tile == TILE_64) {
+    b->scratch.planes_dw += round_up(b->both.dx.planes_bytes, 256);
+    at = b->scratch.planes_dw + round_up(b->both.dw.planes_bytes, 256);
+  } else {
+    at += round_up(std::max(b->both.dx.planes_bytes, b->both.dw.planes_bytes), 256);
+  }
   b->scratch.pack = at;
   if (b->pack.on) {
     lay_out(&b->pack, at, es);
@@ -457,7 +495,8 @@ void product_name(const ProductPlan& pl, char* buf, size_t len) {
 
 void backward_name(const char* call, int dtype, const BackwardPlan& pl, char* buf, size_t len) {
   const char* pack = pl.pack.on ? ".pack" : "";
-  if (pl.both.tile >= 0) {
+  const bool small = pl.both.tile == TILE_64;
+  if (pl.both.tile >= 0 && !small) {
     snprintf(buf, len, "%s.%s.both.tile256x%d%s", call, dtype_name(dtype),
              pl.both.tile == TILE_256 ? 256 : 128, pack);
     return;
@@ -465,7 +504,8 @@ void backward_name(const char* call, int dtype, const BackwardPlan& pl, char* bu
   char dx[48], dw[48];
   product_name(pl.both.dx, dx, sizeof dx);
   product_name(pl.both.dw, dw, sizeof dw);
-  snprintf(buf, len, "%s.%s.dx.%s.dw.%s%s", call, dtype_name(dtype), dx, dw, pack);
+  snprintf(buf, len, "%s.%s.dx.%s.dw.%s%s%s", call, dtype_name(dtype), dx, dw, small ? ".both" : "",
+           pack);
 }
 
 int put(const char* text, char* buf, uint64_t len) {

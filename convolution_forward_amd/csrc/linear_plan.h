@@ -75,7 +75,8 @@ struct BackwardScratch {
   int64_t dz;      // dz [m, dz_ld] (gated: dg and du side by side)
   int64_t dz_ld;   // elements
   int64_t sums;    // column-sum partials
-  int64_t planes;  // split planes (the two products run one after the other)
+  int64_t planes;  // split planes (dw's behind dx's where they run in one launch)
+  int64_t planes_dw;
   int64_t pack;    // packed operands
   int64_t total;
 };
@@ -86,12 +87,12 @@ int linear_validate(const linear_problem* p, int dtype, LinearGeo* g);
 int gated_validate(const gated_problem* p, int dtype, GatedGeo* g);
 
 ProductPlan plan_product(const ProductShape& s, int es);
-// Both products of a backward pass: in one launch of a tile (TILE_256 or
-// TILE_256X128), or one after the other (tile -1).
+// Both products of a backward pass: in one launch of a tile (TILE_256, TILE_256X128,
+// or TILE_64, each with its splits), or one after the other (tile -1).
 struct PairPlan {
   int tile;
   double time;         // estimated, us
-  ProductPlan dx, dw;  // of each alone
+  ProductPlan dx, dw;  // of each alone; for TILE_64 in that launch
 };
 PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es);
 ColsumPlan plan_colsum(int64_t m, int64_t n);

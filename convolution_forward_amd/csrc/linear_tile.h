@@ -218,19 +218,22 @@ struct Ragged {
 // WVR x WVC waves; GATED: P's rows are gate and up rows, side by side within
 // each wave's share.
 template <typename E, bool PT, bool QT, int BR, int BC, int WVR, int WVC, bool DMA, bool GATED>
-__global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const ProductArgs a) {
+struct LinearTile {
+  static constexpr int NT = WVR * WVC * 64;
+  static constexpr int STAGE = lin::Tile<E, BR, PT, NT>::BYTES + lin::Tile<E, BC, QT, NT>::BYTES;
+  // small tiles: buffers for two steps ahead (a step's products are shorter than a
+  // load's way); large ones: two buffers, so that two workgroups fit on a compute unit
+  static constexpr int STAGES = DMA && BR * BC <= 64 * 64 ? 3 : 2;
+  static constexpr int SMEM = STAGES * STAGE;
+
+// id: index of this workgroup among the product's own, after xcd_logical
+static __device__ __forceinline__ void run(const ProductArgs& a, const int id, char* smem) {
   using namespace lin;
-  constexpr int NT = WVR * WVC * 64;
   constexpr int WR = BR / WVR, WC = BC / WVC, NI = WR / 16, NJ = WC / 16;
   constexpr int HW = WR / 2;  // gated: rows of each kind per wave
   using TP = Tile<E, BR, PT, NT>;
   using TQ = Tile<E, BC, QT, NT>;
-  constexpr int STAGE = TP::BYTES + TQ::BYTES;
-  // small tiles: buffers for two steps ahead (a step's products are shorter than a
-  // load's way); large ones: two buffers, so that two workgroups fit on a compute unit
-  constexpr int STAGES = DMA && BR * BC <= 64 * 64 ? 3 : 2;
   static_assert(!GATED || (!PT && !QT), "gated weights are k-major");
-  __shared__ __attribute__((aligned(1024))) char smem[STAGES * STAGE];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -239,7 +242,6 @@ __global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const Produ
   // tile of this workgroup: bands of 8 tiles along c, so that the tiles an XCD
   // runs at one time share few rows of P and Q
   const int per = a.ntr * a.ntc;
-  const int id = xcd_logical(blockIdx.x, gridDim.x);
   const int batch = id / per;  // split * nz + z
   const int z = batch % a.nz, split = batch / a.nz;
   const int idx = id - batch * per;
@@ -507,6 +509,29 @@ __global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const Produ
       finish_linear_runs<E, NR>(a.e, z, c, in, rl, off, whole, v);
     }
   }
+}
+};
+
+template <typename E, bool PT, bool QT, int BR, int BC, int WVR, int WVC, bool DMA, bool GATED>
+__global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const ProductArgs a) {
+  using K = LinearTile<E, PT, QT, BR, BC, WVR, WVC, DMA, GATED>;
+  __shared__ __attribute__((aligned(1024))) char smem[K::SMEM];
+  K::run(a, xcd_logical(blockIdx.x, gridDim.x), smem);
+}
+
+// Both products of a small backward pass in one launch (see linear_pair_kernel), each
+// with its own splits.
+template <typename E, bool DT>
+__global__ __launch_bounds__(256) void linear_tile_pair_kernel(const PairArgs a) {
+  using DX = LinearTile<E, DT, false, 64, 64, 2, 2, true, false>;
+  using DW = LinearTile<E, true, true, 64, 64, 2, 2, true, false>;
+  static_assert(DX::SMEM == DW::SMEM, "one buffer for both");
+  __shared__ __attribute__((aligned(1024))) char smem[DX::SMEM];
+  const bool second = (int)blockIdx.x >= a.first;
+  const int id = second ? xcd_logical(blockIdx.x - a.first, gridDim.x - a.first)
+                        : xcd_logical(blockIdx.x, a.first);
+  if (second != a.dw_first) DW::run(a.dw, id, smem);
+  else DX::run(a.dx, id, smem);
 }
 
 }  // namespace convfwd

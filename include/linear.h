@@ -101,6 +101,7 @@ int gated_backward_scratch_size(const gated_problem* p, int dtype, uint64_t* byt
 /* Name of the kernel plan, e.g. "linear.bf16.tile256x256" or
  * "gated.f16.stream16"; for the backward calls, of both products, in one launch or
  * in two: "linear_backward.bf16.both.tile256x128",
+ * "linear_backward.f32.dx.tile64x64.split4.dw.tile64x64.split4.both",
  * "linear_backward.f32.dx.tile128x128.split2.dw.tile64x64".  CONV_ERR_ARG when
  * len is too small, or the validation status of the problem. */
 int linear_describe_variant(const linear_problem* p, int dtype, char* buf, uint64_t len);
