@@ -189,9 +189,12 @@ __global__ __launch_bounds__(kStreamWaves * 64) void linear_stream_kernel(const 
   }
 }
 
-// Joins the planes of a split contraction in split order: 8 outputs a thread.
+// Joins the planes of a split contraction in split order: 8 outputs a thread, 8
+// planes' loads in flight: a round trip to planes that other XCDs wrote takes about a
+// us, which bounds this.
 template <typename E, bool GATED>
 __device__ __forceinline__ void join(const JoinArgs& a, long long block) {
+  constexpr int KINDS = GATED ? 2 : 1, B = GATED ? 4 : 8;
   const int per_row = (int)(a.plane_ld / 8);
   const long long id = block * 256 + threadIdx.x;
   const long long row = id / per_row;  // z * C + c
@@ -203,20 +206,27 @@ __device__ __forceinline__ void join(const JoinArgs& a, long long block) {
   float v[8], u[8];
 #pragma unroll
   for (int q = 0; q < 8; ++q) v[q] = u[q] = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < a.splits; ++i) {
-    const lin::f32x4 lo = *reinterpret_cast<const lin::f32x4*>(s);
-    const lin::f32x4 hi = *reinterpret_cast<const lin::f32x4*>(s + 4);
+  for (int i = 0; i < a.splits; i += B) {
+    lin::f32x4 lo[KINDS][B], hi[KINDS][B];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) { v[q] += lo[q]; v[4 + q] += hi[q]; }
-    if constexpr (GATED) {
-      const float* t = s + (long long)a.C * a.plane_ld;
-      const lin::f32x4 tl = *reinterpret_cast<const lin::f32x4*>(t);
-      const lin::f32x4 th = *reinterpret_cast<const lin::f32x4*>(t + 4);
+    for (int p = 0; p < B; ++p)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) { u[q] += tl[q]; u[4 + q] += th[q]; }
-    }
-    s += a.plane_stride;
+      for (int d = 0; d < KINDS; ++d) {  // past the last plane: the last one again, not added
+        const float* f = s + min(i + p, a.splits - 1) * a.plane_stride + d * (long long)a.C * a.plane_ld;
+        lo[d][p] = *reinterpret_cast<const lin::f32x4*>(f);
+        hi[d][p] = *reinterpret_cast<const lin::f32x4*>(f + 4);
+      }
+#pragma unroll
+    for (int p = 0; p < B; ++p)
+      if (i + p < a.splits) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[q] += lo[0][p][q];
+          v[4 + q] += hi[0][p][q];
+          u[q] += lo[KINDS - 1][p][q];
+          u[4 + q] += hi[KINDS - 1][p][q];
+        }
+      }
   }
   if (r >= a.e.R) return;
   if constexpr (GATED) finish_gated<E>(a.e, c, r, v, u);

@@ -214,8 +214,11 @@ ProductPlan plan_product(const ProductShape& s, int es) {
   const int64_t plane = plane_ld * s.C * 4 * (s.gated ? 2 : 1) * s.nz;  // bytes of one
   double best = 0.0;
   pl.tile = -1;
-  for (int i = 0; i < count; ++i) {
+  // fewer than two small tiles a compute unit: the large ones would leave most idle
+  const int first = count == 4 && tile_count(s, table[3]) < 2 * kCus ? 2 : 0;
+  for (int i = first; i < count; ++i) {
     const int64_t tiles = tile_count(s, table[i]);
+    double before = 0.0;
     for (int want : kSplits) {
       if (want > 1 && (all / want < 2 || tiles >= 2 * kCus || plane * want > (1LL << 30))) break;
       const int64_t per = ceil_div(all, want), n = ceil_div(all, per);
@@ -224,6 +227,8 @@ ProductPlan plan_product(const ProductShape& s, int es) {
       const double slow = s.pt && es == 2 && !s.aligned ? 1.35 : 1.0;
       double t = slow * time_of(table[i], tiles * n, per);
       if (n > 1) t += kJoin + kJoinByte * (double)(plane * n);
+      if (want > 2 && t > before) break;  // past the best count
+      before = t;
       if (pl.tile < 0 || t < best) {
         best = t;
         pl.tile = table[i].tile;
@@ -269,6 +274,7 @@ PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es) {
   const Tiling& small = es == 4 ? kTiles32[1] : kTiles16[3];
   const int64_t bk = 128 / es, ax = ceil_div(dx.K, bk) * dx.nseg, aw = ceil_div(dw.K, bk) * dw.nseg;
   const int64_t tx = tile_count(dx, small), tw = tile_count(dw, small);
+  double before = 0.0;
   for (int want : kSplits) {
     const int64_t per = ceil_div(std::max(ax, aw), want);
     if (ax < 1 || aw < 1 || tx + tw >= 8 * kCus || (want > 1 && per < 2)) break;
@@ -291,6 +297,8 @@ PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es) {
     if (bytes > (1LL << 30)) break;
     double t = time_of(small, tx * p[0].splits + tw * p[1].splits, per);
     if (bytes > 0) t += kJoin + kJoinByte * (double)bytes;
+    if (want > 2 && t > before) break;  // past the best count
+    before = t;
     if (t < out.time) out = {TILE_64, t, p[0], p[1]};
   }
   if (es != 2) return out;
@@ -307,7 +315,7 @@ PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es) {
     // the least time by which the units, rest of them busy for a round longer, have
     // taken every tile of the last product
     double lo = full * lf + (rest ? lf : 0.0), hi = (full + 1) * lf + (nl / kCus + 2) * ll;
-    for (int k = 0; k < 40; ++k) {
+    for (int k = 0; k < 20; ++k) {
       const double mid = 0.5 * (lo + hi);
       const double taken = (kCus - rest) * std::floor((mid - full * lf) / ll) +
                            rest * std::floor(std::max(0.0, mid - (full + 1) * lf) / ll);
