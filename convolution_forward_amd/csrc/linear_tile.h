@@ -76,11 +76,14 @@ __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
 }
 
-// Unit rotation of the transposed image (see above).
-template <typename E>
+// Unit rotation h of the transposed image (see above): the rows 8g + i, i = 0 .. 3, of
+// two lane groups g are read together, 32 bytes each, and should hit all banks.  Rows
+// of 4 units start in either half of the banks by their parity.
+template <typename E, int UNITS>
 __device__ __forceinline__ int unit_xor(int k) {
-  if constexpr (sizeof(E) == 2) return (k & 3) | (((k >> 3) & 3) << 2);
-  return (k >> 2) & 3;
+  if constexpr (sizeof(E) == 4) return (k >> 2) & 3 & (UNITS - 1);
+  if constexpr (UNITS == 4) return ((k >> 1) & 1) | ((k >> 2) & 2);
+  return ((k & 3) | (((k >> 3) & 3) << 2)) & (UNITS - 1);
 }
 
 // One operand's tile: ROWS rows (r or c) x 128 bytes of k.
@@ -103,7 +106,7 @@ struct Tile {
     const int lr = q / CPR, slot = q % CPR;
     *row = lr;
     if constexpr (T)
-      *piece = (((slot / UNIT) ^ (unit_xor<E>(lr) & (UNITS - 1))) * UNIT) | (slot % UNIT);
+      *piece = (((slot / UNIT) ^ unit_xor<E, UNITS>(lr)) * UNIT) | (slot % UNIT);
     else
       *piece = slot ^ (lr & 7);
   }
@@ -117,7 +120,7 @@ struct Tile {
       return *reinterpret_cast<const Frag*>(base + (row0 + l) * 128 + (((4 * j + g) ^ (l & 7)) << 4));
     } else if constexpr (EB == 2) {
       const int i = l >> 2;
-      const int u = (row0 / 16) ^ ((i | (g << 2)) & (UNITS - 1));
+      const int u = (row0 / 16) ^ unit_xor<E, UNITS>(8 * g + i);
       const char* p = base + (32 * j + 8 * g + i) * ROWB + u * 32 + (l & 3) * 8;
       typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
       const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)const_cast<char*>(p));
