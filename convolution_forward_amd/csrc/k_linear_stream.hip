@@ -15,6 +15,11 @@
 //    the loads of Q, which comes from L2.
 // The next loads are in flight during the products of the present ones.  The
 // partial sums are added in wave and group order through LDS, then the epilogue runs.
+//
+// Measured, weights from memory: one row, 4096 x 4096 bf16 8.3 us (4.0 TB/s); a gated
+// block of 5632 x 2048 10.0 (4.6 TB/s); 32 rows, 8192 x 8192 40 (3.4 TB/s, bound by Q
+// from L2); one row, 1000 x 2048 f16 3.8 (a launch).  Waves that each stream their own
+// range of k were 10 to 35% slower, 16 waves a workgroup slower still.
 #include "linear_tile.h"
 
 namespace convfwd {

@@ -9,10 +9,9 @@
 //    staged in LDS, in two buffers (small tiles: three); the next step (two) is in
 //    flight while one is multiplied.
 //  * DMA: global to LDS directly (16 bytes a lane, no registers), for rows of
-//    whole aligned 16-byte vectors; descriptor range checks give zeros past the
-//    last row and, per lane, past the end of k.  Otherwise (odd strides, sizes or
-//    bases) the vectors are gathered through registers, element by element where
-//    one crosses an end.
+//    whole 16-byte pieces at multiples of 4 bytes; descriptor range checks give
+//    zeros past the last row and, per lane, past the end of k.  Otherwise (odd
+//    strides, sizes or bases) the pieces come through registers (Ragged).
 //  * k-major image in LDS: 128-byte rows, 16-byte piece p of row i kept at slot
 //    p ^ (i & 7): the 16 rows of a fragment read hit all banks.  Transposed
 //    image: one row per k, kept as it lies, in 32-byte units (16 halves) moved to
@@ -21,6 +20,11 @@
 //  * Epilogue from registers: 16 rows c at a time, one a lane, each lane's sums
 //    exchanged into runs of 8 consecutive r (runs_of_8), so that loads and stores
 //    are 16-byte pieces of rows.
+//
+// What bounds it: 128 x 128 the LDS (a wave's 64 x 64 reads 16 KB for 256 cycles of
+// products), 64 x 64 the barrier and the loads' way, float32 the matrix cores.
+// 2048 x 1024 x 1024 bf16 in 64 x 64: 11 us; 4096 x 4096 x 4096 float32 in 128 x 128:
+// 1050 us (131 TFLOP/s of the 157 that the card has).
 #pragma once
 
 #include <hip/hip_runtime.h>
