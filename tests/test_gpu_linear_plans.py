@@ -195,6 +195,28 @@ def test_views_from_odd_elements(m, n, k):
     assert torch.equal(yv, (product64(x, w) + r.double()).to(torch.float16))
 
 
+@pytest.mark.parametrize("kn", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(4, 1000, 264), (300, 304, 200), (3000, 1504, 264),
+                                   (4096, 4096, 520), (8192, 1024, 1096)])
+def test_rows_at_multiples_of_four_bytes(m, n, k, dtype, kn):
+    """Whole pieces in rows that start on multiples of 4 bytes only."""
+    pad, off = (2, 6) if dtype == "f16" else (1, 3)
+    g = gen(m + k)
+    x, w = whole(g, dtype, m, k), whole(g, dtype, *((k, n) if kn else (n, k)))
+    z, dy = whole(g, dtype, m, n), whole(g, dtype, m, n)
+    (_, xv), (_, wv), (_, zv), (_, dyv) = (strided(t, pad, off) for t in (x, w, z, dy))
+    assert torch.equal(forward(dtype, xv, wv, kn=kn), product64(x, w, kn).to(T[dtype]))
+    if m > 4096 or n > 4000:
+        return
+    for act in ("identity", "relu"):
+        d = dy.float() * ((z > 0).float() if act == "relu" else 1.0)
+        dx, dw, _, _ = backward(dtype, xv, wv, zv, dyv, act=act, kn=kn, want="xw")
+        assert torch.equal(dx, (d @ (w.float().t() if kn else w.float())).to(T[dtype]))
+        want = d.t() @ x.float()
+        assert torch.equal(dw, (want.t() if kn else want).to(T[dtype]))
+
+
 def test_plan_rerun_is_bit_identical():
     g = torch.Generator(device="cuda").manual_seed(3)
     for m, n, k in ((4096, 4096, 264), (64, 256, 4096), (2001, 2003, 1031), (16, 1000, 2048)):
