@@ -4,18 +4,15 @@
 //
 //  * Both operands are cut into halves (128 rows of P, BC / 2 of Q).  A wave owns a
 //    part of each half (2 x 4 waves share 256 x 256, 4 x 2 share 256 x 128, so that
-//    parts stay near square): four quadrants of the accumulators, one for each pair
-//    of halves, taken one a phase.
+//    parts stay near square) and takes a step in two phases, a half of P each.
 //  * The waves form two groups of four, one wave of each on every SIMD, half a
-//    phase apart: while one group multiplies a quadrant, the other reads its next
-//    fragments from LDS and issues global loads, and the SIMD's matrix core is fed
-//    by one or the other all the time.
-//  * Quadrants go round: P0 Qf, P0 Qs, P1 Qs, P1 Qf, where f and s change places
-//    every step, so that each phase reads one half and no half is read twice.
-//  * Half tiles live in two LDS buffers.  The half that a phase has read for the
-//    last time is overwritten from the next phase on by the half of two steps
-//    later; seven phases pass between a half's load and its use, so six halves (96
-//    or 72 KB) are in flight and no phase waits for memory in steady state.
+//    phase apart: while one group multiplies, the other reads its next fragments
+//    from LDS and issues global loads, and the SIMD's matrix core is fed by one or
+//    the other all the time.
+//  * Half tiles live in two LDS buffers.  A half that was read for the last time in
+//    a phase is overwritten from the next one on by the half of two steps later;
+//    three phases pass between a half's load and its use, and the loads of a whole
+//    step (64 or 48 KB) are in flight at every turn.
 //  * Gated products: half 0 of P is gate rows, half 1 the same rows of up, and a
 //    wave holds both sums of its outputs.
 //  * The epilogue takes the sums from registers (runs_of_8): 9600 cycles a tile with
@@ -23,12 +20,13 @@
 //    21000 (as much as 9 steps), with erff's GELU 70000.
 //
 // What bounds it: a step of 256 x 256 has 2048 cycles of products on each SIMD and
-// takes 2350 (the turns between the groups); 256 x 128 takes 1500 for 1024, so it is
-// chosen where 256 x 256 would leave units idle.  With the whole card at work the
-// clock falls to 1.8 GHz (2.2 with zeros as operands): 8192 x 4096 x 4096 bf16 198 us
-// (1390 TFLOP/s), with GELU 204; 4096 x 4096 x 4096 96 us.  Measured and not taken:
-// v_mfma 32x32x16 (2 to 5% slower), four waves of 128 x 128 (2730 cycles a step: one
-// wave a SIMD cannot hide its own scalar code), two phases a step (spills).
+// takes about 2300 (the turns between the groups); 256 x 128 takes 1500 for 1024, so
+// it is chosen where 256 x 256 would leave units idle.  With the whole card at work
+// the clock falls to 1.8 GHz (2.2 with zeros as operands): 8192 x 4096 x 4096 bf16 192
+// us (1430 TFLOP/s), with GELU 204; 4096 x 4096 x 4096 96 us.  Measured and not taken:
+// four phases a step (1 to 3% slower), one (256 x 128, transposed operands 10%
+// slower), v_mfma 32x32x16 (2 to 5%), four waves of 128 x 128 (2730 cycles a step: one
+// wave a SIMD cannot hide its own scalar code).
 #pragma once
 
 #include "linear_tile.h"
@@ -52,8 +50,10 @@ struct PingPong {
   // an operand's four half tiles lie side by side, within an LDS instruction's
   // 64 KB offset of one address
   static constexpr int p_at(int half, int buf) { return (2 * buf + half) * TP::BYTES; }
-  static constexpr int q_at(int half, int buf) { return 4 * TP::BYTES + (2 * buf + half) * TQ::BYTES; }
-  static constexpr int FLIGHT = 3 * (TP::ITEMS + TQ::ITEMS);  // six halves
+  static constexpr int q_at(int half, int buf) {
+    return 4 * TP::BYTES + (2 * buf + half) * TQ::BYTES;
+  }
+  static constexpr int LOADS = 2 * (TP::ITEMS + TQ::ITEMS);  // of a step, per wave
 
   // id: index of this workgroup among the product's own, after xcd_logical
   static __device__ __forceinline__ void run(const ProductArgs& a, int id, char* smem) {
@@ -168,33 +168,37 @@ struct PingPong {
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int j2 = 0; j2 < 2; ++j2) p[i][j2] = TP::frag(b, wr * WR + i * 16, j2, lane);
+        for (int j2 = 0; j2 < 2; ++j2)
+          p[i][j2] = TP::frag(b, wr * WR + i * 16, j2, lane);
     };
-    auto read_q = [&](int half, int buf) {
-      const char* b = smem + q_at(half, buf);
+    auto read_q = [&](int buf) {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j2 = 0; j2 < 2; ++j2) q[half][j][j2] = TQ::frag(b, wc * WC + j * 16, j2, lane);
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int j2 = 0; j2 < 2; ++j2)
+            q[h][j][j2] = TQ::frag(smem + q_at(h, buf), wc * WC + j * 16, j2, lane);
     };
-    // end of a phase's reads: they are in registers, and the half that the next
-    // phase reads has arrived for every wave behind the barrier
+    // end of a phase's reads: they are in registers, and what the next phase reads has
+    // arrived for every wave behind the barrier
     auto turn_over = [&] {
       lds_wait();
-      vm_wait<FLIGHT>();
+      vm_wait<LOADS>();
       fence();
       barrier();
       fence();
     };
-    // a quadrant's products; with MOVE the state of the loads moves on between them
-    auto multiply_all = [&](int hp, int hq, auto move) {
+    // the products of a half of P; with MOVE the state of the loads moves on between
+    // them
+    auto multiply_half = [&](int hp, auto move) {
       constexpr bool MOVE = decltype(move)::value;
-      constexpr int N = 2 * NI * NJ, EACH = N / 8;
+      constexpr int N = 4 * NI * NJ, EACH = N / 8;
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const int j2 = n / (NI * NJ), i = n / NJ % NI, j = n % NJ;
-        acc[hp][hq][i][j] = multiply<E>(p[i][j2], q[hq][j][j2], acc[hp][hq][i][j]);
+        const int j2 = n / (2 * NI * NJ), h = n / (NI * NJ) % 2, i = n / NJ % NI, j = n % NJ;
+        acc[hp][h][i][j] = multiply<E>(p[i][j2], q[h][j][j2], acc[hp][h][i][j]);
         if (MOVE && n % EACH == EACH - 1) {
           fence();
           stage(n / EACH);
@@ -208,26 +212,10 @@ struct PingPong {
     };
     constexpr std::integral_constant<bool, false> stay;
     constexpr std::integral_constant<bool, true> move;
-    // one contraction step in buffer F (its parity): halves f = F, s = 1 - F of Q; the
-    // loads are those of two steps later
-    auto step = [&](auto parity) {
-      constexpr int F = decltype(parity)::value, S = 1 - F;
-      read_p(0, F);
-      issue_q(F, F);
-      turn_over();
-      multiply_all(0, F, stay);
-      read_q(S, F);
-      issue_p(0, F);
-      turn_over();
-      multiply_all(0, S, stay);
-      read_p(1, F);
-      issue_q(S, F);
-      turn_over();
-      multiply_all(1, S, stay);
-      read_q(S, S);  // the next step's first half
-      issue_p(1, F);
-      turn_over();
-      multiply_all(1, F, move);
+    auto issue_first = [&](int buf) {  // what the first phase reads
+      issue_q(0, buf);
+      issue_q(1, buf);
+      issue_p(0, buf);
     };
 
 #pragma unroll
@@ -235,27 +223,31 @@ struct PingPong {
       if (n == 1) kk = min(left, 64);
       else stage(n);
     }
+    issue_first(0);
+    issue_p(1, 0);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      issue_q(b, b);
-      issue_p(0, b);
-      issue_q(1 - b, b);
-      issue_p(1, b);
-#pragma unroll
-      for (int n = 0; n < 8; ++n) stage(n);
-    }
-    vm_wait<FLIGHT>();
-    barrier();
-    read_q(0, 0);
-    lds_wait();
-    fence();
+    for (int n = 0; n < 8; ++n) stage(n);
+    issue_first(1);
+    // the first phase's part of the first step has arrived
+    vm_wait<LOADS>();
     barrier();
     const bool late = wave >= 4;
     if (late) barrier();
     fence();
+    auto step = [&](int b) {
+      read_q(b);
+      read_p(0, b);
+      issue_p(1, b ^ 1);  // the next step's
+      turn_over();
+      multiply_half(0, move);
+      read_p(1, b);
+      issue_first(b);  // of two steps later
+      turn_over();
+      multiply_half(1, stay);
+    };
     for (int t = t0; t < t1; t += 2) {  // an odd count ends with a step of zeros
-      step(std::integral_constant<int, 0>());
-      step(std::integral_constant<int, 1>());
+      step(0);
+      step(1);
     }
     if (!late) barrier();
     vm_wait<0>();  // loads past the end (zeros) land before the workgroup's LDS is given up
