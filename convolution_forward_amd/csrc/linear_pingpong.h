@@ -308,9 +308,9 @@ __global__ __launch_bounds__(512) void linear_pingpong_kernel(const ProductArgs 
 // The two products of a backward pass in one launch, the one with the longer
 // contraction first: dx = dz w (DT: w transposed in the sense of linear_tile.h) and
 // dw = dz^T x.  Each alone often fills part of the card's last round of workgroups
-// only; together they fill one another's.  4096 x 4096 x 1024 bf16: 66 us (1040
+// only; together they fill one another's.  4096 x 4096 x 1024 bf16: 63 us (1090
 // TFLOP/s) with 256 x 128 tiles, 107 in two launches; a gated block of 4096 x 5632 x
-// 2048: 285 us (1330 TFLOP/s), 375 in two.
+// 2048: 275 us (1370 TFLOP/s), 375 in two.
 template <typename E, bool DT, int BC>
 __global__ __launch_bounds__(512) void linear_pair_kernel(const PairArgs a) {
   using DX = lin::PingPong<E, DT, false, BC, false, true>;

@@ -63,7 +63,9 @@ __device__ __forceinline__ i32x4 make_rsrc(const char* p, long long bytes) {
 }
 
 // 16 bytes per lane from rsrc + voff to LDS at lds + 16 * lane (out of range:
-// zeros).  Nothing is returned to registers; wait with vm_wait before reading.
+// zeros).  Nothing is returned to registers; wait with vm_wait before reading.  The
+// descriptor comes from scalar code: after a vector instruction that writes one of its
+// registers the load would need five wait states, which the compiler does not know of.
 __device__ __forceinline__ void dma16(i32x4 rsrc, int voff, unsigned lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "s"(lds), "v"(voff), "s"(rsrc) : "memory", "m0");
