@@ -69,12 +69,12 @@ __device__ __forceinline__ float normal_tail_fast(float v) {
   return p * t * __builtin_amdgcn_exp2f(-0.72134752f * a * a);
 }
 
-// GELU, erf form: v Phi(v).  The fast form's limits are inf and -0 at the infinities.
+// GELU, erf form: v Phi(v); inf at infinity and, as the product says, NaN at -infinity.
 template <bool FX>
 __device__ __forceinline__ float gelu_erf(float v) {
   if constexpr (FX) {
-    const float w = fminf(fabsf(v), 1e4f) * normal_tail_fast(v);
-    return v < 0.0f ? -w : v - w;
+    const float h = normal_tail_fast(v);
+    return v < 0.0f ? v * h : v - fminf(v, 1e4f) * h;
   }
   return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
 }
