@@ -25,7 +25,8 @@
  * Element types CONV_F32, CONV_F16, CONV_BF16, one for every operand of a call.
  * Products of 16-bit operands are exact in float32 and every sum is held in
  * float32; z, pg and pu are rounded only where they are stored.  Activations and
- * their slopes are evaluated to within 16 float32 ulps of argument and value.  The backward
+ * their slopes are evaluated to within 16 float32 ulps of argument and value (below
+ * 2^-119 in size they may come out as 0).  The backward
  * passes round dz, dg and du once to the element type (they are operands of
  * matrix products) unless the type is float32; db, dbg and dbu sum the
  * unrounded values.

@@ -1,0 +1,55 @@
+"""GPU accuracy of the activations and slopes of the linear and gated calls
+(include/linear.h) relative to their own size, against 64-bit definitions.
+
+Bounds: 16 float32 ulps of the value and of the argument.  An ulp of y is at most
+2^-23 |y|; an error of 16 ulps in the argument v moves act by 16 * 2^-23 |v act'(v)|
+and a slope by 16 * 2^-23 |v act''(v)|.  Beside that the rounding to the element
+type, and 2^-119 (below it a result may be 0)."""
+import math
+
+import pytest
+
+import convolution_forward_amd as cf
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_linear import T, act64, backward, forward, h
+
+pytestmark = pytest.mark.gpu
+
+ULP = 2.0 ** -23
+FLOOR = {"f32": 2.0 ** -119, "f16": 2.0 ** -25, "bf16": 2.0 ** -119}
+SMOOTH = ["sigmoid", "silu", "gelu", "gelu_tanh"]
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    cf.lib()
+
+
+def within(name, got, want, err):
+    bad = ~((got - want).abs() <= err)
+    if bad.any():
+        i = int(torch.nonzero(bad.flatten())[0])
+        raise AssertionError(f"{name}: {int(bad.sum())} of {bad.numel()}, first {got.flatten()[i].item()} "
+                             f"for {want.flatten()[i].item()}, bound {err.flatten()[i].item():.3g}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("act", SMOOTH)
+def test_relative_to_the_value(act, dtype):
+    """y = act(x) through a product with one, and act'(z) as the gradient of a residual."""
+    v = torch.cat([torch.linspace(-14, 14, 2801), torch.tensor([20.0, -20, 40, -40, 60, -60, 80, -80])])
+    x = v.to(T[dtype]).cuda().view(-1, 1)
+    one = torch.ones(1, 1, dtype=T[dtype], device="cuda")
+    v = x.double().requires_grad_(True)
+    want, slope = act64(v, act)
+    second = torch.autograd.grad(slope.sum(), v)[0]
+    v, want, slope = v.detach(), want.detach(), slope.detach()
+    y = forward(dtype, x, one, act=act).double()
+    within("value", y, want, 16 * ULP * (want.abs() + (v * slope).abs()) + h(dtype) * want.abs() + FLOOR[dtype])
+    d = backward(dtype, x, one, x, torch.ones_like(x), act=act, res="before", want="r")[3].double()
+    within("slope", d, slope,
+           16 * ULP * (slope.abs() + (v * second).abs()) + h(dtype) * slope.abs() + FLOOR[dtype])
