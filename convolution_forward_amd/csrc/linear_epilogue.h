@@ -156,16 +156,12 @@ __device__ __forceinline__ void act_and_slope(float v, float alpha, float beta, 
     *a = v > 0.0f ? v : 0.0f;
     *d = v > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == 2) {
-    if constexpr (FX) {
-      float q, c;
-      logistic_sides<true>(2.0f * v, &q, &c);
-      *a = tanh_fast(v);
-      *d = 4.0f * q * c;
-    } else {
-      const float t = tanhf(v);
-      *a = t;
-      *d = 1.0f - t * t;
-    }
+    // 1 - tanh^2 as 4 sigmoid(2v) sigmoid(-2v): the difference cancels in float32, 3% of
+    // its value at 7.5 and nearly all of it at 9
+    float q, c;
+    logistic_sides<FX>(2.0f * v, &q, &c);
+    *a = FX ? tanh_fast(v) : tanhf(v);
+    *d = 4.0f * q * c;
   } else if constexpr (ACT == 3) {
     float q, c;
     logistic_sides<FX>(v, &q, &c);
