@@ -199,10 +199,11 @@ __device__ __forceinline__ void act_and_slope(float v, float alpha, float beta, 
     *d = cdf + v * pdf;
   } else if constexpr (ACT == 10) {
     // with q = sigmoid(2u): gelu = v q, derivative q + v q (1 - q) 2u'
+    // (q (1 - q) is 0 long before v^2 overflows: the bound keeps 0 times it from NaN)
     float q, c;
     logistic_sides<FX>(1.5957691216057308f * (v + 0.044715f * v * v * v), &q, &c);
     *a = v * q;
-    *d = q + v * q * c * 1.5957691216057308f * (1.0f + 0.134145f * v * v);
+    *d = q + v * (q * c) * 1.5957691216057308f * (1.0f + 0.134145f * fminf(v * v, 1e30f));
   } else {
     *a = v;
     *d = 1.0f;

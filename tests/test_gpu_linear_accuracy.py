@@ -13,7 +13,7 @@ import convolution_forward_amd as cf
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_linear import T, act64, backward, forward, h
+from test_gpu_linear import T, act64, backward, forward, gated_back, h
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,20 @@ def test_relative_to_the_value(act, dtype):
     d = backward(dtype, x, one, x, torch.ones_like(x), act=act, res="before", want="r")[3].double()
     within("slope", d, slope,
            16 * ULP * (slope.abs() + (v * second).abs()) + h(dtype) * slope.abs() + FLOOR[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", SMOOTH)
+def test_slopes_of_huge_arguments(act, dtype):
+    """Arguments whose square or cube overflows float32: every slope is its limit."""
+    v = [s * q for q in (1e10, 7e12, 1e13, 1.8e19, 2e19, 1e25, 3e38) for s in (1, -1)]
+    x = torch.tensor(v, dtype=T[dtype], device="cuda").view(-1, 1)
+    one = torch.ones(1, 1, dtype=T[dtype], device="cuda")
+    want = (x > 0).double() * (0.0 if act in ("tanh", "sigmoid") else 1.0)
+    d = backward(dtype, x, one, x, torch.ones_like(x), act=act, res="before", want="r")[3]
+    assert torch.equal(d.double(), want)
+    # the gate's gradient dg = dh pu act'(pg), as its column sums of one row each
+    for i in range(len(v)):
+        pg = x[i:i + 1].contiguous()
+        dbg = gated_back(dtype, one, one, one, pg, one, one, act=act, want="b")[3]
+        assert float(dbg) == float(want[i]), v[i]
