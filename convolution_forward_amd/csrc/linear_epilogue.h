@@ -107,6 +107,12 @@ __device__ __forceinline__ float gelu_tanh(float v) {
   return v / (1.0f + expf(-u2));
 }
 
+// v between lo and hi; a NaN stays one (fmaxf would drop it).
+__device__ __forceinline__ float bounded(float v, float lo, float hi) {
+  const float t = v < lo ? lo : v;
+  return t > hi ? hi : t;
+}
+
 // Every activation of include/linear.h over a batch: one uniform branch, then 8
 // values at a time (more of them side by side would cost registers).
 template <bool FX, int N>
@@ -124,9 +130,9 @@ __device__ __forceinline__ void lin_act(float (&v)[N], int act, float alpha, flo
     case 2: each([&](float q) { return FX ? tanh_fast(q) : tanhf(q); }); break;
     case 3: each([&](float q) { return act_t<3, FX>(q, alpha, beta); }); break;
     case 4: each([&](float q) { return act_t<4, FX>(q, alpha, beta); }); break;
-    case 5: each([&](float q) { return act_t<5, FX>(q, alpha, beta); }); break;
+    case 5: each([&](float q) { return bounded(alpha * q + beta, 0.0f, 1.0f); }); break;
     case 6: each([&](float q) { return act_t<6, FX>(q, alpha, beta); }); break;
-    case 7: each([&](float q) { return act_t<7, FX>(q, alpha, beta); }); break;
+    case 7: each([&](float q) { return bounded(q, alpha, beta); }); break;
     case 8: each([&](float q) { return act_t<8, FX>(q, alpha, beta); }); break;
     case 9: each([&](float q) { return gelu_erf<FX>(q); }); break;
     case 10: each([&](float q) { return gelu_tanh<FX>(q); }); break;
@@ -174,13 +180,13 @@ __device__ __forceinline__ void act_and_slope(float v, float alpha, float beta, 
     *d = q * (1.0f + v * c);
   } else if constexpr (ACT == 5) {
     const float u = alpha * v + beta;
-    *a = fminf(fmaxf(u, 0.0f), 1.0f);
+    *a = bounded(u, 0.0f, 1.0f);
     *d = u > 0.0f && u < 1.0f ? alpha : 0.0f;
   } else if constexpr (ACT == 6) {
     *a = v * fminf(fmaxf(v * (1.0f / 6.0f) + 0.5f, 0.0f), 1.0f);
     *d = v >= 3.0f ? 1.0f : v <= -3.0f ? 0.0f : v * (1.0f / 3.0f) + 0.5f;
   } else if constexpr (ACT == 7) {
-    *a = fminf(fmaxf(v, alpha), beta);
+    *a = bounded(v, alpha, beta);
     *d = v > alpha && v < beta ? 1.0f : 0.0f;
   } else if constexpr (ACT == 8) {
     *a = v >= 0.0f ? v : alpha * v;

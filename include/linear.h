@@ -58,7 +58,9 @@ extern "C" {
  * gelu v * Phi(v) with the normal distribution function (erf form), and its
  * tanh approximation v/2 * (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))).
  * Derivatives at corners are the flat side's (relu at 0, the ends of clip,
- * hard_sigmoid and hard_swish); leaky_relu's at 0 is 1. */
+ * hard_sigmoid and hard_swish); leaky_relu's at 0 is 1.  A NaN sum stays NaN, but
+ * for relu, whose comparison fails and gives 0; the slopes that are picked by
+ * comparisons are at NaN 0 (relu, clip, hard_sigmoid) and act_alpha (leaky_relu). */
 enum { LINEAR_ACT_GELU = 9, LINEAR_ACT_GELU_TANH = 10 };
 
 enum { LINEAR_W_NK = 0, LINEAR_W_KN = 1 };

@@ -13,7 +13,7 @@ import convolution_forward_amd as cf
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_linear import T, act64, backward, forward, gated_back, h
+from test_gpu_linear import ACTS, T, act64, backward, forward, gated, gated_back, h
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +76,31 @@ def test_slopes_of_huge_arguments(act, dtype):
         pg = x[i:i + 1].contiguous()
         dbg = gated_back(dtype, one, one, one, pg, one, one, act=act, want="b")[3]
         assert float(dbg) == float(want[i]), v[i]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("act", ACTS)
+def test_nan_stays_nan(act, dtype):
+    """A NaN sum is a NaN output of every activation but relu, whose NaN is 0; beside
+    it the other rows are what they are without it."""
+    x = torch.tensor([0.5, math.nan, -0.5], dtype=T[dtype], device="cuda").view(-1, 1)
+    one = torch.ones(1, 1, dtype=T[dtype], device="cuda")
+    y = forward(dtype, x, one, act=act).flatten()
+    hid = gated(dtype, x, one, one, act=act).flatten()
+    nan = act != "relu"
+    assert torch.isnan(y).tolist() == [False, nan, False]
+    assert nan or float(y[1]) == 0.0
+    assert torch.isnan(hid).tolist() == [False, True, False]  # the other factor is NaN too
+    # du = dh act(pg)
+    dbu = gated_back(dtype, one, one, one, x[1:2].contiguous(), one, one, act=act, want="b")[4]
+    assert math.isnan(float(dbu)) == nan
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_clip_of_bounds_and_infinities(dtype):
+    x = torch.tensor([-math.inf, -0.75, -0.0, 1.25, 7.0, math.inf], dtype=T[dtype], device="cuda").view(-1, 1)
+    one = torch.ones(1, 1, dtype=T[dtype], device="cuda")
+    y = forward(dtype, x, one, act="clip").flatten().tolist()
+    assert y == [-0.75, -0.75, 0.0, 1.25, 1.25, 1.25]
+    y = forward(dtype, x, one, act="hard_sigmoid").flatten().tolist()
+    assert y[0] == 0.0 and y[4:] == [1.0, 1.0]
