@@ -95,6 +95,20 @@ JoinArgs join_of(const ProductShape& s, const ProductArgs& a) {
   return j;
 }
 
+// The product's rows c0 .. c0 + rows alone.
+ProductArgs rows_from(const ProductShape& s, ProductArgs a, int64_t c0, int64_t rows, int es) {
+  a.C = (int)std::min(rows, s.C - c0);
+  if (c0 == 0) return a;
+  LinEpilogue& e = a.e;
+  for (int i = 0; i < 2; ++i) {
+    a.Q[i] = at(a.Q[i], s.qt ? c0 : c0 * a.ldq, es);
+    e.out[i] = at(e.out[i], c0 * e.ldo, es);
+    e.save[i] = at(e.save[i], c0 * e.ldsave, es);
+  }
+  e.res = at(e.res, c0 * e.ldres, es);
+  return a;
+}
+
 // Runs one planned product; a's operands and epilogue are set.
 hipError_t run_product(const ProductShape& s, const ProductPlan& pl, int dtype, ProductArgs& a,
                        bool p_padded, bool q_padded, void* planes, hipStream_t st) {
@@ -104,7 +118,10 @@ hipError_t run_product(const ProductShape& s, const ProductPlan& pl, int dtype, 
   if (pl.tile == TILE_STREAM)
     return stream_product(dtype, a, pl.stream_t, pl.stream_rows, s.gated, dma, st);
   const int layout = s.pt ? (s.qt ? 2 : 1) : 0;
-  hipError_t e = product(dtype, a, pl.tile, layout, s.gated, dma, st);
+  const int64_t rows = launch_rows(s, pl.splits);
+  hipError_t e = hipSuccess;
+  for (int64_t c = 0; c < s.C && e == hipSuccess; c += rows)
+    e = product(dtype, rows_from(s, a, c, rows, es), pl.tile, layout, s.gated, dma, st);
   if (e != hipSuccess || pl.splits == 1) return e;
   return join(dtype, join_of(s, a), s.gated, st);
 }
@@ -123,7 +140,9 @@ hipError_t run_both(const BackwardPlan& pl, int dtype, ProductArgs& dx, ProductA
   const int es = (int)dtype_size(dtype);
   void *planes = scratch + pl.scratch.planes, *planes_dw = scratch + pl.scratch.planes_dw;
   if (pl.both.tile < 0 || !direct(pl.dx, dx, es, dx_p_padded, dx_q_padded) ||
-      !direct(pl.dw, dw, es, dw_p_padded, dw_q_padded)) {
+      !direct(pl.dw, dw, es, dw_p_padded, dw_q_padded) ||
+      launch_rows(pl.dx, pl.both.dx.splits) < pl.dx.C ||
+      launch_rows(pl.dw, pl.both.dw.splits) < pl.dw.C) {
     const hipError_t e = run_product(pl.dx, pl.both.dx, dtype, dx, dx_p_padded, dx_q_padded, planes, st);
     if (e != hipSuccess) return e;
     return run_product(pl.dw, pl.both.dw, dtype, dw, dw_p_padded, dw_q_padded, planes_dw, st);

@@ -60,7 +60,7 @@ int64_t stride_of(int64_t ld, int64_t cols) {
 }
 
 // the last element's byte offset stays in int64, and an operand below 2^40
-// elements (beyond the card's memory), which also bounds every grid
+// elements (beyond the card's memory)
 bool offset_ok(int64_t off, int64_t rows, int64_t ld, int es) {
   int64_t e, b;
   if (off < 0) return false;
@@ -266,6 +266,16 @@ ProductPlan plan_product(const ProductShape& s, int es) {
   return pl;
 }
 
+// Counted in tiles of 64 x 64 and 256 threads each, up to 2^30 of them: larger tiles
+// have no more work-items (by a quarter at most, where an odd half tile is left over), and
+// the two products of one launch stay below 2^32 together.  Split products are small
+// (fewer than 8 tiles a compute unit, 2^30 bytes of planes) and never cut.
+int64_t launch_rows(const ProductShape& s, int splits) {
+  const int64_t across = ceil_div(s.gated ? 2 * s.R : s.R, 64) * s.nz * splits;
+  const int64_t rows = 64 * ((1LL << 30) / 256 / across) / 256 * 256;
+  return std::min<int64_t>(std::max<int64_t>(rows, 256), 1LL << 30);
+}
+
 PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es) {
   PairPlan out{-1, 0.0, plan_product(dx, es), plan_product(dw, es)};
   out.time = out.dx.time + out.dw.time;
@@ -361,6 +371,9 @@ double lay_out(Packing* k, int64_t at, int es) {
   return 4.0 + bytes / 4e6;  // a launch, 4 TB/s
 }
 
+// Whether one launch can copy them: 2^33 pieces of 16 bytes are 2^31 work-items.
+bool pack_fits(const Packing& k) { return k.bytes <= (1LL << 37); }
+
 bool any_needed(const Packing& k) {
   for (int i = 0; i < k.n; ++i)
     if (k.item[i].need) return true;
@@ -375,7 +388,7 @@ int64_t settle(ProductShape* s, ProductPlan* run, Packing* k, int es, int64_t* t
     ProductShape t = *s;
     t.aligned = true;
     const ProductPlan packed = plan_product(t, es);
-    if (packed.tile != TILE_STREAM && packed.time + lay_out(k, 0, es) < pl.time) {
+    if (packed.tile != TILE_STREAM && packed.time + lay_out(k, 0, es) < pl.time && pack_fits(*k)) {
       k->on = true;
       *s = t;
       pl = packed;
@@ -394,7 +407,7 @@ void settle_backward(BackwardPlan* b, int es, int64_t at) {
     ProductShape x = b->dx, w = b->dw;
     x.aligned = w.aligned = true;
     const PairPlan packed = plan_pair(x, w, es);
-    if (packed.time + lay_out(&b->pack, 0, es) < b->both.time) {
+    if (packed.time + lay_out(&b->pack, 0, es) < b->both.time && pack_fits(b->pack)) {
       b->pack.on = true;
       b->dx = x;
       b->dw = w;

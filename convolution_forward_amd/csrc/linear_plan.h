@@ -87,6 +87,9 @@ int linear_validate(const linear_problem* p, int dtype, LinearGeo* g);
 int gated_validate(const gated_problem* p, int dtype, GatedGeo* g);
 
 ProductPlan plan_product(const ProductShape& s, int es);
+// Rows c that one launch may take (a multiple of 256): a launch holds fewer than 2^32
+// work-items, and the kernels count rows in 32 bits.  More run one launch after the other.
+int64_t launch_rows(const ProductShape& s, int splits);
 // Both products of a backward pass: in one launch of a tile (TILE_256, TILE_256X128,
 // or TILE_64, each with its splits), or one after the other (tile -1).
 struct PairPlan {
