@@ -96,32 +96,31 @@ __device__ __forceinline__ int entry_of(const ClipArgs<N>& a, int chunk) {
   return lo;
 }
 
-// f(vector index) over whole vectors of [0, n), 4 loads in flight; then scalars.
+// |g|^p of a chunk: whole vectors from any element's address on, 4 loads in flight, then
+// the last elements.  Which thread and sum an element joins does not depend on the
+// address, so neither does the norm.
 template <typename E, int KIND>
 __device__ __forceinline__ void chunk_power(const E* g, int n, double (&s)[4]) {
   using V = VecOf<E>;
-  int done = 0;
-  if (reinterpret_cast<unsigned long long>(g) % 16 == 0) {
-    const typename V::type* v = reinterpret_cast<const typename V::type*>(g);
-    const int nv = n / V::N;
-    done = nv * V::N;
-    int i = threadIdx.x;
-    for (; i + 768 < nv; i += 1024) {
-      typename V::type q[4];
+  struct __attribute__((packed, aligned(sizeof(E)))) Any { typename V::type v; };
+  const Any* v = reinterpret_cast<const Any*>(g);
+  const int nv = n / V::N;
+  int i = threadIdx.x;
+  for (; i + 768 < nv; i += 1024) {
+    typename V::type q[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) q[u] = v[i + 256 * u];
+    for (int u = 0; u < 4; ++u) q[u] = v[i + 256 * u].v;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int e = 0; e < V::N; ++e) add_power(s[u], (float)q[u][e], KIND);
-    }
-    for (; i < nv; i += 256) {
-      const typename V::type q = v[i];
-#pragma unroll
-      for (int e = 0; e < V::N; ++e) add_power(s[0], (float)q[e], KIND);
-    }
+      for (int e = 0; e < V::N; ++e) add_power(s[u], (float)q[u][e], KIND);
   }
-  for (int i = done + threadIdx.x; i < n; i += 256) add_power(s[0], (float)g[i], KIND);
+  for (; i < nv; i += 256) {
+    const typename V::type q = v[i].v;
+#pragma unroll
+    for (int e = 0; e < V::N; ++e) add_power(s[0], (float)q[e], KIND);
+  }
+  for (int j = nv * V::N + threadIdx.x; j < n; j += 256) add_power(s[0], (float)g[j], KIND);
 }
 
 template <int KIND, int N>

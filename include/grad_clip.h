@@ -10,7 +10,7 @@
  *
  * The sums run in float64 over exact squares (the square of a float32 has at most
  * 48 significant bits and its exponent fits), in an order that depends on the
- * lengths alone: no atomics, reruns are bit-identical.  An infinite element gives
+ * lengths and types alone: no atomics, reruns are bit-identical.  An infinite element gives
  * an infinite norm and c = 0, so finite elements become 0 and infinite ones NaN;
  * a NaN makes the norm and every element NaN (for every p).
  *
