@@ -266,7 +266,8 @@ hipError_t stream_g(const ProductArgs& a, bool vec, hipStream_t s) {
 
 template <typename E, int TC, bool GATED>
 hipError_t stream_t(const ProductArgs& a, int rows, bool vec, hipStream_t s) {
-  if (rows == 32) return stream_g<E, TC, GATED, 1, 2>(a, vec, s);
+  if constexpr (TC == 2)  // 32 weight rows share Q's loads, which 16 rows c do not need
+    if (rows == 32) return stream_g<E, TC, GATED, 1, 2>(a, vec, s);
   if (rows == 16) return stream_g<E, TC, GATED, 1, 1>(a, vec, s);
   if (rows == 8) return stream_g<E, TC, GATED, 2, 1>(a, vec, s);
   return stream_g<E, TC, GATED, 4, 1>(a, vec, s);

@@ -501,7 +501,7 @@ namespace {
 
 void product_name(const ProductPlan& pl, char* buf, size_t len) {
   if (pl.tile == TILE_STREAM) {
-    snprintf(buf, len, "stream%d", 16 * pl.stream_t);
+    snprintf(buf, len, "stream%d.r%d", 16 * pl.stream_t, pl.stream_rows);
     return;
   }
   const char* tile = pl.tile == TILE_256       ? "tile256x256"

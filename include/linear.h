@@ -103,8 +103,9 @@ int gated_scratch_size(const gated_problem* p, int dtype, uint64_t* bytes);
 int gated_backward_scratch_size(const gated_problem* p, int dtype, uint64_t* bytes);
 
 /* Name of the kernel plan, e.g. "linear.bf16.tile256x256" or
- * "gated.f16.stream16"; for the backward calls, of both products, in one launch or
- * in two: "linear_backward.bf16.both.tile256x128",
+ * "gated.f16.stream16.r8" (streamed, for up to 16 rows, 8 weight rows a workgroup);
+ * for the backward calls, of both products, in one launch or in two:
+ * "linear_backward.bf16.both.tile256x128",
  * "linear_backward.f32.dx.tile64x64.split4.dw.tile64x64.split4.both",
  * "linear_backward.f32.dx.tile128x128.split2.dw.tile64x64".  CONV_ERR_ARG when
  * len is too small, or the validation status of the problem. */
