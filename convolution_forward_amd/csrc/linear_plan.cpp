@@ -277,7 +277,8 @@ int64_t launch_rows(const ProductShape& s, int splits) {
 }
 
 PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es) {
-  PairPlan out{-1, 0.0, plan_product(dx, es), plan_product(dw, es)};
+  const ProductPlan alone_x = plan_product(dx, es), alone_w = plan_product(dw, es);
+  PairPlan out{-1, 0.0, alone_x, alone_w};
   out.time = out.dx.time + out.dw.time;
   if (!dx.aligned || !dw.aligned) return out;
   // small tiles: the contractions of both cut into pieces of one length
@@ -331,10 +332,7 @@ PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es) {
                            rest * std::floor(std::max(0.0, mid - (full + 1) * lf) / ll);
       (taken >= (double)nl ? hi : lo) = mid;
     }
-    if (t.fixed + hi < out.time) {
-      out.tile = t.tile;
-      out.time = t.fixed + hi;
-    }
+    if (t.fixed + hi < out.time) out = {t.tile, t.fixed + hi, alone_x, alone_w};
   }
   return out;
 }
