@@ -125,7 +125,7 @@ __global__ __launch_bounds__(256) void linear_sums_kernel(const SumsArgs a) {
 // Operands with odd rows, copied so that the products can load them to LDS directly:
 // a thread moves 16-byte pieces, the last one of a row loaded from further back and
 // shifted.  Bound by memory: every element is read and written once (two operands of
-// 1531 x 1001 and 777 x 1531 f16 in 5.5 us, most of it the launch).
+// 1531 x 1001 and 777 x 1531 f16 in 5.7 us, most of it the launch).
 template <typename E>
 __global__ __launch_bounds__(256) void linear_pack_kernel(const PackArgs a) {
   constexpr int EPC = 16 / (int)sizeof(E), PER = 4;

@@ -16,10 +16,16 @@
 // The next loads are in flight during the products of the present ones.  The
 // partial sums are added in wave and group order through LDS, then the epilogue runs.
 //
-// Measured, weights from memory: one row, 4096 x 4096 bf16 8.3 us (4.0 TB/s); a gated
-// block of 5632 x 2048 10.0 (4.6 TB/s); 32 rows, 8192 x 8192 40 (3.4 TB/s, bound by Q
-// from L2); one row, 1000 x 2048 f16 3.8 (a launch).  Waves that each stream their own
+// Measured, weights from memory: one row, bf16 4096 x 4096 8.5 us (4.0 TB/s), 8192 x 4096
+// 13.5 (5.0), 32000 x 4096 43 (6.1); a gated block of 5632 x 2048 10.1 (4.6 TB/s); 32 rows,
+// 8192 x 4096 22 (3.0 TB/s, bound by Q from L2; 64 x 64 tiles in 4 splits take 19); one row,
+// 1000 x 2048 f16 4.2 (a launch).  Waves that each stream their own
 // range of k were 10 to 35% slower, 16 waves a workgroup slower still.
+//
+// The gated kernel of 17 to 32 rows c with 4 weight rows holds 16 pieces of Q twice over
+// and spills (60 registers of aligned 16-bit operands, 382 of odd ones, 69 and 135 of
+// float32).  24 rows, f 1024: k 2048 f16 7.5 us for 8.1 with 8 weight rows, but k 2047 24
+// for 10, and float32 24 for 16: the plan does not know of that.
 #include "linear_tile.h"
 
 namespace convfwd {

@@ -55,8 +55,9 @@ __device__ __forceinline__ void store8(E* p, int nv, const float (&v)[8]) {
 // Phi(-|v|), the normal distribution function's tail, from erfc(x) = e^(-x^2) t P(t)
 // with t = 1 / (1 + 0.38 x), x = |v| / sqrt 2; P's coefficients are a fit of least
 // relative error (1.04e-6 for x in [0, 13], far into the tail), halved.  Together
-// with the hardware's exp2 and reciprocal within 3e-6 of the value, below a 16-bit
-// output's rounding; 14 operations for erff's 40 and more.
+// with the hardware's exp2 and reciprocal within 2e-6 of the value up to |v| = 4 and,
+// by the rounding of the exponent, 4e-6 at 6 and 8e-6 at 13: below a 16-bit output's
+// rounding.  14 operations for erff's 40 and more.
 __device__ __forceinline__ float normal_tail_fast(float v) {
   const float a = fabsf(v), t = __builtin_amdgcn_rcpf(fmaf(0.26870058f, a, 1.0f));
   float p = -0.0627085285f;

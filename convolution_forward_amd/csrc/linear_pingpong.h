@@ -15,15 +15,18 @@
 //    step (64 or 48 KB) are in flight at every turn.
 //  * Gated products: half 0 of P is gate rows, half 1 the same rows of up, and a
 //    wave holds both sums of its outputs.
-//  * The epilogue takes the sums from registers (runs_of_8): 9600 cycles a tile with
-//    no activation, 22800 with GELU.  A trip through LDS, 16 rows at a time, took
-//    21000 (as much as 9 steps), with erff's GELU 70000.
+//  * The epilogue takes the sums from registers (runs_of_8): 9500 cycles a tile with
+//    no activation, 24000 with GELU, beside which nothing multiplies (6 and 14% of a
+//    tile with k = 4096).  A trip through LDS, 16 rows at a time, took 21000 (as much
+//    as 9 steps), with erff's GELU 70000.
 //
 // What bounds it: a step of 256 x 256 has 2048 cycles of products on each SIMD and
-// takes about 2300 (the turns between the groups); 256 x 128 takes 1500 for 1024, so
-// it is chosen where 256 x 256 would leave units idle.  With the whole card at work
-// the clock falls to 1.8 GHz (2.2 with zeros as operands): 8192 x 4096 x 4096 bf16 192
-// us (1430 TFLOP/s), with GELU 204; 4096 x 4096 x 4096 96 us.  Measured and not taken:
+// takes 2360 (the turns between the groups); 256 x 128 takes 1500 for 1024, so it is
+// chosen where 256 x 256 would leave units idle.  With the start (3800 cycles) and the
+// epilogue the matrix cores are busy for 73% of a tile of k = 4096 with GELU, 80%
+// without.  With the whole card at work the clock falls to 1.8 GHz (2.2 with zeros as
+// operands): 8192 x 4096 x 4096 bf16 194 to 201 us (1370 to 1420 TFLOP/s), with GELU 207
+// to 216; 4096 x 4096 x 4096 97 us.  Measured and not taken:
 // four phases a step (1 to 3% slower), one (256 x 128, transposed operands 10%
 // slower), v_mfma 32x32x16 (2 to 5%), four waves of 128 x 128 (2730 cycles a step: one
 // wave a SIMD cannot hide its own scalar code).
@@ -308,9 +311,9 @@ __global__ __launch_bounds__(512) void linear_pingpong_kernel(const ProductArgs 
 // The two products of a backward pass in one launch, the one with the longer
 // contraction first: dx = dz w (DT: w transposed in the sense of linear_tile.h) and
 // dw = dz^T x.  Each alone often fills part of the card's last round of workgroups
-// only; together they fill one another's.  4096 x 4096 x 1024 bf16: 63 us (1090
+// only; together they fill one another's.  4096 x 4096 x 1024 bf16: 61 us (1120
 // TFLOP/s) with 256 x 128 tiles, 107 in two launches; a gated block of 4096 x 5632 x
-// 2048: 275 us (1370 TFLOP/s), 375 in two.
+// 2048: 277 us (1360 TFLOP/s), 375 in two.
 template <typename E, bool DT, int BC>
 __global__ __launch_bounds__(512) void linear_pair_kernel(const PairArgs a) {
   using DX = lin::PingPong<E, DT, false, BC, false, true>;

@@ -165,9 +165,15 @@ namespace {
 // without a step, of every further round's start and epilogue, and of a contraction
 // step (128 bytes of k): step, plus busy by the share of the units at work (the card
 // lowers its clock as they fill), plus more for every further workgroup on a unit,
-// up to units of them.  Fitted to 1300 timings of m 48 .. 8192, n and k 256 .. 4096
-// with 1 to 16 splits: off by 10% (root mean square), and the choice by it costs 1.8%
-// more than the best on average, 16% at most.
+// up to units of them.  Fitted to timings of m 48 .. 8192, n and k 256 .. 4096 with 1 to
+// 16 splits (of the two large tiles, before their steps had two phases).  Checked
+// with 1300 timings of the present kernels at those sizes: the choice by it costs 1.1%
+// more than the best of them on average, more than 10% at 6 of 135 sizes, 14% at most
+// (4096 x 1024 x 256 bf16: 10.1 us for 8.8).
+// It has no term for memory, and promises few rows with more weights than were fitted
+// more than memory gives: one row, bf16 8192 x 4096 runs 64 x 64 tiles in 8 splits (19
+// us) where the streamed kernel takes 13.5, gated 11008 x 4096 45 for 33; at 32 rows the
+// tiles are the faster ones (19 for 22, 42 for 51).
 struct Tiling {
   int tile, r, c, units;
   double fixed, round, step, busy, more;
@@ -222,8 +228,8 @@ ProductPlan plan_product(const ProductShape& s, int es) {
     for (int want : kSplits) {
       if (want > 1 && (all / want < 2 || tiles >= 2 * kCus || plane * want > (1LL << 30))) break;
       const int64_t per = ceil_div(all, want), n = ceil_div(all, per);
-      // a transposed operand that is gathered costs a third more (777 x 1001 x 1531: 21
-      // us for 16)
+      // a transposed operand that is gathered costs a third more (777 x 1001 x 1531, the
+      // one size that was timed: 21 us for 16)
       const double slow = s.pt && es == 2 && !s.aligned ? 1.35 : 1.0;
       double t = slow * time_of(table[i], tiles * n, per);
       if (n > 1) t += kJoin + kJoinByte * (double)(plane * n);
@@ -241,7 +247,8 @@ ProductPlan plan_product(const ProductShape& s, int es) {
     // the streamed kernel: on every compute unit the bytes of its weight rows, of Q
     // (from L2, 0.8 of a weight row's time) and a workgroup's start (4 rows' time), at
     // 30 KB a us (float32, bound by its products as well: 26; 16-bit rows from odd
-    // elements on: 21); within 15% of 8 timings from 4 to 180 MB of weights
+    // elements on: 21).  Of 36 timings of bf16, 34 to 262 MB of weights, 14% below to
+    // 21% above: it overrates what 16 and more rows of Q cost
     const double rate = es == 4 ? 26e3 : s.aligned ? 30e3 : 21e3;
     for (int rows = s.C > 16 ? 32 : 16; rows >= 4; rows /= 2) {
       const int64_t groups = ceil_div(s.R, rows);

@@ -4,9 +4,9 @@
  *
  *   norm = (sum over all tensors and elements of |g|^p)^(1/p), p = 1 or 2, or the
  *          largest |g| (infinity norm);
- *   c    = min(1, max_norm / (norm + eps)), rounded to float32, NaN if the norm is
- *          NaN;
- *   out  = fl(c * g), rounded once to the tensor's type.
+ *   c    = min(1, max_norm / (norm + eps)), rounded to float32, NaN if the quotient
+ *          is (the norm NaN, 0 / 0 or infinity / infinity);
+ *   out  = c * g in float32, rounded to the tensor's type.
  *
  * The sums run in float64 over exact squares (the square of a float32 has at most
  * 48 significant bits and its exponent fits), in an order that depends on the
