@@ -4,7 +4,8 @@ Argument marshalling only: every step of the computation runs in the HIP
 kernels behind the C ABI declared in include/conv.h.  The names mirror the C
 calls (conv_output_extent, conv_resolve_auto_pad, conv_scratch_size,
 conv_describe_variant, conv_forward, conv_transpose_forward; the linear, gated
-and grad_clip calls of include/linear.h and include/grad_clip.h).  Loading fails
+and grad_clip calls of include/linear.h and include/grad_clip.h; layer_norm, dropout,
+quantize_rows and linear_int8 of the headers of those names).  Loading fails
 loudly when the native library has not been built; there is no fallback.
 
 Operands are device pointers (ints) or objects with a ``data_ptr()`` method
@@ -48,6 +49,12 @@ EXPORTS = (
     "gated_describe_variant", "gated_backward_describe_variant", "gated_check",
     "gated_backward_check", "gated_forward", "gated_backward",
     "grad_clip_scratch_size", "grad_clip_check", "grad_clip",
+    "layer_norm_scratch_size", "layer_norm_backward_scratch_size", "layer_norm_describe_variant",
+    "layer_norm_backward_describe_variant", "layer_norm_check", "layer_norm_backward_check",
+    "layer_norm_forward", "layer_norm_backward", "dropout_describe_variant", "dropout_check",
+    "dropout_backward_check", "dropout_forward", "dropout_backward", "quantize_check",
+    "quantize_rows", "linear_int8_scratch_size", "linear_int8_describe_variant",
+    "linear_int8_check", "linear_int8_forward",
 )
 
 
@@ -122,6 +129,45 @@ class grad_clip_problem(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class layer_norm_problem(ctypes.Structure):
+    """Mirror of struct layer_norm_problem in include/layer_norm.h (same field order)."""
+
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "m", "n", "ldx", "ldr", "ldy", "lds", "ldds", "lddx", "lddr",
+        "x_off", "r_off", "w_off", "b_off", "y_off", "s_off",
+        "dy_off", "ds_off", "dx_off", "dr_off", "dw_off", "db_off")] + [
+        ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("eps", ctypes.c_float),
+        ("drop", ctypes.c_float), ("has_weight", ctypes.c_int32), ("has_bias", ctypes.c_int32),
+        ("has_residual", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class dropout_problem(ctypes.Structure):
+    """Mirror of struct dropout_problem in include/dropout.h (same field order)."""
+
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "m", "n", "ldx", "ldr", "ldy", "x_off", "r_off", "y_off")] + [
+        ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("drop", ctypes.c_float),
+        ("has_residual", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class quantize_problem(ctypes.Structure):
+    """Mirror of struct quantize_problem in include/linear_int8.h (same field order)."""
+
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "m", "n", "ldx", "ldq", "x_off", "q_off", "scale_off")] + [("reserved", ctypes.c_int32)]
+
+
+class linear_int8_problem(ctypes.Structure):
+    """Mirror of struct linear_int8_problem in include/linear_int8.h (same field order)."""
+
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "m", "n", "k", "ldx", "ldw", "ldr", "ldy",
+        "x_off", "xs_off", "w_off", "ws_off", "b_off", "r_off", "y_off")] + [
+        ("activation", ctypes.c_int32), ("act_alpha", ctypes.c_float),
+        ("act_beta", ctypes.c_float), ("has_bias", ctypes.c_int32),
+        ("has_residual", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 POOL_KINDS = {"max": 0, "average": 1, "global_max": 2, "global_average": 3}
 
 _lib = None
@@ -175,6 +221,24 @@ def lib():
         L.grad_clip_scratch_size.argtypes = [CP, u64p]
         L.grad_clip_check.argtypes = [CP, vp, vp, ctypes.c_uint64]
         L.grad_clip.argtypes = [CP, vp, vp, ctypes.c_uint64, vp]
+        NP, DP, QP, IP = (ctypes.POINTER(t) for t in (layer_norm_problem, dropout_problem,
+                                                      quantize_problem, linear_int8_problem))
+        i32, u64 = ctypes.c_int, ctypes.c_uint64
+        for name, Q in (("layer_norm", NP), ("layer_norm_backward", NP), ("linear_int8", IP)):
+            getattr(L, name + "_scratch_size").argtypes = [Q, i32, u64p]
+        for name, Q in (("layer_norm", NP), ("layer_norm_backward", NP), ("dropout", DP),
+                        ("linear_int8", IP)):
+            getattr(L, name + "_describe_variant").argtypes = [Q, i32, ctypes.c_char_p, u64]
+        for check, run, Q, n in (("layer_norm_check", "layer_norm_forward", NP, 10),
+                                 ("layer_norm_backward_check", "layer_norm_backward", NP, 12),
+                                 ("linear_int8_check", "linear_int8_forward", IP, 8)):
+            getattr(L, check).argtypes = [Q, i32] + [vp] * n + [u64]
+            getattr(L, run).argtypes = [Q, i32] + [vp] * n + [u64, vp]
+        for check, run, Q, n in (("dropout_check", "dropout_forward", DP, 4),
+                                 ("dropout_backward_check", "dropout_backward", DP, 3),
+                                 ("quantize_check", "quantize_rows", QP, 3)):
+            getattr(L, check).argtypes = [Q, i32] + [vp] * n
+            getattr(L, run).argtypes = [Q, i32] + [vp] * n + [vp]
         L.conv_status_string.argtypes = [ctypes.c_int]
         L.conv_status_string.restype = ctypes.c_char_p
         for name in EXPORTS:
@@ -584,3 +648,172 @@ def grad_clip(p: grad_clip_problem, norm, scratch=None, scratch_bytes=0, stream=
     if check and st:
         raise ConvError(st, "grad_clip")
     return st
+
+
+# ------------------------------------------------------------- layer norm, dropout
+
+def make_layer_norm_problem(m, n, *, eps=1e-5, weight=True, bias=True, residual=False, drop=0.0,
+                            seed=0, offset=0, ldx=0, ldr=0, ldy=0, lds=0, ldds=0, lddx=0, lddr=0,
+                            offsets=(0,) * 6, grad_offsets=(0,) * 6) -> layer_norm_problem:
+    """A layer_norm_problem: s = r + drop(x), y = (s - mean) / sqrt(var + eps) * w + b.
+
+    drop: probability of a zero (0: no dropout), its mask from seed and offset;
+    ld*: row strides in elements (0 = dense); offsets: x, r, w, b, y, s;
+    grad_offsets: dy, ds, dx, dr, dw, db.
+    """
+    return layer_norm_problem(m, n, ldx, ldr, ldy, lds, ldds, lddx, lddr, *offsets, *grad_offsets,
+                              _u64(seed), _u64(offset), eps, drop, int(weight), int(bias),
+                              int(residual), 0)
+
+
+def make_dropout_problem(m, n, drop, *, seed=0, offset=0, residual=False, ldx=0, ldr=0, ldy=0,
+                         offsets=(0, 0, 0)) -> dropout_problem:
+    """A dropout_problem: y = [r +] (x / (1 - drop) where kept, 0 elsewhere).
+
+    ldx, ldy and the offsets of x and y are also dx's and dy's; offsets: x, r, y.
+    """
+    return dropout_problem(m, n, ldx, ldr, ldy, *offsets, _u64(seed), _u64(offset), drop,
+                           int(residual), 0)
+
+
+def _u64(v):
+    if not 0 <= v < 1 << 64:
+        raise ValueError(f"{v} is no unsigned 64-bit number")
+    return v
+
+
+def layer_norm_scratch_size(p: layer_norm_problem, dtype) -> int:
+    return _size("layer_norm_scratch_size", p, _dt(dtype))
+
+
+def layer_norm_backward_scratch_size(p: layer_norm_problem, dtype) -> int:
+    return _size("layer_norm_backward_scratch_size", p, _dt(dtype))
+
+
+def layer_norm_describe_variant(p: layer_norm_problem, dtype) -> str:
+    return _describe("layer_norm_describe_variant", p, dtype)
+
+
+def layer_norm_backward_describe_variant(p: layer_norm_problem, dtype) -> str:
+    return _describe("layer_norm_backward_describe_variant", p, dtype)
+
+
+def layer_norm_check(p, dtype, x, r, w, b, y, s=None, mean=None, rstd=None, step=None,
+                     scratch=None, scratch_bytes=0) -> int:
+    """Status layer_norm_forward would return before enqueueing (host only)."""
+    return lib().layer_norm_check(ctypes.byref(p), _dt(dtype),
+                                  *map(_ptr, (x, r, w, b, y, s, mean, rstd, step, scratch)),
+                                  int(scratch_bytes))
+
+
+def layer_norm_backward_check(p, dtype, s, w, mean, rstd, dy, ds, dx, dr, dw, db, step=None,
+                              scratch=None, scratch_bytes=0) -> int:
+    return lib().layer_norm_backward_check(
+        ctypes.byref(p), _dt(dtype),
+        *map(_ptr, (s, w, mean, rstd, dy, ds, dx, dr, dw, db, step, scratch)), int(scratch_bytes))
+
+
+def layer_norm_forward(p, dtype, x, r, w, b, y, s=None, mean=None, rstd=None, step=None,
+                       scratch=None, scratch_bytes=0, stream=None, check=True) -> int:
+    """Enqueue the layer norm on `stream`; s, mean and rstd receive what the backward
+    pass reads where they are given; step: a device uint64 added to the mask's offset."""
+    return _run("layer_norm_forward", p, dtype, (x, r, w, b, y, s, mean, rstd, step), scratch,
+                scratch_bytes, stream, check)
+
+
+def layer_norm_backward(p, dtype, s, w, mean, rstd, dy, ds, dx, dr, dw, db, step=None,
+                        scratch=None, scratch_bytes=0, stream=None, check=True) -> int:
+    """Enqueue the gradients of the layer norm (and of the dropout and the residual
+    before it); ds is added to the gradient of s; those passed as None are not computed."""
+    return _run("layer_norm_backward", p, dtype,
+                (s, w, mean, rstd, dy, ds, dx, dr, dw, db, step), scratch, scratch_bytes, stream,
+                check)
+
+
+def _enqueue(name, p, dtype, operands, stream, check):
+    st = getattr(_lib or lib(), name)(
+        ctypes.byref(p), DTYPES[dtype] if isinstance(dtype, str) else int(dtype),
+        *[t if t is None or isinstance(t, int) else t.data_ptr() for t in operands],
+        stream or None)
+    if check and st:
+        raise ConvError(st, name)
+    return st
+
+
+def dropout_describe_variant(p: dropout_problem, dtype) -> str:
+    return _describe("dropout_describe_variant", p, dtype)
+
+
+def dropout_check(p, dtype, x, r, y, step=None) -> int:
+    """Status dropout_forward would return before enqueueing (host only)."""
+    return lib().dropout_check(ctypes.byref(p), _dt(dtype), *map(_ptr, (x, r, y, step)))
+
+
+def dropout_backward_check(p, dtype, dy, dx, step=None) -> int:
+    return lib().dropout_backward_check(ctypes.byref(p), _dt(dtype), *map(_ptr, (dy, dx, step)))
+
+
+def dropout_forward(p, dtype, x, r, y, step=None, stream=None, check=True) -> int:
+    """Enqueue the dropout on `stream`; step: a device uint64 added to the offset."""
+    return _enqueue("dropout_forward", p, dtype, (x, r, y, step), stream, check)
+
+
+def dropout_backward(p, dtype, dy, dx, step=None, stream=None, check=True) -> int:
+    """Enqueue the gradient of the dropout's input; step as the forward saw it."""
+    return _enqueue("dropout_backward", p, dtype, (dy, dx, step), stream, check)
+
+
+# -------------------------------------------------------- linear layer in 8 bits
+
+def make_quantize_problem(m, n, *, ldx=0, ldq=0, offsets=(0, 0, 0)) -> quantize_problem:
+    """A quantize_problem: rows of x [m, n] to int8 with a float32 scale each; offsets:
+    x, q, scale."""
+    return quantize_problem(m, n, ldx, ldq, *offsets, 0)
+
+
+def quantize_check(p: quantize_problem, dtype, x, q, scale) -> int:
+    """Status quantize_rows would return before enqueueing (host only)."""
+    return lib().quantize_check(ctypes.byref(p), _dt(dtype), *map(_ptr, (x, q, scale)))
+
+
+def quantize_rows(p: quantize_problem, dtype, x, q, scale, stream=None, check=True) -> int:
+    """Enqueue the quantization of x's rows on `stream`."""
+    return _enqueue("quantize_rows", p, dtype, (x, q, scale), stream, check)
+
+
+def make_linear_int8_problem(m, n, k, *, act="identity", alpha=None, beta=None, bias=False,
+                             residual="none", ldx=0, ldw=0, ldr=0, ldy=0,
+                             offsets=(0,) * 7) -> linear_int8_problem:
+    """A linear_int8_problem: y = act((x w^T) * (xs ws) + b [+ r]) [+ r], x [m, k] and
+    w [n, k] int8, a scale for each row of both.
+
+    residual: "none", "before" or "after" the activation; ld*: row strides in
+    elements (0 = dense); offsets: x, xs, w, ws, b, r, y.
+    """
+    da, db = ACT_DEFAULTS.get(act, (0.0, 0.0))
+    return linear_int8_problem(m, n, k, ldx, ldw, ldr, ldy, *offsets,
+                               _code(LINEAR_ACTIVATIONS, act), da if alpha is None else alpha,
+                               db if beta is None else beta, int(bias),
+                               _code(RESIDUALS, residual), 0)
+
+
+def linear_int8_scratch_size(p: linear_int8_problem, dtype) -> int:
+    return _size("linear_int8_scratch_size", p, _dt(dtype))
+
+
+def linear_int8_describe_variant(p: linear_int8_problem, dtype) -> str:
+    return _describe("linear_int8_describe_variant", p, dtype)
+
+
+def linear_int8_check(p, dtype, x, xs, w, ws, b, r, y, scratch=None, scratch_bytes=0) -> int:
+    """Status linear_int8_forward would return before enqueueing (host only)."""
+    return lib().linear_int8_check(ctypes.byref(p), _dt(dtype),
+                                   *map(_ptr, (x, xs, w, ws, b, r, y, scratch)),
+                                   int(scratch_bytes))
+
+
+def linear_int8_forward(p, dtype, x, xs, w, ws, b, r, y, scratch=None, scratch_bytes=0,
+                        stream=None, check=True) -> int:
+    """Enqueue the 8-bit linear layer on `stream`; dtype: of b, r and y."""
+    return _run("linear_int8_forward", p, dtype, (x, xs, w, ws, b, r, y), scratch, scratch_bytes,
+                stream, check)

@@ -1,0 +1,287 @@
+// Layer norm forward (include/layer_norm.h), with the dropout and the residual before
+// it: one read of x and r, one write of y and s.
+//
+// Rows up to 32768 elements are held in registers by T threads, U runs of 8 each, so
+// that mean and variance are two sums over registers (the second of squared distances,
+// which does not cancel).  Short rows take a wave each, four to a workgroup, with no
+// barrier.  Longer rows go in two launches: a mean and a sum of squared distances for
+// each part of 8192 elements, then every part joins those of its row (Chan, Golub and
+// LeVeque's formula for the variance of joined samples) and normalises.
+#include <algorithm>
+
+#include "row_ops.h"
+#include "rows_plan.h"
+
+namespace convfwd {
+
+namespace {
+
+template <typename E>
+struct NormArgs {
+  const E *x, *r, *w, *b;
+  E *y, *s;
+  float *mean, *rstd;
+  long long ldx, ldr, ldy, lds;
+  long long row0, m;  // first row of this launch, rows of all
+  int n;
+  float eps;
+  DropArgs d;
+  float2* parts;  // [m][nparts]: mean, sum of squared distances
+  int nparts;
+};
+
+// s = r + drop(x) of the runs run0, run0 + T, ... of a row; elements past n are 0 (with
+// or without the mask).
+template <typename E, int T, int U, bool DROP>
+__device__ __forceinline__ void load_row(const NormArgs<E>& a, DropCounter c, long long row,
+                                         int run0, float (&v)[U][8]) {
+  float t[U][8];
+  load_runs<T>(a.x + row * a.ldx, a.n, run0, v);
+  if (a.r) load_runs<T>(a.r + row * a.ldr, a.n, run0, t);
+  if constexpr (DROP) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) drop8(a.d, c, run0 + u * T, (unsigned)row, v[u]);
+  }
+  if (a.r) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[u][e] += t[u][e];
+  }
+}
+
+template <typename E, int T, int U>
+__device__ __forceinline__ void store_row(const NormArgs<E>& a, long long row, int run0, float mean,
+                                          float rstd, float (&v)[U][8]) {
+  if (a.s) store_runs<T>(a.s + row * a.lds, a.n, run0, v);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[u][e] = (v[u][e] - mean) * rstd;
+  float t[U][8];
+  if (a.w) {
+    load_runs<T>(a.w, a.n, run0, t);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[u][e] *= t[u][e];
+  }
+  if (a.b) {
+    load_runs<T>(a.b, a.n, run0, t);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[u][e] += t[u][e];
+  }
+  store_runs<T>(a.y + row * a.ldy, a.n, run0, v);
+}
+
+// Sum of squared distances from mean of a thread's elements before n.
+template <int T, int U>
+__device__ __forceinline__ float spread(const float (&v)[U][8], int run0, int n, float mean) {
+  const int whole = n >> 3;
+  float q = 0.0f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float d = v[u][e] - mean;
+      s = fmaf(d, d, s);
+    }
+    if (run0 + u * T < whole) q += s;
+  }
+  if (n & 7) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (run0 + u * T == whole) {
+#pragma unroll
+        for (int e = 0; e < 7; ++e) {
+          const float d = v[u][e] - mean;
+          if (e < (n & 7)) q = fmaf(d, d, q);
+        }
+      }
+  }
+  return q;
+}
+
+template <int U>
+__device__ __forceinline__ float total(const float (&v)[U][8]) {
+  float t = 0.0f;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t += v[u][e];
+  return t;
+}
+
+template <typename E, int T, int U, bool DROP>
+__global__ __launch_bounds__(T == 64 ? 256 : T) void layer_norm_rows_kernel(const NormArgs<E> a) {
+  constexpr int TEAMS = T == 64 ? 4 : 1;
+  __shared__ float lds[2][T / 64];
+  const int t = threadIdx.x % T, team = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
+  const DropCounter c = DROP ? drop_counter(a.d) : DropCounter{0, 0};
+  const long long row = a.row0 + (long long)blockIdx.x * TEAMS + team;
+  if (row >= a.m) return;
+  float v[U][8];
+  load_row<E, T, U, DROP>(a, c, row, t, v);
+  // quotients, not products with 1 / n: a row of equal values has its value as mean
+  const float mean = row_sum<T>(total(v), lds[0]) / (float)a.n;
+  const float var = row_sum<T>(spread<T>(v, t, a.n, mean), lds[1]) / (float)a.n;
+  const float rstd = 1.0f / sqrtf(var + a.eps);
+  if (a.mean && t == 0) {
+    a.mean[row] = mean;
+    a.rstd[row] = rstd;
+  }
+  store_row<E, T, U>(a, row, t, mean, rstd, v);
+}
+
+constexpr int kPart = 8192;  // elements of a part: 256 threads, 4 runs each
+
+// A workgroup takes one part of one row.
+template <typename E, bool DROP>
+__global__ __launch_bounds__(256) void layer_norm_parts_kernel(const NormArgs<E> a) {
+  __shared__ float lds[2][4];
+  const DropCounter c = DROP ? drop_counter(a.d) : DropCounter{0, 0};
+  const int local = blockIdx.x / a.nparts, part = blockIdx.x - local * a.nparts;
+  const long long row = a.row0 + local;
+  const int run0 = part * (kPart / 8) + threadIdx.x, count = min(kPart, a.n - part * kPart);
+  float v[4][8];
+  load_row<E, 256, 4, DROP>(a, c, row, run0, v);
+  const float mean = row_sum<256>(total(v), lds[0]) / (float)count;
+  const float q = row_sum<256>(spread<256>(v, run0, a.n, mean), lds[1]);
+  if (threadIdx.x == 0) a.parts[row * a.nparts + part] = make_float2(mean, q);
+}
+
+template <typename E, bool DROP>
+__global__ __launch_bounds__(256) void layer_norm_joined_kernel(const NormArgs<E> a) {
+  const DropCounter c = DROP ? drop_counter(a.d) : DropCounter{0, 0};
+  const int lane = threadIdx.x & 63;
+  const int local = blockIdx.x / a.nparts, part = blockIdx.x - local * a.nparts;
+  const long long row = a.row0 + local;
+  const int run0 = part * (kPart / 8) + threadIdx.x;
+  float v[4][8];
+  load_row<E, 256, 4, DROP>(a, c, row, run0, v);
+  // every wave joins the row's parts (128 at most, two a lane)
+  const float2* p = a.parts + row * a.nparts;
+  float2 q[2];
+  float count[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int at = lane + 64 * k;
+    q[k] = at < a.nparts ? p[at] : make_float2(0.0f, 0.0f);
+    count[k] = at < a.nparts ? (float)min(kPart, a.n - at * kPart) : 0.0f;
+  }
+  const float mean = wave_sum(count[0] * q[0].x + count[1] * q[1].x) / (float)a.n;
+  float far = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float d = q[k].x - mean;
+    far += q[k].y + (count[k] > 0.0f ? count[k] * d * d : 0.0f);
+  }
+  const float rstd = 1.0f / sqrtf(wave_sum(far) / (float)a.n + a.eps);
+  if (a.mean && part == 0 && threadIdx.x == 0) {
+    a.mean[row] = mean;
+    a.rstd[row] = rstd;
+  }
+  store_row<E, 256, 4>(a, row, run0, mean, rstd, v);
+}
+
+// Rows go in launches of fewer than 2^32 work-items.
+constexpr long long kMostItems = 0xff000000LL;
+
+// f(args, rows) for the rows of every launch, `each` work-items a row.
+template <typename E, typename F>
+hipError_t by_rows(NormArgs<E> a, long long each, F f) {
+  const long long most = kMostItems / each;
+  for (long long at = 0; at < a.m; at += most) {
+    a.row0 = at;
+    f(a, (unsigned)std::min(most, a.m - at));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <typename E, int T, int U>
+hipError_t launch_rows(const NormArgs<E>& args, hipStream_t s) {
+  constexpr int TEAMS = T == 64 ? 4 : 1;
+  return by_rows(args, T, [&](const NormArgs<E>& a, unsigned rows) {
+    const dim3 grid((rows + TEAMS - 1) / TEAMS), block(T * TEAMS);
+    if (a.d.threshold) hipLaunchKernelGGL((layer_norm_rows_kernel<E, T, U, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((layer_norm_rows_kernel<E, T, U, false>), grid, block, 0, s, a);
+  });
+}
+
+template <typename E>
+hipError_t launch_parts(const NormArgs<E>& args, hipStream_t s) {
+  const hipError_t e = by_rows(args, 256 * args.nparts, [&](const NormArgs<E>& a, unsigned rows) {
+    const dim3 grid(rows * a.nparts), block(256);
+    if (a.d.threshold) hipLaunchKernelGGL((layer_norm_parts_kernel<E, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((layer_norm_parts_kernel<E, false>), grid, block, 0, s, a);
+  });
+  if (e != hipSuccess) return e;
+  return by_rows(args, 256 * args.nparts, [&](const NormArgs<E>& a, unsigned rows) {
+    const dim3 grid(rows * a.nparts), block(256);
+    if (a.d.threshold) hipLaunchKernelGGL((layer_norm_joined_kernel<E, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((layer_norm_joined_kernel<E, false>), grid, block, 0, s, a);
+  });
+}
+
+template <typename E>
+hipError_t norm(const NormArgs<E>& a, const RowPlan& pl, hipStream_t s) {
+  if (pl.parts) return launch_parts(a, s);
+  if (pl.threads == 64)
+    return pl.runs == 1   ? launch_rows<E, 64, 1>(a, s)
+           : pl.runs == 2 ? launch_rows<E, 64, 2>(a, s)
+                          : launch_rows<E, 64, 4>(a, s);
+  if (pl.threads == 256)
+    return pl.runs == 2 ? launch_rows<E, 256, 2>(a, s) : launch_rows<E, 256, 4>(a, s);
+  return pl.runs == 2 ? launch_rows<E, 1024, 2>(a, s) : launch_rows<E, 1024, 4>(a, s);
+}
+
+template <typename E>
+int run(const layer_norm_problem* p, const NormGeo& g, const NormPlan& pl, const void* x,
+        const void* r, const void* w, const void* b, void* y, void* s, void* mean, void* rstd,
+        const void* step, void* scratch, void* stream) {
+  NormArgs<E> a{};
+  a.x = elements<E>(x, p->x_off);
+  a.r = p->has_residual ? elements<E>(r, p->r_off) : nullptr;
+  a.w = p->has_weight ? elements<E>(w, p->w_off) : nullptr;
+  a.b = p->has_bias ? elements<E>(b, p->b_off) : nullptr;
+  a.y = elements<E>(y, p->y_off);
+  a.s = elements<E>(s, p->s_off);
+  a.mean = static_cast<float*>(mean);
+  a.rstd = static_cast<float*>(rstd);
+  a.ldx = g.ldx; a.ldr = g.ldr; a.ldy = g.ldy; a.lds = g.lds;
+  a.m = g.m;
+  a.n = (int)g.n;
+  a.eps = p->eps;
+  a.d = drop_args(drop_threshold(p->drop), p->seed, p->offset, step);
+  a.parts = static_cast<float2*>(scratch);
+  a.nparts = (int)pl.row.parts;
+  return norm<E>(a, pl.row, static_cast<hipStream_t>(stream)) == hipSuccess ? CONV_OK
+                                                                             : CONV_ERR_DEVICE;
+}
+
+}  // namespace
+
+}  // namespace convfwd
+
+using namespace convfwd;
+
+extern "C" int layer_norm_forward(const layer_norm_problem* p, int dtype, const void* x,
+                                  const void* r, const void* w, const void* b, void* y, void* s,
+                                  void* mean, void* rstd, const void* step, void* scratch,
+                                  uint64_t scratch_bytes, void* stream) {
+  NormGeo g;
+  NormPlan pl;
+  const int st = layer_norm_checked(p, dtype, x, r, w, b, y, s, mean, rstd, step, scratch,
+                                    scratch_bytes, &g, &pl);
+  if (st || g.m == 0) return st;
+  if (dtype == CONV_F16)
+    return run<_Float16>(p, g, pl, x, r, w, b, y, s, mean, rstd, step, scratch, stream);
+  if (dtype == CONV_BF16)
+    return run<__bf16>(p, g, pl, x, r, w, b, y, s, mean, rstd, step, scratch, stream);
+  return run<float>(p, g, pl, x, r, w, b, y, s, mean, rstd, step, scratch, stream);
+}

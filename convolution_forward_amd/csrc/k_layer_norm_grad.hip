@@ -1,0 +1,347 @@
+// Layer norm backward (include/layer_norm.h): one read of s, dy (and ds), one write of
+// dx (and dr), and the column sums dw and db on the way.
+//
+// A workgroup walks over rows and keeps, for the columns that its threads hold, the
+// sums of dy u and of dy in registers; at the end it writes one partial row of each,
+// and a second kernel adds the partial rows in order.  So no atomics, and dy and s are
+// read once for both the row's gradient and the columns' sums.  A row needs two sums
+// (of g and of g u) before its first gradient: one exchange through LDS and one barrier
+// a row, none where a wave holds a row.  Rows of more than 16384 elements go in parts
+// of 2048, in two launches: the parts' sums, then the gradients.
+#include <algorithm>
+
+#include "linear_tile.h"
+#include "row_ops.h"
+#include "rows_plan.h"
+
+namespace convfwd {
+
+namespace {
+
+template <typename E>
+struct GradArgs {
+  const E *s, *w, *dy, *ds;
+  const float *mean, *rstd;
+  E *dx, *dr;        // either may be null
+  float* partials;   // [group][2][np] of dw and db; null: neither is wanted
+  float2* sums;      // [m][parts]: sums of g u and of g
+  long long lds, lddy, ldds, lddx, lddr;
+  long long row0, m;  // row0: first row of this launch (parts' sums)
+  int n, np, parts;
+  float inv_n;
+  DropArgs d;
+};
+
+// The gradient of s from u, g and the row's two means, and its stores.
+template <typename E, int T, int U, bool DROP>
+__device__ __forceinline__ void finish_row(const GradArgs<E>& a, DropCounter c, long long row,
+                                           int run0, float rstd, float along, float level,
+                                           const float (&u)[U][8], float (&g)[U][8]) {
+#pragma unroll
+  for (int k = 0; k < U; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[k][e] = rstd * (g[k][e] - level - u[k][e] * along);
+  if (a.ds) {
+    float t[U][8];
+    load_runs<T>(a.ds + row * a.ldds, a.n, run0, t);
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[k][e] += t[k][e];
+  }
+  if (a.dr) store_runs<T>(a.dr + row * a.lddr, a.n, run0, g);
+  if (a.dx) {
+    if constexpr (DROP) {
+#pragma unroll
+      for (int k = 0; k < U; ++k) drop8(a.d, c, run0 + k * T, (unsigned)row, g[k]);
+    }
+    store_runs<T>(a.dx + row * a.lddx, a.n, run0, g);
+  }
+}
+
+// T threads a row, U runs each; TEAMS rows at a time.
+template <typename E, int T, int U, int TEAMS, bool DROP>
+__global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_kernel(const GradArgs<E> a) {
+  constexpr int WAVES = T / 64;
+  __shared__ float2 red[2][TEAMS * WAVES];
+  __shared__ float columns[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? T * 8 : 1];
+  const int t = threadIdx.x % T, team = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const DropCounter c = DROP ? drop_counter(a.d) : DropCounter{0, 0};
+  float w[U][8], dw[U][8], db[U][8];
+#pragma unroll
+  for (int k = 0; k < U; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      w[k][e] = 1.0f;
+      dw[k][e] = db[k][e] = 0.0f;
+    }
+  if (a.w) load_runs<T>(a.w, a.n, t, w);
+  int buf = 0;
+  for (long long base = (long long)blockIdx.x * TEAMS; base < a.m; base += (long long)gridDim.x * TEAMS) {
+    const long long row = base + team;
+    const bool in = row < a.m;  // uniform in a wave; every wave reaches the barrier
+    float u[U][8], g[U][8], rstd = 0.0f, along = 0.0f, level = 0.0f;
+    if (in) {
+      load_runs<T>(a.s + row * a.lds, a.n, t, u);
+      load_runs<T>(a.dy + row * a.lddy, a.n, t, g);
+      const float mean = a.mean[row];
+      rstd = a.rstd[row];
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          u[k][e] = (u[k][e] - mean) * rstd;
+          dw[k][e] = fmaf(g[k][e], u[k][e], dw[k][e]);
+          db[k][e] += g[k][e];
+          g[k][e] *= w[k][e];
+          along = fmaf(g[k][e], u[k][e], along);
+          level += g[k][e];
+        }
+      along = wave_sum(along);
+      level = wave_sum(level);
+    }
+    if constexpr (WAVES > 1) {
+      if ((threadIdx.x & 63) == 0) red[buf][wave] = make_float2(along, level);
+      __syncthreads();  // a wave may be one row ahead, hence two buffers
+      along = level = 0.0f;
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) {
+        along += red[buf][team * WAVES + i].x;
+        level += red[buf][team * WAVES + i].y;
+      }
+      buf ^= 1;
+    }
+    if (in) finish_row<E, T, U, DROP>(a, c, row, t, rstd, along * a.inv_n, level * a.inv_n, u, g);
+  }
+  if (!a.partials) return;
+  float* p = a.partials + (long long)blockIdx.x * 2 * a.np;
+  if constexpr (TEAMS == 1) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int at = (t + k * T) * 8;
+      if (at < a.np) {
+        store8(p + at, 8, dw[k]);
+        store8(p + a.np + at, 8, db[k]);
+      }
+    }
+  } else {
+    // the teams' sums joined in order, T runs at a time
+#pragma unroll
+    for (int k = 0; k < 2 * U; ++k) {
+      float* own = &columns[team][t * 8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) own[e] = k < U ? dw[k % U][e] : db[k % U][e];
+      __syncthreads();
+      for (int i = threadIdx.x; i < T * 8; i += T * TEAMS) {
+        const int at = k % U * T * 8 + i;
+        if (at < a.np) {
+          float s = columns[0][i];
+#pragma unroll
+          for (int j = 1; j < TEAMS; ++j) s += columns[j][i];
+          p[(k < U ? 0 : a.np) + at] = s;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+constexpr int kPartRuns = 256;  // runs of a part, a thread each
+
+// Sums of g u and g of one part of one row.
+template <typename E>
+__global__ __launch_bounds__(256) void layer_norm_grad_sums_kernel(const GradArgs<E> a) {
+  __shared__ float lds[2][4];
+  const int local = blockIdx.x / a.parts, part = blockIdx.x - local * a.parts;
+  const long long row = a.row0 + local;
+  const int run0 = part * kPartRuns + threadIdx.x;
+  float u[1][8], g[1][8], along = 0.0f, level = 0.0f;
+  load_runs<kPartRuns>(a.s + row * a.lds, a.n, run0, u);
+  load_runs<kPartRuns>(a.dy + row * a.lddy, a.n, run0, g);
+  if (a.w) {
+    float w[1][8];
+    load_runs<kPartRuns>(a.w, a.n, run0, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[0][e] *= w[0][e];
+  }
+  const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    along = fmaf(g[0][e], (u[0][e] - mean) * rstd, along);
+    level += g[0][e];
+  }
+  along = row_sum<256>(along, lds[0]);
+  level = row_sum<256>(level, lds[1]);
+  if (threadIdx.x == 0) a.sums[row * a.parts + part] = make_float2(along, level);
+}
+
+// Gradients of one part of every gridDim.x / parts-th row.
+template <typename E, bool DROP>
+__global__ __launch_bounds__(256) void layer_norm_grad_parts_kernel(const GradArgs<E> a) {
+  const DropCounter c = DROP ? drop_counter(a.d) : DropCounter{0, 0};
+  const int group = blockIdx.x / a.parts, part = blockIdx.x - group * a.parts;
+  const int groups = gridDim.x / a.parts, lane = threadIdx.x & 63;
+  const int run0 = part * kPartRuns + threadIdx.x;
+  float w[1][8], dw[8], db[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    w[0][e] = 1.0f;
+    dw[e] = db[e] = 0.0f;
+  }
+  if (a.w) load_runs<kPartRuns>(a.w, a.n, run0, w);
+  for (long long row = group; row < a.m; row += groups) {
+    float u[1][8], g[1][8], along = 0.0f, level = 0.0f;
+    load_runs<kPartRuns>(a.s + row * a.lds, a.n, run0, u);
+    load_runs<kPartRuns>(a.dy + row * a.lddy, a.n, run0, g);
+    for (int i = lane; i < a.parts; i += 64) {
+      const float2 q = a.sums[row * a.parts + i];
+      along += q.x;
+      level += q.y;
+    }
+    along = wave_sum(along) * a.inv_n;
+    level = wave_sum(level) * a.inv_n;
+    const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      u[0][e] = (u[0][e] - mean) * rstd;
+      dw[e] = fmaf(g[0][e], u[0][e], dw[e]);
+      db[e] += g[0][e];
+      g[0][e] *= w[0][e];
+    }
+    finish_row<E, kPartRuns, 1, DROP>(a, c, row, run0, rstd, along, level, u, g);
+  }
+  if (!a.partials || run0 * 8 >= a.np) return;
+  float* p = a.partials + (long long)group * 2 * a.np + run0 * 8;
+  store8(p, 8, dw);
+  store8(p + a.np, 8, db);
+}
+
+// Adds the groups' partial rows: 64 columns of dw or db a workgroup, 64 rows at a time
+// (16 lanes of 4 columns a row), then the 64 sums in order.
+template <typename E>
+__global__ __launch_bounds__(1024) void layer_norm_grad_join_kernel(const float* partials, E* dw,
+                                                                    E* db, int groups, int n,
+                                                                    int np) {
+  __shared__ float lds[64][64 + 4];
+  const int slot = threadIdx.x >> 4, col = (threadIdx.x & 15) * 4, at = blockIdx.x * 64 + col;
+  const float* p = partials + (blockIdx.y ? np : 0) + at;
+  lin::f32x4 s = {0, 0, 0, 0};
+  if (at < np) {
+    constexpr int B = 8;
+    for (int i = slot; i < groups; i += 64 * B) {
+      lin::f32x4 q[B];
+#pragma unroll
+      for (int k = 0; k < B; ++k)
+        q[k] = i + 64 * k < groups
+                   ? *reinterpret_cast<const lin::f32x4*>(p + (long long)(i + 64 * k) * 2 * np)
+                   : lin::f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < B; ++k) s += q[k];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) lds[slot][col + e] = s[e];
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int c = blockIdx.x * 64 + threadIdx.x;
+    float t = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < 64; ++i) t += lds[i][threadIdx.x];
+    E* out = blockIdx.y ? db : dw;
+    if (c < n && out) out[c] = (E)t;
+  }
+}
+
+template <typename E, int T, int U, int TEAMS>
+void launch_grad(const GradArgs<E>& a, unsigned groups, hipStream_t s) {
+  if (a.d.threshold)
+    hipLaunchKernelGGL((layer_norm_grad_kernel<E, T, U, TEAMS, true>), dim3(groups), dim3(T * TEAMS), 0, s, a);
+  else
+    hipLaunchKernelGGL((layer_norm_grad_kernel<E, T, U, TEAMS, false>), dim3(groups), dim3(T * TEAMS), 0, s, a);
+}
+
+template <typename E>
+hipError_t grad(GradArgs<E>& a, const NormBackwardPlan& pl, E* dw, E* db, hipStream_t s) {
+  const unsigned groups = (unsigned)pl.groups;
+  if (pl.row.parts) {
+    const long long most = 0xff000000LL / 256 / a.parts;  // fewer than 2^32 work-items a launch
+    for (long long at = 0; at < a.m; at += most) {
+      a.row0 = at;
+      const dim3 grid((unsigned)(std::min(most, a.m - at) * a.parts));
+      hipLaunchKernelGGL((layer_norm_grad_sums_kernel<E>), grid, dim3(256), 0, s, a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    const dim3 grid(groups * a.parts);
+    if (a.d.threshold)
+      hipLaunchKernelGGL((layer_norm_grad_parts_kernel<E, true>), grid, dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((layer_norm_grad_parts_kernel<E, false>), grid, dim3(256), 0, s, a);
+  } else if (pl.row.threads == 64) {
+    if (pl.row.runs == 1) launch_grad<E, 64, 1, 4>(a, groups, s);
+    else if (pl.row.runs == 2) launch_grad<E, 64, 2, 4>(a, groups, s);
+    else launch_grad<E, 64, 4, 4>(a, groups, s);
+  } else if (pl.row.threads == 256) {
+    launch_grad<E, 256, 2, 1>(a, groups, s);
+  } else {
+    if (pl.row.runs == 1) launch_grad<E, 1024, 1, 1>(a, groups, s);
+    else launch_grad<E, 1024, 2, 1>(a, groups, s);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.partials) return e;
+  hipLaunchKernelGGL((layer_norm_grad_join_kernel<E>), dim3((a.np + 63) / 64, 2), dim3(1024), 0, s,
+                     a.partials, dw, db, (int)groups, a.n, a.np);
+  return hipGetLastError();
+}
+
+template <typename E>
+int run(const layer_norm_problem* p, const NormGeo& g, const NormBackwardPlan& pl, const void* s,
+        const void* w, const void* mean, const void* rstd, const void* dy, const void* ds, void* dx,
+        void* dr, void* dw, void* db, const void* step, void* scratch, void* stream) {
+  GradArgs<E> a{};
+  a.s = elements<E>(s, p->s_off);
+  a.w = p->has_weight ? elements<E>(w, p->w_off) : nullptr;
+  a.dy = elements<E>(dy, p->dy_off);
+  a.ds = elements<E>(ds, p->ds_off);
+  a.mean = static_cast<const float*>(mean);
+  a.rstd = static_cast<const float*>(rstd);
+  a.dx = elements<E>(dx, p->dx_off);
+  a.dr = elements<E>(dr, p->dr_off);
+  char* sc = static_cast<char*>(scratch);
+  a.partials = dw || db ? reinterpret_cast<float*>(sc + pl.partials) : nullptr;
+  a.sums = reinterpret_cast<float2*>(sc + pl.sums);
+  a.lds = g.lds; a.lddy = g.ldy; a.ldds = g.ldds; a.lddx = g.lddx; a.lddr = g.lddr;
+  a.m = g.m;
+  a.n = (int)g.n;
+  a.np = (int)(ceil_div(g.n, 8) * 8);
+  a.parts = (int)pl.row.parts;
+  a.inv_n = 1.0f / (float)g.n;
+  a.d = drop_args(drop_threshold(p->drop), p->seed, p->offset, step);
+  const hipError_t e = grad<E>(a, pl, elements<E>(dw, p->dw_off), elements<E>(db, p->db_off),
+                               static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? CONV_OK : CONV_ERR_DEVICE;
+}
+
+}  // namespace
+
+}  // namespace convfwd
+
+using namespace convfwd;
+
+extern "C" int layer_norm_backward(const layer_norm_problem* p, int dtype, const void* s,
+                                   const void* w, const void* mean, const void* rstd,
+                                   const void* dy, const void* ds, void* dx, void* dr, void* dw,
+                                   void* db, const void* step, void* scratch,
+                                   uint64_t scratch_bytes, void* stream) {
+  NormGeo g;
+  NormBackwardPlan pl;
+  const int st = layer_norm_backward_checked(p, dtype, s, w, mean, rstd, dy, ds, dx, dr, dw, db,
+                                             step, scratch, scratch_bytes, &g, &pl);
+  if (st || (g.m == 0 && !dw && !db)) return st;
+  if (dtype == CONV_F16)
+    return run<_Float16>(p, g, pl, s, w, mean, rstd, dy, ds, dx, dr, dw, db, step, scratch, stream);
+  if (dtype == CONV_BF16)
+    return run<__bf16>(p, g, pl, s, w, mean, rstd, dy, ds, dx, dr, dw, db, step, scratch, stream);
+  return run<float>(p, g, pl, s, w, mean, rstd, dy, ds, dx, dr, dw, db, step, scratch, stream);
+}

@@ -185,5 +185,6 @@ CONVFWD_INST(_Float16)
 CONVFWD_INST(__bf16)
 CONVFWD_INST(float)
 #undef CONVFWD_INST
+template hipError_t launch_pack<signed char>(const PackArgs&, hipStream_t);
 
 }  // namespace convfwd

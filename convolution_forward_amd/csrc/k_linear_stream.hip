@@ -36,7 +36,8 @@ constexpr int kStreamWaves = 8;
 
 // VEC: rows of whole aligned 16-byte pieces; otherwise rows start anywhere and the
 // last pieces of a row are loaded from further back and shifted.
-template <typename E, int TC, bool GATED, bool VEC, int G, int M>
+// O: the outputs' type (8-bit operands have int32 sums).
+template <typename E, int TC, bool GATED, bool VEC, int G, int M, typename O = E>
 __global__ __launch_bounds__(kStreamWaves * 64) void linear_stream_kernel(const ProductArgs a) {
   using namespace lin;
   constexpr int EB = (int)sizeof(E), EPC = 16 / EB, UE = 64 / EB, WAVES = kStreamWaves;
@@ -44,10 +45,11 @@ __global__ __launch_bounds__(kStreamWaves * 64) void linear_stream_kernel(const 
   // weight loads of a batch, each of G units
   constexpr int N = G > 1 || M > 1 || TC * KINDS >= 4 ? 2 : 4;
   constexpr int BU = N * G;  // units of a batch
-  typedef std::conditional_t<EB == 2, s16x8, f32x4> Frag;
+  using Frag = typename Tile<E, 16, false, 64>::Frag;
   using R = Ragged<E, false>;
+  typedef std::conditional_t<EB == 1, int, float> S;
   constexpr int PARTS = WAVES * G;
-  __shared__ __attribute__((aligned(16))) float red[PARTS][KINDS * TC][16][RB];
+  __shared__ __attribute__((aligned(16))) S red[PARTS][KINDS * TC][16][RB];
 
   const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -79,7 +81,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void linear_stream_kernel(const 
     qrow[t] = (int)((VEC ? t * 16 + l : min(t * 16 + l, a.C - 1)) * a.ldq * EB);
   const int last = (a.K - EPC) * EB;  // of a row's last whole piece
 
-  mfma_f32x4 acc[M][KINDS][TC][G];
+  Sums<E> acc[M][KINDS][TC][G];
 #pragma unroll
   for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -87,7 +89,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void linear_stream_kernel(const 
 #pragma unroll
       for (int t = 0; t < TC; ++t)
 #pragma unroll
-        for (int j = 0; j < G; ++j) acc[m][d][t][j] = mfma_f32x4{0, 0, 0, 0};
+        for (int j = 0; j < G; ++j) acc[m][d][t][j] = Sums<E>{0, 0, 0, 0};
 
   struct Batch {
     Frag p[M][KINDS][N], q[TC][BU];
@@ -163,18 +165,18 @@ __global__ __launch_bounds__(kStreamWaves * 64) void linear_stream_kernel(const 
     for (int d = 0; d < KINDS; ++d)
 #pragma unroll
       for (int t = 0; t < TC; ++t) {
-        mfma_f32x4 v = acc[m][d][t][0];
+        Sums<E> v = acc[m][d][t][0];
 #pragma unroll
         for (int j = 1; j < G; ++j)
           if (g * 4 / RG == j) v = acc[m][d][t][j];
-        *reinterpret_cast<mfma_f32x4*>(
+        *reinterpret_cast<Sums<E>*>(
             &red[wave * G + g * 4 / RG][d * TC + t][l][m * RG + g * 4 % RG]) = v;
       }
   __syncthreads();
   constexpr int ALL = KINDS * TC * 16 * RB;
   for (int i = tid; i < ALL; i += WAVES * 64) {
-    float* f = &red[0][0][0][0] + i;
-    float s = f[0];
+    S* f = &red[0][0][0][0] + i;
+    S s = f[0];
 #pragma unroll
     for (int w = 1; w < PARTS; ++w) s += f[w * ALL];
     f[0] = s;
@@ -188,13 +190,13 @@ __global__ __launch_bounds__(kStreamWaves * 64) void linear_stream_kernel(const 
       e.R = min(e.R, r0 + RB);
       float v[8], w[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = q < RB ? red[0][c >> 4][c & 15][rr + q % RB] : 0.0f;
+      for (int q = 0; q < 8; ++q) v[q] = q < RB ? (float)red[0][c >> 4][c & 15][rr + q % RB] : 0.0f;
       if constexpr (GATED) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) w[q] = q < RB ? red[0][TC + (c >> 4)][c & 15][rr + q % RB] : 0.0f;
         finish_gated<E>(e, c, r, v, w);
       } else {
-        finish_linear<E>(e, 0, c, r, v);
+        finish_linear<O, EB == 1>(e, 0, c, r, v);
       }
     }
   }
@@ -203,7 +205,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void linear_stream_kernel(const 
 // Joins the planes of a split contraction in split order: 8 outputs a thread, 8
 // planes' loads in flight: a round trip to planes that other XCDs wrote takes about a
 // us, which bounds this.
-template <typename E, bool GATED>
+template <typename E, bool GATED, typename S = float>
 __device__ __forceinline__ void join(const JoinArgs& a, long long block) {
   constexpr int KINDS = GATED ? 2 : 1, B = GATED ? 4 : 8;
   const int per_row = (int)(a.plane_ld / 8);
@@ -214,18 +216,19 @@ __device__ __forceinline__ void join(const JoinArgs& a, long long block) {
   const int z = (int)(row / a.C);
   const long long c = row - (long long)z * a.C;
   const float* s = a.planes + row * a.plane_ld + r;
-  float v[8], u[8];
+  S v[8], u[8];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) v[q] = u[q] = 0.0f;
+  for (int q = 0; q < 8; ++q) v[q] = u[q] = 0;
+  typedef S V __attribute__((ext_vector_type(4)));
   for (int i = 0; i < a.splits; i += B) {
-    lin::f32x4 lo[KINDS][B], hi[KINDS][B];
+    V lo[KINDS][B], hi[KINDS][B];
 #pragma unroll
     for (int p = 0; p < B; ++p)
 #pragma unroll
       for (int d = 0; d < KINDS; ++d) {  // past the last plane: the last one again, not added
         const float* f = s + min(i + p, a.splits - 1) * a.plane_stride + d * (long long)a.C * a.plane_ld;
-        lo[d][p] = *reinterpret_cast<const lin::f32x4*>(f);
-        hi[d][p] = *reinterpret_cast<const lin::f32x4*>(f + 4);
+        lo[d][p] = *reinterpret_cast<const V*>(f);
+        hi[d][p] = *reinterpret_cast<const V*>(f + 4);
       }
 #pragma unroll
     for (int p = 0; p < B; ++p)
@@ -240,13 +243,27 @@ __device__ __forceinline__ void join(const JoinArgs& a, long long block) {
       }
   }
   if (r >= a.e.R) return;
-  if constexpr (GATED) finish_gated<E>(a.e, c, r, v, u);
-  else finish_linear<E>(a.e, z, c, r, v);
+  if constexpr (GATED) {
+    finish_gated<E>(a.e, c, r, v, u);
+  } else if constexpr (std::is_same_v<S, float>) {
+    finish_linear<E>(a.e, z, c, r, v);
+  } else {
+    float f[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) f[q] = (float)v[q];
+    finish_linear<E, true>(a.e, z, c, r, f);
+  }
 }
 
 template <typename E, bool GATED>
 __global__ __launch_bounds__(256) void linear_join_kernel(const JoinArgs a) {
   join<E, GATED>(a, blockIdx.x);
+}
+
+// Planes of int32 sums (8-bit operands).
+template <typename O>
+__global__ __launch_bounds__(256) void linear_int8_join_kernel(const JoinArgs a) {
+  join<O, false, int>(a, blockIdx.x);
 }
 
 template <typename E>
@@ -261,22 +278,22 @@ unsigned join_blocks(const JoinArgs& a) {
   return (unsigned)((items + 255) / 256);
 }
 
-template <typename E, int TC, bool GATED, int G, int M>
+template <typename E, int TC, bool GATED, int G, int M, typename O>
 hipError_t stream_g(const ProductArgs& a, bool vec, hipStream_t s) {
   const int rb = 16 * M / G;
   const dim3 grid((a.R + rb - 1) / rb), block(kStreamWaves * 64);
-  if (vec) hipLaunchKernelGGL((linear_stream_kernel<E, TC, GATED, true, G, M>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((linear_stream_kernel<E, TC, GATED, false, G, M>), grid, block, 0, s, a);
+  if (vec) hipLaunchKernelGGL((linear_stream_kernel<E, TC, GATED, true, G, M, O>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((linear_stream_kernel<E, TC, GATED, false, G, M, O>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
-template <typename E, int TC, bool GATED>
+template <typename E, int TC, bool GATED, typename O = E>
 hipError_t stream_t(const ProductArgs& a, int rows, bool vec, hipStream_t s) {
   if constexpr (TC == 2)  // 32 weight rows share Q's loads, which 16 rows c do not need
-    if (rows == 32) return stream_g<E, TC, GATED, 1, 2>(a, vec, s);
-  if (rows == 16) return stream_g<E, TC, GATED, 1, 1>(a, vec, s);
-  if (rows == 8) return stream_g<E, TC, GATED, 2, 1>(a, vec, s);
-  return stream_g<E, TC, GATED, 4, 1>(a, vec, s);
+    if (rows == 32) return stream_g<E, TC, GATED, 1, 2, O>(a, vec, s);
+  if (rows == 16) return stream_g<E, TC, GATED, 1, 1, O>(a, vec, s);
+  if (rows == 8) return stream_g<E, TC, GATED, 2, 1, O>(a, vec, s);
+  return stream_g<E, TC, GATED, 4, 1, O>(a, vec, s);
 }
 
 }  // namespace
@@ -299,6 +316,18 @@ hipError_t launch_join(const JoinArgs& a, bool gated, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename O>
+hipError_t launch_int8_stream(const ProductArgs& a, int blocks16, int rows, bool vec, hipStream_t s) {
+  return blocks16 == 1 ? stream_t<signed char, 1, false, O>(a, rows, vec, s)
+                       : stream_t<signed char, 2, false, O>(a, rows, vec, s);
+}
+
+template <typename O>
+hipError_t launch_int8_join(const JoinArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((linear_int8_join_kernel<O>), dim3(join_blocks(a)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
 template <typename E>
 hipError_t launch_join_pair(const JoinArgs& a, const JoinArgs& b, hipStream_t s) {
   const unsigned first = join_blocks(a);
@@ -310,7 +339,9 @@ hipError_t launch_join_pair(const JoinArgs& a, const JoinArgs& b, hipStream_t s)
 #define CONVFWD_INST(E)                                                                      \
   template hipError_t launch_stream<E>(const ProductArgs&, int, int, bool, bool, hipStream_t); \
   template hipError_t launch_join<E>(const JoinArgs&, bool, hipStream_t);                   \
-  template hipError_t launch_join_pair<E>(const JoinArgs&, const JoinArgs&, hipStream_t);
+  template hipError_t launch_join_pair<E>(const JoinArgs&, const JoinArgs&, hipStream_t);    \
+  template hipError_t launch_int8_stream<E>(const ProductArgs&, int, int, bool, hipStream_t); \
+  template hipError_t launch_int8_join<E>(const JoinArgs&, hipStream_t);
 CONVFWD_INST(_Float16)
 CONVFWD_INST(__bf16)
 CONVFWD_INST(float)

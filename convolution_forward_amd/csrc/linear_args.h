@@ -21,6 +21,7 @@ struct LinEpilogue {
   int res_mode;   // LINEAR_RES_*
   int act;
   float alpha, beta;
+  const float *xs, *ws;  // 8-bit operands: scales of the rows c and of r
 };
 
 // out[c][r] = sum_k P(r, k) Q(c, k), see linear_plan.h.
@@ -101,6 +102,13 @@ template <typename E>
 hipError_t launch_join(const JoinArgs& a, bool gated, hipStream_t s);
 template <typename E>
 hipError_t launch_join_pair(const JoinArgs& a, const JoinArgs& b, hipStream_t s);
+// 8-bit operands, outputs of type O.
+template <typename O>
+hipError_t launch_int8_product(const ProductArgs& a, int tile, bool dma, hipStream_t s);
+template <typename O>
+hipError_t launch_int8_stream(const ProductArgs& a, int blocks16, int rows, bool vec, hipStream_t s);
+template <typename O>
+hipError_t launch_int8_join(const JoinArgs& a, hipStream_t s);
 template <typename E>
 hipError_t launch_dz(const DzArgs& a, bool gated, int chunks, hipStream_t s);
 template <typename E>

@@ -267,10 +267,26 @@ __device__ __forceinline__ int run_offset(int lane) {
   return ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
 }
 
+// The scales of 8-bit operands, before anything is added: v of row c times xs[c] ws[r],
+// rounded here whatever follows, so that every kernel gives the same bits.
+template <int NR, typename Off>
+__device__ __forceinline__ void scale_runs(const LinEpilogue& e, long long c, bool in, int r,
+                                           Off off, bool whole, float (&v)[NR * 8]) {
+#pragma clang fp contract(off)
+  const float xs = in ? e.xs[c] : 0.0f;
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    float t[8];
+    load8(e.ws + r + off(n), whole ? 8 : e.R - r - off(n), t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[n * 8 + i] *= xs * t[i];
+  }
+}
+
 // Linear: v holds the sums of one row c, NR runs of 8 outputs at r + off(n).  whole
 // (uniform): every run is inside; in: c is a row.  The runs' loads are in flight
 // together and one branch picks the activation for all.
-template <typename E, int NR, typename Off>
+template <typename E, int NR, bool SCALED = false, typename Off>
 __device__ __forceinline__ void finish_linear_runs(const LinEpilogue& e, int z, long long c,
                                                    bool in, int r, Off off, bool whole,
                                                    float (&v)[NR * 8]) {
@@ -294,6 +310,7 @@ __device__ __forceinline__ void finish_linear_runs(const LinEpilogue& e, int z, 
       store8(p + off(n), whole ? 8 : e.R - r - off(n), t);
     }
   };
+  if constexpr (SCALED) scale_runs<NR>(e, c, in, r, off, whole, v);
   if (e.bias[0]) add(e.bias[0], 0);
   if (e.res_mode == 1 && in) add(e.res, c * e.ldres);
   if (e.save[0] && in) store(e.save[0], c * e.ldsave);
@@ -318,10 +335,10 @@ __device__ __forceinline__ void finish_plain_runs(const LinEpilogue& e, int z, l
   }
 }
 
-template <typename E>
+template <typename E, bool SCALED = false>
 __device__ __forceinline__ void finish_linear(const LinEpilogue& e, int z, long long c, int r,
                                               float (&v)[8]) {
-  finish_linear_runs<E, 1>(e, z, c, true, r, [](int) { return 0; }, false, v);
+  finish_linear_runs<E, 1, SCALED>(e, z, c, true, r, [](int) { return 0; }, false, v);
 }
 
 // Gated: g and u hold both projections' sums.

@@ -7,23 +7,24 @@
 
 namespace convfwd {
 
-template <typename E, bool PT, bool QT, int BR, int BC, int WVR, int WVC, bool DMA, bool GATED>
+template <typename E, bool PT, bool QT, int BR, int BC, int WVR, int WVC, bool DMA, bool GATED,
+          typename O = E>
 static hipError_t launch_tile(ProductArgs a, hipStream_t s) {
   a.ntr = (a.R + (GATED ? BR / 2 : BR) - 1) / (GATED ? BR / 2 : BR);
   a.ntc = (a.C + BC - 1) / BC;
   const int grid = a.ntr * a.ntc * a.nz * a.splits;
-  hipLaunchKernelGGL((linear_tile_kernel<E, PT, QT, BR, BC, WVR, WVC, DMA, GATED>), dim3(grid),
+  hipLaunchKernelGGL((linear_tile_kernel<E, PT, QT, BR, BC, WVR, WVC, DMA, GATED, O>), dim3(grid),
                      dim3(WVR * WVC * 64), 0, s, a);
   return hipGetLastError();
 }
 
-template <typename E, bool PT, bool QT, int BC, bool GATED>
+template <typename E, bool PT, bool QT, int BC, bool GATED, typename O = E>
 static hipError_t launch_pingpong(ProductArgs a, hipStream_t s) {
   constexpr int BR = GATED ? 128 : 256;
   a.ntr = (a.R + BR - 1) / BR;
   a.ntc = (a.C + BC - 1) / BC;
   const int grid = a.ntr * a.ntc * a.nz * a.splits;
-  hipLaunchKernelGGL((linear_pingpong_kernel<E, PT, QT, BC, GATED>), dim3(grid), dim3(512), 0, s, a);
+  hipLaunchKernelGGL((linear_pingpong_kernel<E, PT, QT, BC, GATED, O>), dim3(grid), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 
@@ -38,6 +39,19 @@ static hipError_t launch_layout(const ProductArgs& a, int tile, bool dma, hipStr
                : launch_tile<E, PT, QT, 64, 64, 2, 2, false, false>(a, s);
   return dma ? launch_tile<E, PT, QT, 128, 128, 2, 2, true, false>(a, s)
              : launch_tile<E, PT, QT, 128, 128, 2, 2, false, false>(a, s);
+}
+
+template <typename O>
+hipError_t launch_int8_product(const ProductArgs& a, int tile, bool dma, hipStream_t s) {
+  typedef signed char E;
+  if (dma) {
+    if (tile == TILE_256) return launch_pingpong<E, false, false, 256, false, O>(a, s);
+    if (tile == TILE_256X128) return launch_pingpong<E, false, false, 128, false, O>(a, s);
+    if (tile == TILE_64) return launch_tile<E, false, false, 64, 64, 2, 2, true, false, O>(a, s);
+    return launch_tile<E, false, false, 128, 128, 2, 2, true, false, O>(a, s);
+  }
+  if (tile == TILE_64) return launch_tile<E, false, false, 64, 64, 2, 2, false, false, O>(a, s);
+  return launch_tile<E, false, false, 128, 128, 2, 2, false, false, O>(a, s);
 }
 
 template <typename E>

@@ -40,15 +40,17 @@ namespace lin {
 
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
-template <typename E, bool PT, bool QT, int BC, bool GATED, bool PLAIN = false>
+template <typename E, bool PT, bool QT, int BC, bool GATED, bool PLAIN = false, typename O = E>
 struct PingPong {
-  static_assert(sizeof(E) == 2 && (BC == 256 || BC == 128), "16-bit operands");
+  static_assert(sizeof(E) <= 2 && (BC == 256 || BC == 128), "16-bit and 8-bit operands");
+  static_assert(sizeof(E) == 2 || (!PT && !QT && !GATED), "8-bit operands are k-major");
   static constexpr int NT = 512, HR = 128, HC = BC / 2;
   static constexpr int WVR = BC == 256 ? 2 : 4, WVC = 8 / WVR;  // waves along r and c
   static constexpr int WR = HR / WVR, WC = HC / WVC;  // a wave's part of a half
   static constexpr int NI = WR / 16, NJ = WC / 16;
   using TP = Tile<E, HR, PT, NT>;
   using TQ = Tile<E, HC, QT, NT>;
+  static constexpr int EB = TP::EB, EPC = TP::EPC, BKE = TP::BKE;
   static constexpr int SMEM = 4 * (TP::BYTES + TQ::BYTES);
   // an operand's four half tiles lie side by side, within an LDS instruction's
   // 64 KB offset of one address
@@ -78,12 +80,12 @@ struct PingPong {
     const int t_all = a.ktiles * a.nseg;
     const int t0 = split * a.per_split, t1 = min(t0 + a.per_split, t_all);
 
-    mfma_f32x4 acc[2][2][NI][NJ];
+    Sums<E> acc[2][2][NI][NJ];
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
-        acc[0][0][i][j] = acc[0][1][i][j] = acc[1][0][i][j] = acc[1][1][i][j] = mfma_f32x4{0, 0, 0, 0};
+        acc[0][0][i][j] = acc[0][1][i][j] = acc[1][0][i][j] = acc[1][1][i][j] = Sums<E>{0, 0, 0, 0};
 
     // byte offsets of this thread's pieces in a half; the piece's k, alike for all
     int poff[TP::ITEMS], qoff[TQ::ITEMS], pk, qk;
@@ -109,15 +111,16 @@ struct PingPong {
     // last valid row (transposed: the last valid k), so that everything past an end
     // reads as zeros; it is empty past the last step and past the operand's rows.
     constexpr int kNone = -(1 << 30);
-    const int ldpb = (int)a.ldp * 2, ldqb = (int)a.ldq * 2;
+    const int ldpb = (int)a.ldp * EB, ldqb = (int)a.ldq * EB;
     const int seg0 = t0 >= a.ktiles ? 1 : 0, kt0 = t0 - (seg0 ? a.ktiles : 0);
-    const long long pstep = PT ? 64LL * ldpb : 128, qstep = QT ? 64LL * ldqb : 128;
+    const long long pstep = PT ? (long long)BKE * ldpb : 128, qstep = QT ? (long long)BKE * ldqb : 128;
+    auto up = [](int n) { return (n + EPC - 1) / EPC * EPC * EB; };  // bytes of whole pieces
     const char *pb[2], *qb[2], *pseg[2], *qseg[2];  // present, and of the second segment
     int pspan[2], qspan[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const long long pr = r0 + (GATED ? 0 : h * HR), qr = c0 + h * HC;
-      const long long po = PT ? pr * 2 : pr * ldpb, qo = QT ? qr * 2 : qr * ldqb;
+      const long long po = PT ? pr * EB : pr * ldpb, qo = QT ? qr * EB : qr * ldqb;
       pseg[h] = static_cast<const char*>(a.P[1]) + po;
       qseg[h] = static_cast<const char*>(a.Q[1]) + qo;
       pb[h] = (GATED ? h : seg0) ? pseg[h] : static_cast<const char*>(a.P[0]) + po;
@@ -125,24 +128,24 @@ struct PingPong {
       pb[h] += kt0 * pstep;
       qb[h] += kt0 * qstep;
       const int np = (int)min(a.R - pr, (long long)HR), nq = (int)min(a.C - qr, (long long)HC);
-      pspan[h] = np <= 0 ? kNone : PT ? ((np + 7) & ~7) * 2 : (np - 1) * ldpb;
-      qspan[h] = nq <= 0 ? kNone : QT ? ((nq + 7) & ~7) * 2 : (nq - 1) * ldqb;
+      pspan[h] = np <= 0 ? kNone : PT ? up(np) : (np - 1) * ldpb;
+      qspan[h] = nq <= 0 ? kNone : QT ? up(nq) : (nq - 1) * ldqb;
     }
-    int count = t0, left = a.K - kt0 * 64, kk, pbytes, qbytes;
-    const int ktail = a.K - (a.K - 1) / 64 * 64;  // k of a segment's last step
+    int count = t0, left = a.K - kt0 * BKE, kk, pbytes, qbytes;
+    const int ktail = a.K - (a.K - 1) / BKE * BKE;  // k of a segment's last step
     const bool ptail = PT || pk < ktail, qtail = QT || qk < ktail;
     bool turn = false;
     auto stage = [&](int n) {
       if (n == 0) {
         ++count;
         turn = !GATED && count == a.ktiles;
-        left = turn ? a.K : left - 64;
+        left = turn ? a.K : left - BKE;
       } else if (n == 1) {
-        kk = count < t1 ? min(left, 64) : kNone;
+        kk = count < t1 ? min(left, BKE) : kNone;
       } else if (n == 2) {
-        pbytes = kk < 0 ? kNone : PT ? (kk - 1) * ldpb : ((kk + 7) & ~7) * 2;
+        pbytes = kk < 0 ? kNone : PT ? (kk - 1) * ldpb : up(kk);
       } else if (n == 3) {
-        qbytes = kk < 0 ? kNone : QT ? (kk - 1) * ldqb : ((kk + 7) & ~7) * 2;
+        qbytes = kk < 0 ? kNone : QT ? (kk - 1) * ldqb : up(kk);
       } else if (n < 6) {
         pb[n - 4] = turn ? pseg[n - 4] : pb[n - 4] + pstep;
       } else {
@@ -151,14 +154,14 @@ struct PingPong {
     };
     auto issue_p = [&](int half, int buf) {
       const i32x4 rs = make_rsrc(pb[half], max(pspan[half] + pbytes, 0));
-      const bool all = kk >= 64 || ptail;
+      const bool all = kk >= BKE || ptail;
 #pragma unroll
       for (int i = 0; i < TP::ITEMS; ++i)
         dma16(rs, all ? poff[i] : kOob, lds0 + p_at(half, buf) + i * NT * 16);
     };
     auto issue_q = [&](int half, int buf) {
       const i32x4 rs = make_rsrc(qb[half], max(qspan[half] + qbytes, 0));
-      const bool all = kk >= 64 || qtail;
+      const bool all = kk >= BKE || qtail;
 #pragma unroll
       for (int i = 0; i < TQ::ITEMS; ++i)
         dma16(rs, all ? qoff[i] : kOob, lds0 + q_at(half, buf) + i * NT * 16);
@@ -223,7 +226,7 @@ struct PingPong {
 
 #pragma unroll
     for (int n = 1; n < 4; ++n) {
-      if (n == 1) kk = min(left, 64);
+      if (n == 1) kk = min(left, BKE);
       else stage(n);
     }
     issue_first(0);
@@ -269,7 +272,9 @@ struct PingPong {
 #pragma unroll
           for (int i = 0; i < NR; ++i) {
             const int h = GATED ? 0 : i / (NI / 2), b = i % (NI / 2) * 2;
-            runs_of_8(acc[h][n / NJ][b][n % NJ], acc[h][n / NJ][b + 1][n % NJ], v + i * 8);
+            const bool raw = !PLAIN && a.splits > 1;
+            runs_of_8(as_floats<E>(acc[h][n / NJ][b][n % NJ], raw),
+                      as_floats<E>(acc[h][n / NJ][b + 1][n % NJ], raw), v + i * 8);
             if constexpr (GATED)
               runs_of_8(acc[1][n / NJ][b][n % NJ], acc[1][n / NJ][b + 1][n % NJ], u + i * 8);
           }
@@ -293,7 +298,7 @@ struct PingPong {
       } else if constexpr (GATED) {
         finish_gated_runs<E, NR>(a.e, c, in, rl, off, whole, v, u);
       } else {
-        finish_linear_runs<E, NR>(a.e, z, c, in, rl, off, whole, v);
+        finish_linear_runs<O, NR, sizeof(E) == 1>(a.e, z, c, in, rl, off, whole, v);
       }
     }
   }
@@ -301,9 +306,9 @@ struct PingPong {
 
 }  // namespace lin
 
-template <typename E, bool PT, bool QT, int BC, bool GATED>
+template <typename E, bool PT, bool QT, int BC, bool GATED, typename O = E>
 __global__ __launch_bounds__(512) void linear_pingpong_kernel(const ProductArgs a) {
-  using K = lin::PingPong<E, PT, QT, BC, GATED>;
+  using K = lin::PingPong<E, PT, QT, BC, GATED, false, O>;
   __shared__ __attribute__((aligned(1024))) char smem[K::SMEM];
   K::run(a, xcd_logical(blockIdx.x, gridDim.x), smem);
 }

@@ -215,7 +215,7 @@ ProductPlan plan_product(const ProductShape& s, int es) {
   pl.per_split = all;
   // the cheapest tile and split count by the model of the measured times
   const Tiling* table = es == 4 ? kTiles32 : s.aligned ? kTiles16 : kTiles16Gather;
-  const int count = es == 2 && s.aligned ? 4 : 2;
+  const int count = es <= 2 && s.aligned ? 4 : 2;
   const int64_t plane_ld = round_up(s.R, 8);
   const int64_t plane = plane_ld * s.C * 4 * (s.gated ? 2 : 1) * s.nz;  // bytes of one
   double best = 0.0;
@@ -447,6 +447,17 @@ LinearPlan plan_linear(const linear_problem* p, const LinearGeo& g) {
   return o;
 }
 
+LinearPlan plan_int8(int64_t m, int64_t n, int64_t k, int64_t ldx, int64_t ldw, int64_t x_off,
+                     int64_t w_off) {
+  LinearPlan o{};
+  o.pack.n = 2;
+  o.pack.item[0] = item_of(m, k, ldx, x_off, 1);
+  o.pack.item[1] = item_of(n, k, ldw, w_off, 1);
+  o.product = {n, m, k, 1, 1, false, false, false, !any_needed(o.pack)};
+  o.planes = settle(&o.product, &o.run, &o.pack, 1, &o.total);
+  return o;
+}
+
 GatedPlan plan_gated(const gated_problem* p, const GatedGeo& g) {
   GatedPlan o{};
   o.pack.n = 3;
@@ -502,8 +513,6 @@ BackwardPlan plan_gated_backward(const gated_problem* p, const GatedGeo& g) {
   return o;
 }
 
-namespace {
-
 void product_name(const ProductPlan& pl, char* buf, size_t len) {
   if (pl.tile == TILE_STREAM) {
     snprintf(buf, len, "stream%d.r%d", 16 * pl.stream_t, pl.stream_rows);
@@ -518,6 +527,8 @@ void product_name(const ProductPlan& pl, char* buf, size_t len) {
   else
     snprintf(buf, len, "%s", tile);
 }
+
+namespace {
 
 void backward_name(const char* call, int dtype, const BackwardPlan& pl, char* buf, size_t len) {
   const char* pack = pl.pack.on ? ".pack" : "";

@@ -5,6 +5,8 @@
 
 #include <stdint.h>
 
+#include <stddef.h>
+
 #include "linear.h"
 #include "plan.h"
 
@@ -120,9 +122,16 @@ struct BackwardPlan {
   BackwardScratch scratch;
 };
 LinearPlan plan_linear(const linear_problem* p, const LinearGeo& g);
+// Products of 8-bit operands (include/linear_int8.h): the same kernels and planes of
+// int32 sums; a contraction step is 128 bytes of every type, so the times are alike.
+LinearPlan plan_int8(int64_t m, int64_t n, int64_t k, int64_t ldx, int64_t ldw, int64_t x_off,
+                     int64_t w_off);
 GatedPlan plan_gated(const gated_problem* p, const GatedGeo& g);
 BackwardPlan plan_linear_backward(const linear_problem* p, const LinearGeo& g);
 BackwardPlan plan_gated_backward(const gated_problem* p, const GatedGeo& g);
+
+// A plan's part of a variant's name ("tile64x64.split4").
+void product_name(const ProductPlan& pl, char* buf, size_t len);
 
 // The checks of include/linear.h; a call that passes gets its geometry and plan.
 int linear_checked(const linear_problem* p, int dtype, const void* x, const void* w, const void* b,

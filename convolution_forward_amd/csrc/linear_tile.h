@@ -5,7 +5,8 @@
 //
 //  * A workgroup owns BR x BC outputs; P rows feed MFMA's A operand and Q rows
 //    its B operand, so a lane ends with 4 consecutive r of one c.
-//  * Contraction step: 128 bytes of k (64 halves, 32 floats).  Both operands are
+//  * Contraction step: 128 bytes of k (64 halves, 32 floats, 128 elements of 8 bits;
+//    those are k-major only, with int32 sums and outputs of another type O).  Both operands are
 //    staged in LDS, in two buffers (small tiles: three); the next step (two) is in
 //    flight while one is multiplied.
 //  * DMA: global to LDS directly (16 bytes a lane, no registers), for rows of
@@ -119,8 +120,8 @@ struct Tile {
   }
 
   // A 16-row fragment at row0 (a multiple of 16), 64 bytes of k (16-bit: 32 k,
-  // float32: 16 k; lane group g holds k 8g.. or 4g..), step half j.
-  typedef std::conditional_t<EB == 2, s16x8, f32x4> Frag;
+  // float32: 16 k; lane group g holds k 8g.. or 4g..; 8-bit: 64 k, 16g..), step half j.
+  typedef std::conditional_t<EB == 1, i32x4, std::conditional_t<EB == 2, s16x8, f32x4>> Frag;
   static __device__ __forceinline__ Frag frag(const char* base, int row0, int j, int lane) {
     const int l = lane & 15, g = lane >> 4;
     if constexpr (!T) {
@@ -145,9 +146,15 @@ struct Tile {
   }
 };
 
+// Sums of a 16 x 16 block: four a lane.
+template <typename E>
+using Sums = std::conditional_t<sizeof(E) == 1, i32x4, mfma_f32x4>;
+
 template <typename E, typename F>
-__device__ __forceinline__ mfma_f32x4 multiply(const F& p, const F& q, mfma_f32x4 c) {
-  if constexpr (sizeof(E) == 2) {
+__device__ __forceinline__ Sums<E> multiply(const F& p, const F& q, Sums<E> c) {
+  if constexpr (sizeof(E) == 1) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(p, q, c, 0, 0, 0);
+  } else if constexpr (sizeof(E) == 2) {
     return mfma_16x16x32<E>(p, q, c);
   } else {
 #pragma unroll
@@ -156,18 +163,36 @@ __device__ __forceinline__ mfma_f32x4 multiply(const F& p, const F& q, mfma_f32x
   }
 }
 
+// Sums as floats for runs_of_8: integer sums by their values, or, raw, by their bits.
+template <typename E>
+__device__ __forceinline__ mfma_f32x4 as_floats(const Sums<E>& s, bool raw) {
+  if constexpr (sizeof(E) == 1) {
+    mfma_f32x4 f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int v = s[i];
+      f[i] = raw ? __builtin_bit_cast(float, v) : (float)v;
+    }
+    return f;
+  } else {
+    return s;
+  }
+}
+
 // 16 bytes at base + off, aligned to their elements.  The card reads 16 bytes at a
-// multiple of 4 at full speed, at an odd multiple of 2 at less than half: those come
-// as the five words around them (a word that holds an element is on its page).
+// multiple of 4 at full speed, elsewhere at less than half: those come as the five
+// words around them (a word that holds an element is on its page).
 template <typename E>
 __device__ __forceinline__ i32x4 load_piece(const char* base, int off) {
   typedef i32x4 A4 __attribute__((aligned(4)));
   if constexpr (sizeof(E) == 4) {
     return *reinterpret_cast<const A4*>(base + off);
   } else {
-    const int odd = ((int)reinterpret_cast<unsigned long long>(base) + off) & 2;
+    constexpr int PAST = 4 - (int)sizeof(E);  // largest distance from a multiple of 4
+    const int odd = ((int)reinterpret_cast<unsigned long long>(base) + off) & PAST;
     const i32x4 v = *reinterpret_cast<const A4*>(base + (off - odd));
-    const int w = *reinterpret_cast<const int*>(base + (off + odd + 12));
+    const int last = sizeof(E) == 2 ? off + odd + 12 : off - odd + (odd ? 16 : 12);
+    const int w = *reinterpret_cast<const int*>(base + last);
     i32x4 o;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -226,8 +251,9 @@ struct Ragged {
 }  // namespace lin
 
 // WVR x WVC waves; GATED: P's rows are gate and up rows, side by side within
-// each wave's share.
-template <typename E, bool PT, bool QT, int BR, int BC, int WVR, int WVC, bool DMA, bool GATED>
+// each wave's share.  O: the outputs' type.
+template <typename E, bool PT, bool QT, int BR, int BC, int WVR, int WVC, bool DMA, bool GATED,
+          typename O = E>
 struct LinearTile {
   static constexpr int NT = WVR * WVC * 64;
   static constexpr int STAGE = lin::Tile<E, BR, PT, NT>::BYTES + lin::Tile<E, BC, QT, NT>::BYTES;
@@ -244,6 +270,7 @@ static __device__ __forceinline__ void run(const ProductArgs& a, const int id, c
   using TP = Tile<E, BR, PT, NT>;
   using TQ = Tile<E, BC, QT, NT>;
   static_assert(!GATED || (!PT && !QT), "gated weights are k-major");
+  static_assert(sizeof(E) > 1 || (!GATED && !PT && !QT), "8-bit operands are k-major");
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -265,11 +292,11 @@ static __device__ __forceinline__ void run(const ProductArgs& a, const int id, c
   const int t_all = a.ktiles * a.nseg;
   const int t0 = split * a.per_split, t1 = min(t0 + a.per_split, t_all);
 
-  mfma_f32x4 acc[NI][NJ];
+  Sums<E> acc[NI][NJ];
 #pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_f32x4{0, 0, 0, 0};
+    for (int j = 0; j < NJ; ++j) acc[i][j] = Sums<E>{0, 0, 0, 0};
 
   // byte offsets of this thread's pieces, constant over the contraction; the piece's
   // k, alike for all
@@ -496,7 +523,8 @@ static __device__ __forceinline__ void run(const ProductArgs& a, const int id, c
     float v[NR * 8], u[GATED ? NR * 8 : 1];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      runs_of_8(acc[2 * i][j], acc[2 * i + 1][j], v + i * 8);
+      runs_of_8(as_floats<E>(acc[2 * i][j], a.splits > 1),
+                as_floats<E>(acc[2 * i + 1][j], a.splits > 1), v + i * 8);
       if constexpr (GATED) runs_of_8(acc[NI / 2 + 2 * i][j], acc[NI / 2 + 2 * i + 1][j], u + i * 8);
     }
     const long long c = c0 + wc * WC + j * 16 + (lane & 15);
@@ -516,15 +544,16 @@ static __device__ __forceinline__ void run(const ProductArgs& a, const int id, c
     } else if constexpr (GATED) {
       finish_gated_runs<E, NR>(a.e, c, in, rl, off, whole, v, u);
     } else {
-      finish_linear_runs<E, NR>(a.e, z, c, in, rl, off, whole, v);
+      finish_linear_runs<O, NR, sizeof(E) == 1>(a.e, z, c, in, rl, off, whole, v);
     }
   }
 }
 };
 
-template <typename E, bool PT, bool QT, int BR, int BC, int WVR, int WVC, bool DMA, bool GATED>
+template <typename E, bool PT, bool QT, int BR, int BC, int WVR, int WVC, bool DMA, bool GATED,
+          typename O = E>
 __global__ __launch_bounds__(WVR * WVC * 64) void linear_tile_kernel(const ProductArgs a) {
-  using K = LinearTile<E, PT, QT, BR, BC, WVR, WVC, DMA, GATED>;
+  using K = LinearTile<E, PT, QT, BR, BC, WVR, WVC, DMA, GATED, O>;
   __shared__ __attribute__((aligned(1024))) char smem[K::SMEM];
   K::run(a, xcd_logical(blockIdx.x, gridDim.x), smem);
 }

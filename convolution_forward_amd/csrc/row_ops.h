@@ -1,0 +1,242 @@
+// Device pieces shared by the row operators: sums over the threads of a row, and the
+// dropout mask (include/dropout.h).  A row is cut into runs of 8 consecutive elements;
+// run i of a row belongs to thread i mod T of the T threads that hold it.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "linear_epilogue.h"
+
+namespace convfwd {
+
+// Sum over the 64 lanes, the same in every lane: four steps within rows of 16 (lanes
+// paired by 1, 2, and mirrored halves and rows), two between them by lane swaps; no LDS.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL,
+                                                               0xf, 0xf, true));
+}
+template <typename F>
+__device__ __forceinline__ float wave_join(float v, F f) {
+  v = f(v, dpp<0xB1>(v));   // lane ^ 1
+  v = f(v, dpp<0x4E>(v));   // lane ^ 2
+  v = f(v, dpp<0x141>(v));  // mirrored within 8
+  v = f(v, dpp<0x140>(v));  // mirrored within 16
+  const unsigned u = __builtin_bit_cast(unsigned, v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const unsigned a0 = a[0], a1 = a[1];
+  v = f(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1));
+  const unsigned w = __builtin_bit_cast(unsigned, v);
+  const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  const unsigned b0 = b[0], b1 = b[1];
+  return f(__builtin_bit_cast(float, b0), __builtin_bit_cast(float, b1));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  return wave_join(v, [](float a, float b) { return a + b; });
+}
+
+// Sum over the T threads of a workgroup that hold a row (T = 64: one wave, no barrier).
+// Two calls in turn need two arrays: a wave may be a call ahead, never two.
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float* lds) {
+  v = wave_sum(v);
+  if constexpr (T > 64) {
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < T / 64; ++i) v += lds[i];
+  }
+  return v;
+}
+
+// The numbers of a mask, see include/dropout.h.
+struct DropArgs {
+  unsigned threshold;  // 0: no dropout
+  float scale;
+  unsigned key0, key1;
+  unsigned long long offset;
+  const unsigned long long* step;
+};
+
+struct DropCounter {
+  unsigned lo, hi;
+};
+__device__ __forceinline__ DropCounter drop_counter(const DropArgs& a) {
+  const unsigned long long c = a.offset + (a.step ? *a.step : 0);
+  return {(unsigned)c, (unsigned)(c >> 32)};
+}
+
+// Philox4x32-10: 8 numbers of 16 bits for run `run` of row `row`.  20 products of 32
+// bits (low and high half from one instruction) and 40 logic operations for 8 elements.
+struct DropBits {
+  unsigned w[4];
+};
+__device__ __forceinline__ DropBits drop_bits(const DropArgs& a, DropCounter c, unsigned run,
+                                              unsigned row) {
+  unsigned x0 = run, x1 = row, x2 = c.lo, x3 = c.hi, k0 = a.key0, k1 = a.key1;
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const unsigned long long p = (unsigned long long)x0 * 0xD2511F53u;
+    const unsigned long long q = (unsigned long long)x2 * 0xCD9E8D57u;
+    x0 = (unsigned)(q >> 32) ^ x1 ^ k0;
+    x1 = (unsigned)q;
+    x2 = (unsigned)(p >> 32) ^ x3 ^ k1;
+    x3 = (unsigned)p;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return {{x0, x1, x2, x3}};
+}
+
+__device__ __forceinline__ bool drop_keeps(const DropBits& b, int e, unsigned threshold) {
+  const unsigned u = e & 1 ? b.w[e >> 1] >> 16 : b.w[e >> 1] & 0xffffu;
+  return u >= threshold;
+}
+
+__device__ __forceinline__ void drop8(const DropArgs& a, DropCounter c, unsigned run, unsigned row,
+                                      float (&v)[8]) {
+  const DropBits b = drop_bits(a, c, run, row);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = drop_keeps(b, e, a.threshold) ? v[e] * a.scale : 0.0f;
+}
+
+// Host side: the numbers of a problem.
+inline DropArgs drop_args(int threshold, uint64_t seed, uint64_t offset, const void* step) {
+  DropArgs a;
+  a.threshold = (unsigned)threshold;
+  a.scale = threshold < 65536 ? (float)(65536.0 / (65536 - threshold)) : 0.0f;
+  a.key0 = (unsigned)seed;
+  a.key1 = (unsigned)(seed >> 32);
+  a.offset = offset;
+  a.step = static_cast<const unsigned long long*>(step);
+  return a;
+}
+
+// A run of 8 elements in memory as it is held: two pieces of 16 bytes of float32, one of
+// 16 bits, from any element's address on.
+template <typename E>
+__device__ __forceinline__ void unpack(const Eight<E>& q, float (&v)[8]) {
+  constexpr int W = 16 / (int)sizeof(E);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = (float)q.q[e / W][e % W];
+}
+
+// A few elements at any element's address.
+template <typename E, int N>
+struct __attribute__((packed, aligned(sizeof(E)))) Few {
+  typedef E vec __attribute__((ext_vector_type(N)));
+  vec v;
+};
+
+// The last, partial run of a row, 1 <= left <= 7 elements at p: pieces of 4, 2 and 1,
+// zeros behind them.  Nothing past the end is read.
+template <typename E>
+__device__ __forceinline__ void load_tail(const E* p, int left, float (&v)[8]) {
+  float q[4] = {0, 0, 0, 0}, d[2] = {0, 0}, s = 0;
+  const bool has4 = left & 4, has2 = left & 2;
+  if (has4) {
+    const auto f = reinterpret_cast<const Few<E, 4>*>(p)->v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = (float)f[e];
+  }
+  if (has2) {
+    const auto f = reinterpret_cast<const Few<E, 2>*>(p + (left & 4))->v;
+    d[0] = (float)f[0];
+    d[1] = (float)f[1];
+  }
+  if (left & 1) s = (float)p[left & 6];
+  const float d0 = d[0], d1 = d[1], rest[4] = {has2 ? d0 : s, has2 ? d1 : 0.0f, has2 ? s : 0.0f, 0.0f};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float four = q[e], behind = rest[e];
+    v[e] = has4 ? four : behind;
+    v[4 + e] = has4 ? behind : 0.0f;
+  }
+}
+template <typename E>
+__device__ __forceinline__ void store_tail(E* p, int left, const float (&v)[8]) {
+  const bool has4 = left & 4, has2 = left & 2;
+  if (has4) {
+    typename Few<E, 4>::vec f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = (E)v[e];
+    reinterpret_cast<Few<E, 4>*>(p)->v = f;
+  }
+  float r[3];
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+    const float near = v[e], far = v[4 + e];  // values: a choice of places would need memory
+    r[e] = has4 ? far : near;
+  }
+  if (has2) {
+    typename Few<E, 2>::vec f;
+    f[0] = (E)r[0];
+    f[1] = (E)r[1];
+    reinterpret_cast<Few<E, 2>*>(p + (left & 4))->v = f;
+  }
+  const float first = r[0], last = r[2];
+  if (left & 1) p[left & 6] = (E)(has2 ? last : first);
+}
+
+// Runs run0, run0 + T, .. of a row of n elements at p; zeros past its end.  The partial
+// run, which is one thread's at the same u for all, is loaded once.
+template <int T, int U, typename E>
+__device__ __forceinline__ void load_runs(const E* p, int n, int run0, float (&v)[U][8]) {
+  const int whole = n >> 3;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int run = run0 + u * T;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[u][e] = 0.0f;
+    if (run < whole) unpack(*reinterpret_cast<const Eight<E>*>(p + run * 8), v[u]);
+  }
+  if (n & 7) {
+    if ((whole - run0) % T == 0 && whole >= run0 && whole < run0 + T * U) {
+      float t[8];
+      load_tail(p + whole * 8, n & 7, t);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float here = t[e], other = v[u][e];
+          v[u][e] = run0 + u * T == whole ? here : other;
+        }
+    }
+  }
+}
+template <int T, int U, typename E>
+__device__ __forceinline__ void store_runs(E* p, int n, int run0, const float (&v)[U][8]) {
+  const int whole = n >> 3;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int run = run0 + u * T;
+    if (run < whole) store8(p + run * 8, 8, v[u]);
+  }
+  if (n & 7) {
+    if ((whole - run0) % T == 0 && whole >= run0 && whole < run0 + T * U) {
+      float t[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] = v[0][e];
+#pragma unroll
+      for (int u = 1; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float here = v[u][e], other = t[e];
+          t[e] = run0 + u * T == whole ? here : other;
+        }
+      store_tail(p + whole * 8, n & 7, t);
+    }
+  }
+}
+
+template <typename E>
+inline const E* elements(const void* p, int64_t off) {
+  return p ? static_cast<const E*>(p) + off : nullptr;
+}
+template <typename E>
+inline E* elements(void* p, int64_t off) {
+  return p ? static_cast<E*>(p) + off : nullptr;
+}
+
+}  // namespace convfwd
