@@ -3,8 +3,8 @@
 //
 // Rows up to 32768 elements are held in registers by T threads, U runs of 8 each, so
 // that mean and variance are two sums over registers (the second of squared distances,
-// which does not cancel).  Short rows take a wave each, four to a workgroup, with no
-// barrier.  Longer rows go in two launches: a mean and a sum of squared distances for
+// which does not cancel).  Short rows take 8 to 64 lanes of a wave, several to a
+// workgroup, with no barrier.  Longer rows go in two launches: a mean and a sum of squared distances for
 // each part of 8192 elements, then every part joins those of its row (Chan, Golub and
 // LeVeque's formula for the variance of joined samples) and normalises.
 #include <algorithm>
@@ -30,19 +30,42 @@ struct NormArgs {
   int nparts;
 };
 
-// s = r + drop(x) of the runs run0, run0 + T, ... of a row; elements past n are 0 (with
-// or without the mask).
+// Everything that a thread reads for its runs run0, run0 + T, .. of a row, all in flight
+// before the first is used; w and b only where there are registers to spare (HOLD).
+template <typename E, int T, int U>
+struct Loads {
+  static constexpr bool HOLD = T * U <= 1024 && U < 4;
+  Runs<E, T, U> x, r, w, b;
+  __device__ __forceinline__ void fetch(const NormArgs<E>& a, long long row, int run0, bool params) {
+    x.clear();
+    x.fetch(a.x + row * a.ldx, a.n, run0);
+    if (a.r) {
+      r.clear();
+      r.fetch(a.r + row * a.ldr, a.n, run0);
+    }
+    if (HOLD && params && a.w) {
+      w.clear();
+      w.fetch(a.w, a.n, run0);
+    }
+    if (HOLD && params && a.b) {
+      b.clear();
+      b.fetch(a.b, a.n, run0);
+    }
+  }
+};
+
+// s = r + drop(x); elements past n are 0 (with or without the mask).
 template <typename E, int T, int U, bool DROP>
-__device__ __forceinline__ void load_row(const NormArgs<E>& a, DropCounter c, long long row,
-                                         int run0, float (&v)[U][8]) {
-  float t[U][8];
-  load_runs<T>(a.x + row * a.ldx, a.n, run0, v);
-  if (a.r) load_runs<T>(a.r + row * a.ldr, a.n, run0, t);
+__device__ __forceinline__ void join_row(const NormArgs<E>& a, const Loads<E, T, U>& l,
+                                         DropCounter c, long long row, int run0, float (&v)[U][8]) {
+  l.x.get(a.n, run0, v);
   if constexpr (DROP) {
 #pragma unroll
     for (int u = 0; u < U; ++u) drop8(a.d, c, run0 + u * T, (unsigned)row, v[u]);
   }
   if (a.r) {
+    float t[U][8];
+    l.r.get(a.n, run0, t);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -51,23 +74,25 @@ __device__ __forceinline__ void load_row(const NormArgs<E>& a, DropCounter c, lo
 }
 
 template <typename E, int T, int U>
-__device__ __forceinline__ void store_row(const NormArgs<E>& a, long long row, int run0, float mean,
-                                          float rstd, float (&v)[U][8]) {
-  if (a.s) store_runs<T>(a.s + row * a.lds, a.n, run0, v);
+__device__ __forceinline__ void store_row(const NormArgs<E>& a, const Loads<E, T, U>& l,
+                                          long long row, int run0, float mean, float rstd,
+                                          float (&v)[U][8]) {
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[u][e] = (v[u][e] - mean) * rstd;
   float t[U][8];
   if (a.w) {
-    load_runs<T>(a.w, a.n, run0, t);
+    if constexpr (Loads<E, T, U>::HOLD) l.w.get(a.n, run0, t);
+    else load_runs<T>(a.w, a.n, run0, t);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[u][e] *= t[u][e];
   }
   if (a.b) {
-    load_runs<T>(a.b, a.n, run0, t);
+    if constexpr (Loads<E, T, U>::HOLD) l.b.get(a.n, run0, t);
+    else load_runs<T>(a.b, a.n, run0, t);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -116,15 +141,17 @@ __device__ __forceinline__ float total(const float (&v)[U][8]) {
 }
 
 template <typename E, int T, int U, bool DROP>
-__global__ __launch_bounds__(T == 64 ? 256 : T) void layer_norm_rows_kernel(const NormArgs<E> a) {
-  constexpr int TEAMS = T == 64 ? 4 : 1;
-  __shared__ float lds[2][T / 64];
-  const int t = threadIdx.x % T, team = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
-  const DropCounter c = DROP ? drop_counter(a.d) : DropCounter{0, 0};
-  const long long row = a.row0 + (long long)blockIdx.x * TEAMS + team;
+__global__ __launch_bounds__(T* teams_of(T)) void layer_norm_rows_kernel(const NormArgs<E> a) {
+  __shared__ float lds[2][waves_of(T)];
+  const int t = threadIdx.x % T;
+  const long long row = a.row0 + (long long)blockIdx.x * teams_of(T) + team_of<T>();
   if (row >= a.m) return;
+  Loads<E, T, U> l;
+  l.fetch(a, row, t, true);
+  const DropCounter c = DROP ? drop_counter(a.d) : DropCounter{0, 0};
   float v[U][8];
-  load_row<E, T, U, DROP>(a, c, row, t, v);
+  join_row<E, T, U, DROP>(a, l, c, row, t, v);
+  if (a.s) store_runs<T>(a.s + row * a.lds, a.n, t, v);
   // quotients, not products with 1 / n: a row of equal values has its value as mean
   const float mean = row_sum<T>(total(v), lds[0]) / (float)a.n;
   const float var = row_sum<T>(spread<T>(v, t, a.n, mean), lds[1]) / (float)a.n;
@@ -133,7 +160,7 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void layer_norm_rows_kernel(cons
     a.mean[row] = mean;
     a.rstd[row] = rstd;
   }
-  store_row<E, T, U>(a, row, t, mean, rstd, v);
+  store_row<E, T, U>(a, l, row, t, mean, rstd, v);
 }
 
 constexpr int kPart = 8192;  // elements of a part: 256 threads, 4 runs each
@@ -147,7 +174,9 @@ __global__ __launch_bounds__(256) void layer_norm_parts_kernel(const NormArgs<E>
   const long long row = a.row0 + local;
   const int run0 = part * (kPart / 8) + threadIdx.x, count = min(kPart, a.n - part * kPart);
   float v[4][8];
-  load_row<E, 256, 4, DROP>(a, c, row, run0, v);
+  Loads<E, 256, 4> l;
+  l.fetch(a, row, run0, false);
+  join_row<E, 256, 4, DROP>(a, l, c, row, run0, v);
   const float mean = row_sum<256>(total(v), lds[0]) / (float)count;
   const float q = row_sum<256>(spread<256>(v, run0, a.n, mean), lds[1]);
   if (threadIdx.x == 0) a.parts[row * a.nparts + part] = make_float2(mean, q);
@@ -161,7 +190,8 @@ __global__ __launch_bounds__(256) void layer_norm_joined_kernel(const NormArgs<E
   const long long row = a.row0 + local;
   const int run0 = part * (kPart / 8) + threadIdx.x;
   float v[4][8];
-  load_row<E, 256, 4, DROP>(a, c, row, run0, v);
+  Loads<E, 256, 4> l;
+  l.fetch(a, row, run0, true);
   // every wave joins the row's parts (128 at most, two a lane)
   const float2* p = a.parts + row * a.nparts;
   float2 q[2];
@@ -184,7 +214,9 @@ __global__ __launch_bounds__(256) void layer_norm_joined_kernel(const NormArgs<E
     a.mean[row] = mean;
     a.rstd[row] = rstd;
   }
-  store_row<E, 256, 4>(a, row, run0, mean, rstd, v);
+  join_row<E, 256, 4, DROP>(a, l, c, row, run0, v);
+  if (a.s) store_runs<256>(a.s + row * a.lds, a.n, run0, v);
+  store_row<E, 256, 4>(a, l, row, run0, mean, rstd, v);
 }
 
 // Rows go in launches of fewer than 2^32 work-items.
@@ -205,7 +237,7 @@ hipError_t by_rows(NormArgs<E> a, long long each, F f) {
 
 template <typename E, int T, int U>
 hipError_t launch_rows(const NormArgs<E>& args, hipStream_t s) {
-  constexpr int TEAMS = T == 64 ? 4 : 1;
+  constexpr int TEAMS = teams_of(T);
   return by_rows(args, T, [&](const NormArgs<E>& a, unsigned rows) {
     const dim3 grid((rows + TEAMS - 1) / TEAMS), block(T * TEAMS);
     if (a.d.threshold) hipLaunchKernelGGL((layer_norm_rows_kernel<E, T, U, true>), grid, block, 0, s, a);
@@ -231,13 +263,17 @@ hipError_t launch_parts(const NormArgs<E>& args, hipStream_t s) {
 template <typename E>
 hipError_t norm(const NormArgs<E>& a, const RowPlan& pl, hipStream_t s) {
   if (pl.parts) return launch_parts(a, s);
-  if (pl.threads == 64)
-    return pl.runs == 1   ? launch_rows<E, 64, 1>(a, s)
-           : pl.runs == 2 ? launch_rows<E, 64, 2>(a, s)
-                          : launch_rows<E, 64, 4>(a, s);
-  if (pl.threads == 256)
-    return pl.runs == 2 ? launch_rows<E, 256, 2>(a, s) : launch_rows<E, 256, 4>(a, s);
-  return pl.runs == 2 ? launch_rows<E, 1024, 2>(a, s) : launch_rows<E, 1024, 4>(a, s);
+  switch (pl.threads) {
+    case 8: return launch_rows<E, 8, 1>(a, s);
+    case 16: return launch_rows<E, 16, 1>(a, s);
+    case 32: return launch_rows<E, 32, 1>(a, s);
+    case 64: return pl.runs == 1 ? launch_rows<E, 64, 1>(a, s) : launch_rows<E, 64, 2>(a, s);
+    case 256: return pl.runs == 1 ? launch_rows<E, 256, 1>(a, s) : launch_rows<E, 256, 2>(a, s);
+    default:
+      return pl.runs == 1   ? launch_rows<E, 1024, 1>(a, s)
+             : pl.runs == 2 ? launch_rows<E, 1024, 2>(a, s)
+                            : launch_rows<E, 1024, 4>(a, s);
+  }
 }
 
 template <typename E>

@@ -6,7 +6,7 @@
 // and a second kernel adds the partial rows in order.  So no atomics, and dy and s are
 // read once for both the row's gradient and the columns' sums.  A row needs two sums
 // (of g and of g u) before its first gradient: one exchange through LDS and one barrier
-// a row, none where a wave holds a row.  Rows of more than 16384 elements go in parts
+// a row, none where lanes of a wave hold it.  Rows of more than 8192 elements go in parts
 // of 2048, in two launches: the parts' sums, then the gradients.
 #include <algorithm>
 
@@ -32,18 +32,19 @@ struct GradArgs {
   DropArgs d;
 };
 
-// The gradient of s from u, g and the row's two means, and its stores.
+// The gradient of s from u, g and the row's two means (and ds), and its stores.
 template <typename E, int T, int U, bool DROP>
 __device__ __forceinline__ void finish_row(const GradArgs<E>& a, DropCounter c, long long row,
                                            int run0, float rstd, float along, float level,
-                                           const float (&u)[U][8], float (&g)[U][8]) {
+                                           const float (&u)[U][8], float (&g)[U][8],
+                                           const Runs<E, T, U>& ds) {
 #pragma unroll
   for (int k = 0; k < U; ++k)
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[k][e] = rstd * (g[k][e] - level - u[k][e] * along);
   if (a.ds) {
     float t[U][8];
-    load_runs<T>(a.ds + row * a.ldds, a.n, run0, t);
+    ds.get(a.n, run0, t);
 #pragma unroll
     for (int k = 0; k < U; ++k)
 #pragma unroll
@@ -59,13 +60,15 @@ __device__ __forceinline__ void finish_row(const GradArgs<E>& a, DropCounter c, 
   }
 }
 
-// T threads a row, U runs each; TEAMS rows at a time.
+// T threads a row, U runs each; TEAMS rows at a time.  The next row's loads are in
+// flight from before the present one's sums are exchanged (8192 x 4096 bf16: 73 us with
+// it, 108 without).
 template <typename E, int T, int U, int TEAMS, bool DROP>
 __global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_kernel(const GradArgs<E> a) {
-  constexpr int WAVES = T / 64;
+  constexpr int WAVES = waves_of(T);
   __shared__ float2 red[2][TEAMS * WAVES];
   __shared__ float columns[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? T * 8 : 1];
-  const int t = threadIdx.x % T, team = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
+  const int t = threadIdx.x % T, team = team_of<T>();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const DropCounter c = DROP ? drop_counter(a.d) : DropCounter{0, 0};
   float w[U][8], dw[U][8], db[U][8];
@@ -77,29 +80,45 @@ __global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_kernel(const GradArg
       dw[k][e] = db[k][e] = 0.0f;
     }
   if (a.w) load_runs<T>(a.w, a.n, t, w);
+  const long long stride = (long long)gridDim.x * TEAMS;
+  long long row = (long long)blockIdx.x * TEAMS + team;
+  Runs<E, T, U> s, dy, ds, ds_next;
+  s.clear();
+  dy.clear();
+  ds_next.clear();
+  float mean = 0.0f, rstd = 0.0f;
+  auto fetch = [&](long long at) {
+    s.fetch(a.s + at * a.lds, a.n, t);
+    dy.fetch(a.dy + at * a.lddy, a.n, t);
+    if (a.ds) ds_next.fetch(a.ds + at * a.ldds, a.n, t);
+    mean = a.mean[at];
+    rstd = a.rstd[at];
+  };
+  if (row < a.m) fetch(row);
   int buf = 0;
-  for (long long base = (long long)blockIdx.x * TEAMS; base < a.m; base += (long long)gridDim.x * TEAMS) {
-    const long long row = base + team;
-    const bool in = row < a.m;  // uniform in a wave; every wave reaches the barrier
-    float u[U][8], g[U][8], rstd = 0.0f, along = 0.0f, level = 0.0f;
+  for (long long base = (long long)blockIdx.x * TEAMS; base < a.m; base += stride, row += stride) {
+    const bool in = row < a.m;  // every wave reaches the barrier
+    float u[U][8], g[U][8], along = 0.0f, level = 0.0f;
+    const float r = rstd;
     if (in) {
-      load_runs<T>(a.s + row * a.lds, a.n, t, u);
-      load_runs<T>(a.dy + row * a.lddy, a.n, t, g);
-      const float mean = a.mean[row];
-      rstd = a.rstd[row];
+      s.get(a.n, t, u);
+      dy.get(a.n, t, g);
+      const float mu = mean;
+      ds = ds_next;
+      if (row + stride < a.m) fetch(row + stride);
 #pragma unroll
       for (int k = 0; k < U; ++k)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          u[k][e] = (u[k][e] - mean) * rstd;
+          u[k][e] = (u[k][e] - mu) * r;
           dw[k][e] = fmaf(g[k][e], u[k][e], dw[k][e]);
           db[k][e] += g[k][e];
           g[k][e] *= w[k][e];
           along = fmaf(g[k][e], u[k][e], along);
           level += g[k][e];
         }
-      along = wave_sum(along);
-      level = wave_sum(level);
+      along = lanes_sum<T < 64 ? T : 64>(along);
+      level = lanes_sum<T < 64 ? T : 64>(level);
     }
     if constexpr (WAVES > 1) {
       if ((threadIdx.x & 63) == 0) red[buf][wave] = make_float2(along, level);
@@ -112,7 +131,7 @@ __global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_kernel(const GradArg
       }
       buf ^= 1;
     }
-    if (in) finish_row<E, T, U, DROP>(a, c, row, t, rstd, along * a.inv_n, level * a.inv_n, u, g);
+    if (in) finish_row<E, T, U, DROP>(a, c, row, t, r, along * a.inv_n, level * a.inv_n, u, g, ds);
   }
   if (!a.partials) return;
   float* p = a.partials + (long long)blockIdx.x * 2 * a.np;
@@ -136,10 +155,10 @@ __global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_kernel(const GradArg
       for (int i = threadIdx.x; i < T * 8; i += T * TEAMS) {
         const int at = k % U * T * 8 + i;
         if (at < a.np) {
-          float s = columns[0][i];
+          float q = columns[0][i];
 #pragma unroll
-          for (int j = 1; j < TEAMS; ++j) s += columns[j][i];
-          p[(k < U ? 0 : a.np) + at] = s;
+          for (int j = 1; j < TEAMS; ++j) q += columns[j][i];
+          p[(k < U ? 0 : a.np) + at] = q;
         }
       }
       __syncthreads();
@@ -190,8 +209,12 @@ __global__ __launch_bounds__(256) void layer_norm_grad_parts_kernel(const GradAr
     dw[e] = db[e] = 0.0f;
   }
   if (a.w) load_runs<kPartRuns>(a.w, a.n, run0, w);
-  for (long long row = group; row < a.m; row += groups) {
+  // from the last row back: what the sums read last is what the last-level cache holds
+  for (long long row = a.m - 1 - group; row >= 0; row -= groups) {
     float u[1][8], g[1][8], along = 0.0f, level = 0.0f;
+    Runs<E, kPartRuns, 1> ds;
+    ds.clear();
+    if (a.ds) ds.fetch(a.ds + row * a.ldds, a.n, run0);
     load_runs<kPartRuns>(a.s + row * a.lds, a.n, run0, u);
     load_runs<kPartRuns>(a.dy + row * a.lddy, a.n, run0, g);
     for (int i = lane; i < a.parts; i += 64) {
@@ -209,7 +232,7 @@ __global__ __launch_bounds__(256) void layer_norm_grad_parts_kernel(const GradAr
       db[e] += g[0][e];
       g[0][e] *= w[0][e];
     }
-    finish_row<E, kPartRuns, 1, DROP>(a, c, row, run0, rstd, along, level, u, g);
+    finish_row<E, kPartRuns, 1, DROP>(a, c, row, run0, rstd, along, level, u, g, ds);
   }
   if (!a.partials || run0 * 8 >= a.np) return;
   float* p = a.partials + (long long)group * 2 * a.np + run0 * 8;
@@ -253,12 +276,14 @@ __global__ __launch_bounds__(1024) void layer_norm_grad_join_kernel(const float*
   }
 }
 
-template <typename E, int T, int U, int TEAMS>
+template <typename E, int T, int U>
 void launch_grad(const GradArgs<E>& a, unsigned groups, hipStream_t s) {
+  constexpr int TEAMS = teams_of(T);
+  const dim3 grid(groups), block(T * TEAMS);
   if (a.d.threshold)
-    hipLaunchKernelGGL((layer_norm_grad_kernel<E, T, U, TEAMS, true>), dim3(groups), dim3(T * TEAMS), 0, s, a);
+    hipLaunchKernelGGL((layer_norm_grad_kernel<E, T, U, TEAMS, true>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((layer_norm_grad_kernel<E, T, U, TEAMS, false>), dim3(groups), dim3(T * TEAMS), 0, s, a);
+    hipLaunchKernelGGL((layer_norm_grad_kernel<E, T, U, TEAMS, false>), grid, block, 0, s, a);
 }
 
 template <typename E>
@@ -278,15 +303,20 @@ hipError_t grad(GradArgs<E>& a, const NormBackwardPlan& pl, E* dw, E* db, hipStr
       hipLaunchKernelGGL((layer_norm_grad_parts_kernel<E, true>), grid, dim3(256), 0, s, a);
     else
       hipLaunchKernelGGL((layer_norm_grad_parts_kernel<E, false>), grid, dim3(256), 0, s, a);
+  } else if (pl.row.threads == 8) {
+    launch_grad<E, 8, 1>(a, groups, s);
+  } else if (pl.row.threads == 16) {
+    launch_grad<E, 16, 1>(a, groups, s);
+  } else if (pl.row.threads == 32) {
+    launch_grad<E, 32, 1>(a, groups, s);
   } else if (pl.row.threads == 64) {
-    if (pl.row.runs == 1) launch_grad<E, 64, 1, 4>(a, groups, s);
-    else if (pl.row.runs == 2) launch_grad<E, 64, 2, 4>(a, groups, s);
-    else launch_grad<E, 64, 4, 4>(a, groups, s);
+    if (pl.row.runs == 1) launch_grad<E, 64, 1>(a, groups, s);
+    else launch_grad<E, 64, 2>(a, groups, s);
   } else if (pl.row.threads == 256) {
-    launch_grad<E, 256, 2, 1>(a, groups, s);
+    if (pl.row.runs == 1) launch_grad<E, 256, 1>(a, groups, s);
+    else launch_grad<E, 256, 2>(a, groups, s);
   } else {
-    if (pl.row.runs == 1) launch_grad<E, 1024, 1, 1>(a, groups, s);
-    else launch_grad<E, 1024, 2, 1>(a, groups, s);
+    launch_grad<E, 1024, 1>(a, groups, s);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.partials) return e;

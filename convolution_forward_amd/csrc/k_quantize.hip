@@ -36,7 +36,7 @@ __device__ __forceinline__ unsigned largest(const float (&v)[U][8]) {
 
 template <int T>
 __device__ __forceinline__ unsigned row_max(unsigned v, unsigned* lds) {
-  v = __builtin_bit_cast(unsigned, wave_join(__builtin_bit_cast(float, v), [](float a, float b) {
+  v = __builtin_bit_cast(unsigned, lanes_join<T < 64 ? T : 64>(__builtin_bit_cast(float, v), [](float a, float b) {
         return __builtin_bit_cast(float, max(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b)));
       }));
   if constexpr (T > 64) {
@@ -93,11 +93,10 @@ __device__ __forceinline__ void scales(unsigned top, float* scale, float* inv) {
 }
 
 template <typename E, int T, int U, bool LONG>
-__global__ __launch_bounds__(T == 64 ? 256 : T) void quantize_kernel(const QuantArgs<E> a) {
-  constexpr int TEAMS = T == 64 ? 4 : 1;
-  __shared__ unsigned lds[T / 64];
-  const int t = threadIdx.x % T, team = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
-  const long long row = a.row0 + (long long)blockIdx.x * TEAMS + team;
+__global__ __launch_bounds__(T* teams_of(T)) void quantize_kernel(const QuantArgs<E> a) {
+  __shared__ unsigned lds[waves_of(T)];
+  const int t = threadIdx.x % T;
+  const long long row = a.row0 + (long long)blockIdx.x * teams_of(T) + team_of<T>();
   if (row >= a.m) return;
   const E* x = a.x + row * a.ldx;
   signed char* q = a.q + row * a.ldq;
@@ -135,7 +134,7 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void quantize_kernel(const Quant
 
 template <typename E, int T, int U, bool LONG>
 hipError_t launch(QuantArgs<E> a, hipStream_t s) {
-  constexpr int TEAMS = T == 64 ? 4 : 1;
+  constexpr int TEAMS = teams_of(T);
   const long long most = 0xff000000LL / T;  // fewer than 2^32 work-items a launch
   for (long long at = 0; at < a.m; at += most) {
     a.row0 = at;
@@ -161,14 +160,15 @@ int run(const quantize_problem* p, const QuantGeo& g, const void* x, void* q, vo
   hipStream_t s = static_cast<hipStream_t>(stream);
   const RowPlan& r = g.row;
   hipError_t e;
-  if (r.threads == 64)
-    e = r.runs == 1   ? launch<E, 64, 1, false>(a, s)
-        : r.runs == 2 ? launch<E, 64, 2, false>(a, s)
-                      : launch<E, 64, 4, false>(a, s);
-  else if (r.threads == 256)
-    e = r.runs == 2 ? launch<E, 256, 2, false>(a, s) : launch<E, 256, 4, false>(a, s);
-  else
-    e = r.parts ? launch<E, 1024, 4, true>(a, s) : launch<E, 1024, 4, false>(a, s);
+  if (r.threads == 8) e = launch<E, 8, 1, false>(a, s);
+  else if (r.threads == 16) e = launch<E, 16, 1, false>(a, s);
+  else if (r.threads == 32) e = launch<E, 32, 1, false>(a, s);
+  else if (r.threads == 64) e = r.runs == 1 ? launch<E, 64, 1, false>(a, s) : launch<E, 64, 2, false>(a, s);
+  else if (r.threads == 256) e = r.runs == 1 ? launch<E, 256, 1, false>(a, s) : launch<E, 256, 2, false>(a, s);
+  else if (r.parts) e = launch<E, 1024, 4, true>(a, s);
+  else if (r.runs == 1) e = launch<E, 1024, 1, false>(a, s);
+  else if (r.runs == 2) e = launch<E, 1024, 2, false>(a, s);
+  else e = launch<E, 1024, 4, false>(a, s);
   return e == hipSuccess ? CONV_OK : CONV_ERR_DEVICE;
 }
 

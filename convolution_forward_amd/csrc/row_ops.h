@@ -9,46 +9,67 @@
 
 namespace convfwd {
 
-// Sum over the 64 lanes, the same in every lane: four steps within rows of 16 (lanes
-// paired by 1, 2, and mirrored halves and rows), two between them by lane swaps; no LDS.
+// v joined over the T = 8, 16, 32 or 64 neighbouring lanes of a row by f, the same in all
+// of them: lanes paired by 1, 2, and mirrored halves and rows of 16, then lane swaps
+// between rows of 16; no LDS.
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL,
                                                                0xf, 0xf, true));
 }
-template <typename F>
-__device__ __forceinline__ float wave_join(float v, F f) {
+template <int T, typename F>
+__device__ __forceinline__ float lanes_join(float v, F f) {
+  static_assert(T == 8 || T == 16 || T == 32 || T == 64, "lanes of a row");
   v = f(v, dpp<0xB1>(v));   // lane ^ 1
   v = f(v, dpp<0x4E>(v));   // lane ^ 2
   v = f(v, dpp<0x141>(v));  // mirrored within 8
-  v = f(v, dpp<0x140>(v));  // mirrored within 16
-  const unsigned u = __builtin_bit_cast(unsigned, v);
-  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  const unsigned a0 = a[0], a1 = a[1];
-  v = f(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1));
-  const unsigned w = __builtin_bit_cast(unsigned, v);
-  const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-  const unsigned b0 = b[0], b1 = b[1];
-  return f(__builtin_bit_cast(float, b0), __builtin_bit_cast(float, b1));
+  if constexpr (T >= 16) v = f(v, dpp<0x140>(v));  // mirrored within 16
+  if constexpr (T >= 32) {
+    const unsigned u = __builtin_bit_cast(unsigned, v);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const unsigned a0 = a[0], a1 = a[1];
+    v = f(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1));
+  }
+  if constexpr (T >= 64) {
+    const unsigned w = __builtin_bit_cast(unsigned, v);
+    const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    const unsigned b0 = b[0], b1 = b[1];
+    v = f(__builtin_bit_cast(float, b0), __builtin_bit_cast(float, b1));
+  }
+  return v;
 }
-__device__ __forceinline__ float wave_sum(float v) {
-  return wave_join(v, [](float a, float b) { return a + b; });
+template <int T>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return lanes_join<T>(v, [](float a, float b) { return a + b; });
 }
+__device__ __forceinline__ float wave_sum(float v) { return lanes_sum<64>(v); }
 
-// Sum over the T threads of a workgroup that hold a row (T = 64: one wave, no barrier).
-// Two calls in turn need two arrays: a wave may be a call ahead, never two.
+// Sum over the T threads that hold a row (T <= 64: lanes of a wave, no barrier; more: a
+// whole workgroup).  Two calls in turn need two arrays: a wave may be a call ahead,
+// never two.
 template <int T>
 __device__ __forceinline__ float row_sum(float v, float* lds) {
-  v = wave_sum(v);
-  if constexpr (T > 64) {
+  if constexpr (T <= 64) {
+    return lanes_sum<T>(v);
+  } else {
+    v = wave_sum(v);
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
     v = 0.0f;
 #pragma unroll
     for (int i = 0; i < T / 64; ++i) v += lds[i];
+    return v;
   }
-  return v;
 }
+
+// Which of a workgroup's rows a thread works on; the same in a wave where it can be.
+template <int T>
+__device__ __forceinline__ int team_of() {
+  const int team = threadIdx.x / T;
+  return T >= 64 ? __builtin_amdgcn_readfirstlane(team) : team;
+}
+constexpr int teams_of(int threads) { return threads >= 256 ? 1 : 256 / threads; }
+constexpr int waves_of(int threads) { return threads > 64 ? threads / 64 : 1; }
 
 // The numbers of a mask, see include/dropout.h.
 struct DropArgs {
@@ -129,30 +150,42 @@ struct __attribute__((packed, aligned(sizeof(E)))) Few {
   vec v;
 };
 
-// The last, partial run of a row, 1 <= left <= 7 elements at p: pieces of 4, 2 and 1,
-// zeros behind them.  Nothing past the end is read.
+// The last, partial run of a row, 1 <= left <= 7 elements at p, in pieces of 4, 2 and 1
+// (nothing past the end is read), which are held at elements 0, 4 and 6 of q; those that
+// left does not have stay as they were: zeros.
 template <typename E>
-__device__ __forceinline__ void load_tail(const E* p, int left, float (&v)[8]) {
-  float q[4] = {0, 0, 0, 0}, d[2] = {0, 0}, s = 0;
-  const bool has4 = left & 4, has2 = left & 2;
-  if (has4) {
+__device__ __forceinline__ void fetch_tail(const E* p, int left, Eight<E>& q) {
+  constexpr int W = 16 / (int)sizeof(E);
+  if (left & 4) {
     const auto f = reinterpret_cast<const Few<E, 4>*>(p)->v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) q[e] = (float)f[e];
+    for (int e = 0; e < 4; ++e) q.q[0][e] = f[e];
   }
-  if (has2) {
+  if (left & 2) {
     const auto f = reinterpret_cast<const Few<E, 2>*>(p + (left & 4))->v;
-    d[0] = (float)f[0];
-    d[1] = (float)f[1];
+    q.q[4 / W][4 % W] = f[0];
+    q.q[5 / W][5 % W] = f[1];
   }
-  if (left & 1) s = (float)p[left & 6];
-  const float d0 = d[0], d1 = d[1], rest[4] = {has2 ? d0 : s, has2 ? d1 : 0.0f, has2 ? s : 0.0f, 0.0f};
+  if (left & 1) q.q[6 / W][6 % W] = p[left & 6];
+}
+// The pieces, as floats in v, moved to where they belong; zeros behind them.
+__device__ __forceinline__ void order_tail(int left, float (&v)[8]) {
+  const bool has4 = left & 4, has2 = left & 2;
+  const float d0 = v[4], d1 = v[5], s = v[6];
+  const float rest[4] = {has2 ? d0 : s, has2 ? d1 : 0.0f, has2 ? s : 0.0f, 0.0f};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float four = q[e], behind = rest[e];
-    v[e] = has4 ? four : behind;
+    const float q = v[e], behind = rest[e];  // values: a choice of places would need memory
+    v[e] = has4 ? q : behind;
     v[4 + e] = has4 ? behind : 0.0f;
   }
+}
+template <typename E>
+__device__ __forceinline__ void load_tail(const E* p, int left, float (&v)[8]) {
+  Eight<E> q{};
+  fetch_tail(p, left, q);
+  unpack(q, v);
+  order_tail(left, v);
 }
 template <typename E>
 __device__ __forceinline__ void store_tail(E* p, int left, const float (&v)[8]) {
@@ -179,31 +212,42 @@ __device__ __forceinline__ void store_tail(E* p, int left, const float (&v)[8]) 
   if (left & 1) p[left & 6] = (E)(has2 ? last : first);
 }
 
-// Runs run0, run0 + T, .. of a row of n elements at p; zeros past its end.  The partial
-// run, which is one thread's at the same u for all, is loaded once.
-template <int T, int U, typename E>
-__device__ __forceinline__ void load_runs(const E* p, int n, int run0, float (&v)[U][8]) {
-  const int whole = n >> 3;
+// Runs run0, run0 + T, .. of a row of n elements, as they lie in memory: fetched ahead of
+// their use.  Runs past the end stay as they were made: zeros.
+template <typename E, int T, int U>
+struct Runs {
+  Eight<E> q[U];
+
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int run = run0 + u * T;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[u][e] = 0.0f;
-    if (run < whole) unpack(*reinterpret_cast<const Eight<E>*>(p + run * 8), v[u]);
+    for (int u = 0; u < U; ++u) q[u] = Eight<E>{};
   }
-  if (n & 7) {
-    if ((whole - run0) % T == 0 && whole >= run0 && whole < run0 + T * U) {
-      float t[8];
-      load_tail(p + whole * 8, n & 7, t);
+  __device__ __forceinline__ void fetch(const E* p, int n, int run0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (run0 + u * T < (n >> 3)) q[u] = *reinterpret_cast<const Eight<E>*>(p + (run0 + u * T) * 8);
+    if (n & 7) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float here = t[e], other = v[u][e];
-          v[u][e] = run0 + u * T == whole ? here : other;
-        }
+        if (run0 + u * T == (n >> 3)) fetch_tail(p + (n & ~7), n & 7, q[u]);
     }
   }
+  __device__ __forceinline__ void get(int n, int run0, float (&v)[U][8]) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) unpack(q[u], v[u]);
+    if (n & 7) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (run0 + u * T == (n >> 3)) order_tail(n & 7, v[u]);
+    }
+  }
+};
+template <int T, int U, typename E>
+__device__ __forceinline__ void load_runs(const E* p, int n, int run0, float (&v)[U][8]) {
+  Runs<E, T, U> r;
+  r.clear();
+  r.fetch(p, n, run0);
+  r.get(n, run0, v);
 }
 template <int T, int U, typename E>
 __device__ __forceinline__ void store_runs(E* p, int n, int run0, const float (&v)[U][8]) {

@@ -19,6 +19,19 @@ bool probability(float p) { return p >= 0.0f && p <= 1.0f; }
 
 bool off8(const void* p) { return (uintptr_t)p % 8 != 0; }
 
+// Threads that hold a row of up to 32768 elements, one run of 8 each where that does
+// not take too many: more runs a thread cost registers, and with them loads in flight
+// (bf16 16384 x 2048: 64 threads of 4 runs 63 us, 256 of 1 53; 4096 x 8192: 256 of 4 63,
+// 1024 of 1 54).
+RowPlan row_plan(int64_t runs) {
+  if (runs <= 8) return {8, 1, 0};
+  if (runs <= 16) return {16, 1, 0};
+  if (runs <= 32) return {32, 1, 0};
+  if (runs <= 128) return {64, runs <= 64 ? 1 : 2, 0};
+  if (runs <= 512) return {256, runs <= 256 ? 1 : 2, 0};
+  return {1024, runs <= 1024 ? 1 : runs <= 2048 ? 2 : 4, 0};
+}
+
 }  // namespace
 
 int drop_threshold(float p) { return (int)nearbyint((double)p * 65536.0); }
@@ -59,12 +72,8 @@ int layer_norm_validate(const layer_norm_problem* p, int dtype, NormGeo* out) {
 NormPlan plan_layer_norm(const NormGeo& g) {
   NormPlan o{};
   const int64_t runs = ceil_div(g.n, 8);
-  if (runs <= 64 * 4) {
-    o.row = {64, runs <= 64 ? 1 : runs <= 128 ? 2 : 4, 0};
-  } else if (runs <= 256 * 4) {
-    o.row = {256, runs <= 512 ? 2 : 4, 0};
-  } else if (runs <= 1024 * 4) {
-    o.row = {1024, runs <= 2048 ? 2 : 4, 0};
+  if (runs <= 4096) {
+    o.row = row_plan(runs);
   } else {
     o.row = {256, 4, ceil_div(runs, 256 * 4)};
     // a mean and a sum of squares for each part of each row
@@ -77,15 +86,9 @@ NormBackwardPlan plan_layer_norm_backward(const NormGeo& g) {
   NormBackwardPlan o{};
   const int64_t runs = ceil_div(g.n, 8), np = runs * 8;
   int64_t at = 0;
-  if (runs <= 256) {
-    o.row = {64, runs <= 64 ? 1 : runs <= 128 ? 2 : 4, 0};
-    o.teams = 4;
-  } else if (runs <= 512) {
-    o.row = {256, 2, 0};
-    o.teams = 1;
-  } else if (runs <= 2048) {
-    o.row = {1024, runs <= 1024 ? 1 : 2, 0};
-    o.teams = 1;
+  if (runs <= 1024) {
+    o.row = row_plan(runs);
+    o.teams = o.row.threads >= 256 ? 1 : 256 / o.row.threads;
   } else {
     o.row = {256, 1, ceil_div(runs, 256)};
     o.teams = 1;
@@ -249,12 +252,7 @@ int quantize_checked(const quantize_problem* p, int dtype, const void* x, const 
   const int st = o.check(nullptr, 0);
   if (st) return st;
   const int64_t runs = ceil_div(g.n, 8);
-  if (runs <= 64 * 4)
-    g.row = {64, runs <= 64 ? 1 : runs <= 128 ? 2 : 4, 0};
-  else if (runs <= 256 * 4)
-    g.row = {256, runs <= 512 ? 2 : 4, 0};
-  else
-    g.row = {1024, 4, runs <= 4096 ? 0 : ceil_div(runs, 4096)};
+  g.row = runs <= 4096 ? row_plan(runs) : RowPlan{1024, 4, ceil_div(runs, 4096)};
   *out = g;
   return CONV_OK;
 }
