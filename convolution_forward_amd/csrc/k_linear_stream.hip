@@ -196,7 +196,8 @@ __global__ __launch_bounds__(kStreamWaves * 64) void linear_stream_kernel(const 
         for (int q = 0; q < 8; ++q) w[q] = q < RB ? red[0][TC + (c >> 4)][c & 15][rr + q % RB] : 0.0f;
         finish_gated<E>(e, c, r, v, w);
       } else {
-        finish_linear<O, EB == 1>(e, 0, c, r, v);
+        if constexpr (EB == 1) finish_scaled<O>(e, c, r, v);
+        else finish_linear<O>(e, 0, c, r, v);
       }
     }
   }
@@ -251,7 +252,7 @@ __device__ __forceinline__ void join(const JoinArgs& a, long long block) {
     float f[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) f[q] = (float)v[q];
-    finish_linear<E, true>(a.e, z, c, r, f);
+    finish_scaled<E>(a.e, c, r, f);
   }
 }
 

@@ -10,6 +10,8 @@
 
 namespace convfwd {
 
+typedef float lin_f32x4 __attribute__((ext_vector_type(4)));
+
 // Eight elements at p, whatever its alignment (the card reads and writes 16 bytes at
 // any element's address): two pieces of float32, one of 16 bits.  The last run of a
 // row, nv < 8 of them, goes element by element.
@@ -267,26 +269,10 @@ __device__ __forceinline__ int run_offset(int lane) {
   return ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
 }
 
-// The scales of 8-bit operands, before anything is added: v of row c times xs[c] ws[r],
-// rounded here whatever follows, so that every kernel gives the same bits.
-template <int NR, typename Off>
-__device__ __forceinline__ void scale_runs(const LinEpilogue& e, long long c, bool in, int r,
-                                           Off off, bool whole, float (&v)[NR * 8]) {
-#pragma clang fp contract(off)
-  const float xs = in ? e.xs[c] : 0.0f;
-#pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    float t[8];
-    load8(e.ws + r + off(n), whole ? 8 : e.R - r - off(n), t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[n * 8 + i] *= xs * t[i];
-  }
-}
-
 // Linear: v holds the sums of one row c, NR runs of 8 outputs at r + off(n).  whole
 // (uniform): every run is inside; in: c is a row.  The runs' loads are in flight
 // together and one branch picks the activation for all.
-template <typename E, int NR, bool SCALED = false, typename Off>
+template <typename E, int NR, typename Off>
 __device__ __forceinline__ void finish_linear_runs(const LinEpilogue& e, int z, long long c,
                                                    bool in, int r, Off off, bool whole,
                                                    float (&v)[NR * 8]) {
@@ -310,7 +296,6 @@ __device__ __forceinline__ void finish_linear_runs(const LinEpilogue& e, int z, 
       store8(p + off(n), whole ? 8 : e.R - r - off(n), t);
     }
   };
-  if constexpr (SCALED) scale_runs<NR>(e, c, in, r, off, whole, v);
   if (e.bias[0]) add(e.bias[0], 0);
   if (e.res_mode == 1 && in) add(e.res, c * e.ldres);
   if (e.save[0] && in) store(e.save[0], c * e.ldsave);
@@ -335,10 +320,90 @@ __device__ __forceinline__ void finish_plain_runs(const LinEpilogue& e, int z, l
   }
 }
 
-template <typename E, bool SCALED = false>
+// 8-bit operands: what the outputs r of a lane need whatever their row c, the scales ws
+// and the bias, taken once for all rows: into registers, or, a tile's, into LDS.
+template <typename O, int NR>
+struct ScaledColumns {
+  float ws[NR * 8], b[NR * 8];
+  __device__ __forceinline__ float scale(int i) const { return ws[i]; }
+  __device__ __forceinline__ float bias(int i) const { return b[i]; }
+
+  template <typename Off>
+  __device__ __forceinline__ void load(const LinEpilogue& e, int r, Off off, bool whole) {
+    auto take = [&](auto* p, float* to) {
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        float t[8];
+        load8(p + r + off(n), whole ? 8 : e.R - r - off(n), t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) to[n * 8 + i] = t[i];
+      }
+    };
+    take(e.ws, ws);
+#pragma unroll
+    for (int i = 0; i < NR * 8; ++i) b[i] = 0.0f;
+    if (e.bias[0]) take(static_cast<const O*>(e.bias[0]), b);
+  }
+};
+
+template <int NR>
+struct ScaledColumnsLds {
+  lin_f32x4 ws[NR * 2], b[NR * 2];
+  __device__ __forceinline__ float scale(int i) const { return ws[i / 4][i % 4]; }
+  __device__ __forceinline__ float bias(int i) const { return b[i / 4][i % 4]; }
+
+  // at: the scale of the lane's first output; the bias lies `apart` floats behind
+  template <typename Off>
+  __device__ __forceinline__ void load(const float* at, int apart, Off off) {
+#pragma unroll
+    for (int n = 0; n < NR * 2; ++n) {
+      const float* p = at + off(n / 2) + n % 2 * 4;
+      ws[n] = *reinterpret_cast<const lin_f32x4*>(p);
+      b[n] = *reinterpret_cast<const lin_f32x4*>(p + apart);
+    }
+  }
+};
+
+// Linear, 8-bit operands: v holds the sums of one row c, xs is its scale.  The product
+// with the scales is rounded whatever follows, so that every kernel gives the same bits.
+template <typename O, int NR, typename Columns, typename Off>
+__device__ __forceinline__ void finish_scaled_runs(const LinEpilogue& e, const Columns& cols, float xs,
+                                                   long long c, bool in, int r, Off off, bool whole,
+                                                   float (&v)[NR * 8]) {
+#pragma clang fp contract(off)
+  auto residual = [&] {
+    const O* p = static_cast<const O*>(e.res) + c * e.ldres + r;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      float t[8];
+      load8(p + off(n), whole ? 8 : e.R - r - off(n), t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[n * 8 + i] += t[i];
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < NR * 8; ++i) v[i] = v[i] * (xs * cols.scale(i)) + cols.bias(i);
+  if (e.res_mode == 1 && in) residual();
+  lin_act<sizeof(O) == 2>(v, e.act, e.alpha, e.beta);
+  if (in) {
+    if (e.res_mode == 2) residual();
+    finish_plain_runs<O, NR>(e, 0, c, r, off, whole, v);
+  }
+}
+
+template <typename E>
 __device__ __forceinline__ void finish_linear(const LinEpilogue& e, int z, long long c, int r,
                                               float (&v)[8]) {
-  finish_linear_runs<E, 1, SCALED>(e, z, c, true, r, [](int) { return 0; }, false, v);
+  finish_linear_runs<E, 1>(e, z, c, true, r, [](int) { return 0; }, false, v);
+}
+
+template <typename O>
+__device__ __forceinline__ void finish_scaled(const LinEpilogue& e, long long c, int r,
+                                              float (&v)[8]) {
+  const auto off = [](int) { return 0; };
+  ScaledColumns<O, 1> cols;
+  cols.load(e, r, off, false);
+  finish_scaled_runs<O, 1>(e, cols, e.xs[c], c, true, r, off, false, v);
 }
 
 // Gated: g and u hold both projections' sums.

@@ -80,11 +80,13 @@ int linear_int8_describe_variant(const linear_int8_problem* p, int dtype, char* 
   Int8Geo g;
   const int st = int8_validate(p, dtype, &g);
   if (st) return st;
-  char name[48], text[96];
+  char name[48], text[112];
   const LinearPlan pl = plan_linear_int8(p, g);
   product_name(pl.run, name, sizeof name);
-  snprintf(text, sizeof text, "linear_int8.%s.%s%s", float_dtype_name(dtype), name,
-           pl.pack.on ? ".pack" : "");
+  const bool cut = pl.run.tile == TILE_256 && pl.run.splits == 1 &&
+                   cut_tiles(ceil_div(g.n, 256) * ceil_div(g.m, 256)) > 0;
+  snprintf(text, sizeof text, "linear_int8.%s.%s%s%s", float_dtype_name(dtype), name,
+           cut ? ".cut" : "", pl.pack.on ? ".pack" : "");
   return put_name(text, buf, len);
 }
 

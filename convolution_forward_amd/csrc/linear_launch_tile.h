@@ -42,9 +42,19 @@ static hipError_t launch_layout(const ProductArgs& a, int tile, bool dma, hipStr
 }
 
 template <typename O>
-hipError_t launch_int8_product(const ProductArgs& a, int tile, bool dma, hipStream_t s) {
+hipError_t launch_int8_product(const ProductArgs& args, int tile, bool dma, hipStream_t s) {
   typedef signed char E;
+  ProductArgs a = args;
   if (dma) {
+    if (tile == TILE_256 && a.splits == 1) {
+      a.ntr = (a.R + 255) / 256;
+      a.ntc = (a.C + 255) / 256;
+      const int tiles = a.ntr * a.ntc, cut = (int)cut_tiles(tiles);
+      if (cut > 0) {
+        hipLaunchKernelGGL((linear_cut_kernel<E, O>), dim3(tiles + cut), dim3(512), 0, s, a, tiles - cut);
+        return hipGetLastError();
+      }
+    }
     if (tile == TILE_256) return launch_pingpong<E, false, false, 256, false, O>(a, s);
     if (tile == TILE_256X128) return launch_pingpong<E, false, false, 128, false, O>(a, s);
     if (tile == TILE_64) return launch_tile<E, false, false, 64, 64, 2, 2, true, false, O>(a, s);

@@ -232,6 +232,13 @@ ProductPlan plan_product(const ProductShape& s, int es) {
       // one size that was timed: 21 us for 16)
       const double slow = s.pt && es == 2 && !s.aligned ? 1.35 : 1.0;
       double t = slow * time_of(table[i], tiles * n, per);
+      if (es == 1 && table[i].tile == TILE_256 && n == 1 && cut_tiles(tiles) > 0) {
+        // the last round in halves
+        const int64_t cut = cut_tiles(tiles);
+        const Tiling& h = table[1];
+        t = time_of(table[i], tiles - cut, per) + h.round +
+            (double)per * (h.step + h.busy * (double)(2 * cut) / kCus);
+      }
       if (n > 1) t += kJoin + kJoinByte * (double)(plane * n);
       if (want > 2 && t > before) break;  // past the best count
       before = t;

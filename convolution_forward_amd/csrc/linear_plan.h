@@ -99,6 +99,12 @@ struct PairPlan {
   double time;         // estimated, us
   ProductPlan dx, dw;  // of each alone; for TILE_64 in that launch
 };
+// 8-bit products: tiles of 256 x 256 of the last round that are cut in two (0: none).  Fewer
+// than half of the units would have one in it.
+inline int64_t cut_tiles(int64_t tiles) {
+  const int64_t rest = tiles % 256;
+  return tiles > 256 && rest <= 128 ? rest : 0;
+}
 PairPlan plan_pair(const ProductShape& dx, const ProductShape& dw, int es);
 ColsumPlan plan_colsum(int64_t m, int64_t n);
 

@@ -518,6 +518,9 @@ static __device__ __forceinline__ void run(const ProductArgs& a, const int id, c
   auto off = [](int n) { return n * 32; };
   const int rl = r0 + wr * RUN + run_offset(lane);
   const bool whole = nr >= WVR * RUN;
+  ScaledColumns<O, sizeof(E) == 1 ? NR : 1> cols;
+  if constexpr (sizeof(E) == 1)
+    if (a.splits == 1) cols.load(a.e, rl, off, whole);
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     float v[NR * 8], u[GATED ? NR * 8 : 1];
@@ -543,8 +546,10 @@ static __device__ __forceinline__ void run(const ProductArgs& a, const int id, c
         }
     } else if constexpr (GATED) {
       finish_gated_runs<E, NR>(a.e, c, in, rl, off, whole, v, u);
+    } else if constexpr (sizeof(E) == 1) {
+      finish_scaled_runs<O, NR>(a.e, cols, in ? a.e.xs[c] : 0.0f, c, in, rl, off, whole, v);
     } else {
-      finish_linear_runs<O, NR, sizeof(E) == 1>(a.e, z, c, in, rl, off, whole, v);
+      finish_linear_runs<O, NR>(a.e, z, c, in, rl, off, whole, v);
     }
   }
 }

@@ -72,7 +72,7 @@ int quantize_rows(const quantize_problem* p, int dtype, const void* x, void* q, 
 int linear_int8_scratch_size(const linear_int8_problem* p, int dtype, uint64_t* bytes);
 
 /* Name of the kernel plan, e.g. "linear_int8.bf16.tile256x256" (the type is that of
- * b, r and y), as in linear.h. */
+ * b, r and y), as in linear.h; ".cut": the tiles of the last round are cut in two. */
 int linear_int8_describe_variant(const linear_int8_problem* p, int dtype, char* buf, uint64_t len);
 
 /* The status linear_int8_forward would return before enqueueing (host only). */
