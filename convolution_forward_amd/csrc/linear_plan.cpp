@@ -240,6 +240,9 @@ ProductPlan plan_product(const ProductShape& s, int es) {
             (double)per * (h.step + h.busy * (double)(2 * cut) / kCus);
       }
       if (n > 1) t += kJoin + kJoinByte * (double)(plane * n);
+      // 8 bits: no less than the weights take from memory (one row, 32000 x 4096: 64 x 64
+      // tiles 33 us, streamed 25)
+      if (es == 1) t = std::max(t, 4.0 + (double)(s.R * s.K) / 4.4e6 + 0.01 * t);
       if (want > 2 && t > before) break;  // past the best count
       before = t;
       if (pl.tile < 0 || t < best) {
