@@ -24,46 +24,42 @@ struct DropoutArgs {
   DropArgs d;
 };
 
-// left: elements from p to the end of the row, 0 or less where there is no run.
-template <typename E>
-__device__ __forceinline__ void load_run(const E* p, int left, float (&v)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-  if (left >= 8) unpack(*reinterpret_cast<const Eight<E>*>(p), v);
-  else if (left > 0) load_tail(p, left, v);
-}
-template <typename E>
-__device__ __forceinline__ void store_run(E* p, int left, const float (&v)[8]) {
-  if (left >= 8) store8(p, 8, v);
-  else if (left > 0) store_tail(p, left, v);
-}
-
 // A workgroup takes 256 R runs in order, a thread R of them 256 apart: their loads are
 // in flight together.
 template <typename E, int R, bool RES>
 __global__ __launch_bounds__(256) void dropout_kernel(const DropoutArgs<E> a) {
-  const DropCounter c = drop_counter(a.d);
   const unsigned i0 = blockIdx.x * (256 * R) + threadIdx.x;
-  float v[R][8], t[R][8];
+  Eight<E> x[R] = {}, r[R] = {};
   unsigned row[R], run[R];
-  int left[R];
+  int left[R];  // elements to the end of the row, 0 where there is no run
+  auto fetch = [](const E* p, int n, Eight<E>& q) {
+    if (n >= 8) q = *reinterpret_cast<const Eight<E>*>(p);
+    else if (n > 0) fetch_tail(p, n, q);
+  };
 #pragma unroll
   for (int k = 0; k < R; ++k) {
     const unsigned i = i0 + 256 * k;
     row[k] = mdiv(i, a.mg);
     run[k] = i - row[k] * a.runs;
     left[k] = i < a.runs_all ? a.n - (int)run[k] * 8 : 0;
-    load_run(a.x + row[k] * a.ldx + run[k] * 8, left[k], v[k]);
-    if constexpr (RES) load_run(a.r + row[k] * a.ldr + run[k] * 8, left[k], t[k]);
+    fetch(a.x + row[k] * a.ldx + run[k] * 8, left[k], x[k]);
+    if constexpr (RES) fetch(a.r + row[k] * a.ldr + run[k] * 8, left[k], r[k]);
   }
+  const DropCounter c = drop_counter(a.d);
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    drop8(a.d, c, run[k], a.row0 + row[k], v[k]);
+    float v[8];
+    unpack(x[k], v);
+    drop8(a.d, c, run[k], a.row0 + row[k], left[k], v);
     if constexpr (RES) {
+      float t[8];
+      unpack(r[k], t);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[k][e] += t[k][e];
+      for (int e = 0; e < 8; ++e) v[e] += t[e];
     }
-    store_run(a.y + row[k] * a.ldy + run[k] * 8, left[k], v[k]);
+    E* y = a.y + row[k] * a.ldy + run[k] * 8;
+    if (left[k] >= 8) store8(y, 8, v);
+    else if (left[k] > 0) store_tail(y, left[k], v);
   }
 }
 

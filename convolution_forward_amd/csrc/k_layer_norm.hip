@@ -8,6 +8,7 @@
 // each part of 8192 elements, then every part joins those of its row (Chan, Golub and
 // LeVeque's formula for the variance of joined samples) and normalises.
 #include <algorithm>
+#include <type_traits>
 
 #include "row_ops.h"
 #include "rows_plan.h"
@@ -58,14 +59,14 @@ struct Loads {
 template <typename E, int T, int U, bool DROP>
 __device__ __forceinline__ void join_row(const NormArgs<E>& a, const Loads<E, T, U>& l,
                                          DropCounter c, long long row, int run0, float (&v)[U][8]) {
-  l.x.get(a.n, run0, v);
+  l.x.get(v);
   if constexpr (DROP) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) drop8(a.d, c, run0 + u * T, (unsigned)row, v[u]);
+    for (int u = 0; u < U; ++u) drop8(a.d, c, run0 + u * T, (unsigned)row, a.n - (run0 + u * T) * 8, v[u]);
   }
   if (a.r) {
     float t[U][8];
-    l.r.get(a.n, run0, t);
+    l.r.get(t);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -83,7 +84,7 @@ __device__ __forceinline__ void store_row(const NormArgs<E>& a, const Loads<E, T
     for (int e = 0; e < 8; ++e) v[u][e] = (v[u][e] - mean) * rstd;
   float t[U][8];
   if (a.w) {
-    if constexpr (Loads<E, T, U>::HOLD) l.w.get(a.n, run0, t);
+    if constexpr (Loads<E, T, U>::HOLD) l.w.get(t);
     else load_runs<T>(a.w, a.n, run0, t);
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -91,7 +92,7 @@ __device__ __forceinline__ void store_row(const NormArgs<E>& a, const Loads<E, T
       for (int e = 0; e < 8; ++e) v[u][e] *= t[u][e];
   }
   if (a.b) {
-    if constexpr (Loads<E, T, U>::HOLD) l.b.get(a.n, run0, t);
+    if constexpr (Loads<E, T, U>::HOLD) l.b.get(t);
     else load_runs<T>(a.b, a.n, run0, t);
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -123,7 +124,7 @@ __device__ __forceinline__ float spread(const float (&v)[U][8], int run0, int n,
 #pragma unroll
         for (int e = 0; e < 7; ++e) {
           const float d = v[u][e] - mean;
-          if (e < (n & 7)) q = fmaf(d, d, q);
+          if (in_tail(e, n & 7)) q = fmaf(d, d, q);
         }
       }
   }
@@ -235,13 +236,21 @@ hipError_t by_rows(NormArgs<E> a, long long each, F f) {
   return hipSuccess;
 }
 
+// f(DROP) as a constant.
+template <typename E, typename F>
+void with_drop(const NormArgs<E>& a, F f) {
+  if (a.d.threshold) f(std::true_type());
+  else f(std::false_type());
+}
+
 template <typename E, int T, int U>
 hipError_t launch_rows(const NormArgs<E>& args, hipStream_t s) {
   constexpr int TEAMS = teams_of(T);
   return by_rows(args, T, [&](const NormArgs<E>& a, unsigned rows) {
     const dim3 grid((rows + TEAMS - 1) / TEAMS), block(T * TEAMS);
-    if (a.d.threshold) hipLaunchKernelGGL((layer_norm_rows_kernel<E, T, U, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((layer_norm_rows_kernel<E, T, U, false>), grid, block, 0, s, a);
+    with_drop(a, [&](auto drop) {
+      hipLaunchKernelGGL((layer_norm_rows_kernel<E, T, U, drop.value>), grid, block, 0, s, a);
+    });
   });
 }
 
@@ -249,14 +258,16 @@ template <typename E>
 hipError_t launch_parts(const NormArgs<E>& args, hipStream_t s) {
   const hipError_t e = by_rows(args, 256 * args.nparts, [&](const NormArgs<E>& a, unsigned rows) {
     const dim3 grid(rows * a.nparts), block(256);
-    if (a.d.threshold) hipLaunchKernelGGL((layer_norm_parts_kernel<E, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((layer_norm_parts_kernel<E, false>), grid, block, 0, s, a);
+    with_drop(a, [&](auto drop) {
+      hipLaunchKernelGGL((layer_norm_parts_kernel<E, drop.value>), grid, block, 0, s, a);
+    });
   });
   if (e != hipSuccess) return e;
   return by_rows(args, 256 * args.nparts, [&](const NormArgs<E>& a, unsigned rows) {
     const dim3 grid(rows * a.nparts), block(256);
-    if (a.d.threshold) hipLaunchKernelGGL((layer_norm_joined_kernel<E, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((layer_norm_joined_kernel<E, false>), grid, block, 0, s, a);
+    with_drop(a, [&](auto drop) {
+      hipLaunchKernelGGL((layer_norm_joined_kernel<E, drop.value>), grid, block, 0, s, a);
+    });
   });
 }
 

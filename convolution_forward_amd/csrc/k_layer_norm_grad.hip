@@ -9,6 +9,7 @@
 // a row, none where lanes of a wave hold it.  Rows of more than 8192 elements go in parts
 // of 2048, in two launches: the parts' sums, then the gradients.
 #include <algorithm>
+#include <type_traits>
 
 #include "linear_tile.h"
 #include "row_ops.h"
@@ -44,7 +45,7 @@ __device__ __forceinline__ void finish_row(const GradArgs<E>& a, DropCounter c, 
     for (int e = 0; e < 8; ++e) g[k][e] = rstd * (g[k][e] - level - u[k][e] * along);
   if (a.ds) {
     float t[U][8];
-    ds.get(a.n, run0, t);
+    ds.get(t);
 #pragma unroll
     for (int k = 0; k < U; ++k)
 #pragma unroll
@@ -54,10 +55,16 @@ __device__ __forceinline__ void finish_row(const GradArgs<E>& a, DropCounter c, 
   if (a.dx) {
     if constexpr (DROP) {
 #pragma unroll
-      for (int k = 0; k < U; ++k) drop8(a.d, c, run0 + k * T, (unsigned)row, g[k]);
+      for (int k = 0; k < U; ++k) drop8(a.d, c, run0 + k * T, (unsigned)row, a.n - (run0 + k * T) * 8, g[k]);
     }
     store_runs<T>(a.dx + row * a.lddx, a.n, run0, g);
   }
+}
+
+// The sums of a run's columns to p, from the slots of a partial run where it is one.
+__device__ __forceinline__ void store_columns(float* p, int left, const float (&v)[8]) {
+  if (left >= 8) store8(p, 8, v);
+  else store_tail(p, left, v);
 }
 
 // T threads a row, U runs each; TEAMS rows at a time.  The next row's loads are in
@@ -80,8 +87,8 @@ __global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_kernel(const GradArg
       dw[k][e] = db[k][e] = 0.0f;
     }
   if (a.w) load_runs<T>(a.w, a.n, t, w);
-  const long long stride = (long long)gridDim.x * TEAMS;
-  long long row = (long long)blockIdx.x * TEAMS + team;
+  const long long stride = (long long)gridDim.x * TEAMS, first = (long long)blockIdx.x * TEAMS;
+  long long row = first + team;
   Runs<E, T, U> s, dy, ds, ds_next;
   s.clear();
   dy.clear();
@@ -96,13 +103,13 @@ __global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_kernel(const GradArg
   };
   if (row < a.m) fetch(row);
   int buf = 0;
-  for (long long base = (long long)blockIdx.x * TEAMS; base < a.m; base += stride, row += stride) {
+  for (long long base = first; base < a.m; base += stride, row += stride) {
     const bool in = row < a.m;  // every wave reaches the barrier
     float u[U][8], g[U][8], along = 0.0f, level = 0.0f;
     const float r = rstd;
     if (in) {
-      s.get(a.n, t, u);
-      dy.get(a.n, t, g);
+      s.get(u);
+      dy.get(g);
       const float mu = mean;
       ds = ds_next;
       if (row + stride < a.m) fetch(row + stride);
@@ -139,9 +146,9 @@ __global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_kernel(const GradArg
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int at = (t + k * T) * 8;
-      if (at < a.np) {
-        store8(p + at, 8, dw[k]);
-        store8(p + a.np + at, 8, db[k]);
+      if (at < a.n) {
+        store_columns(p + at, a.n - at, dw[k]);
+        store_columns(p + a.np + at, a.n - at, db[k]);
       }
     }
   } else {
@@ -149,12 +156,15 @@ __global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_kernel(const GradArg
 #pragma unroll
     for (int k = 0; k < 2 * U; ++k) {
       float* own = &columns[team][t * 8];
+      const int left = a.n - (t + k % U * T) * 8;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) own[e] = k < U ? dw[k % U][e] : db[k % U][e];
+      for (int e = 0; e < 8; ++e)
+        if (left >= 8 || in_tail(e, left))
+          own[left >= 8 ? e : tail_element(e, left)] = k < U ? dw[k % U][e] : db[k % U][e];
       __syncthreads();
       for (int i = threadIdx.x; i < T * 8; i += T * TEAMS) {
         const int at = k % U * T * 8 + i;
-        if (at < a.np) {
+        if (at < a.n) {
           float q = columns[0][i];
 #pragma unroll
           for (int j = 1; j < TEAMS; ++j) q += columns[j][i];
@@ -234,10 +244,11 @@ __global__ __launch_bounds__(256) void layer_norm_grad_parts_kernel(const GradAr
     }
     finish_row<E, kPartRuns, 1, DROP>(a, c, row, run0, rstd, along, level, u, g, ds);
   }
-  if (!a.partials || run0 * 8 >= a.np) return;
+  const int left = a.n - run0 * 8;
+  if (!a.partials || left <= 0) return;
   float* p = a.partials + (long long)group * 2 * a.np + run0 * 8;
-  store8(p, 8, dw);
-  store8(p + a.np, 8, db);
+  store_columns(p, left, dw);
+  store_columns(p + a.np, left, db);
 }
 
 // Adds the groups' partial rows: 64 columns of dw or db a workgroup, 64 rows at a time
@@ -276,14 +287,20 @@ __global__ __launch_bounds__(1024) void layer_norm_grad_join_kernel(const float*
   }
 }
 
+// f(DROP) as a constant.
+template <typename E, typename F>
+void with_drop(const GradArgs<E>& a, F f) {
+  if (a.d.threshold) f(std::true_type());
+  else f(std::false_type());
+}
+
 template <typename E, int T, int U>
 void launch_grad(const GradArgs<E>& a, unsigned groups, hipStream_t s) {
   constexpr int TEAMS = teams_of(T);
   const dim3 grid(groups), block(T * TEAMS);
-  if (a.d.threshold)
-    hipLaunchKernelGGL((layer_norm_grad_kernel<E, T, U, TEAMS, true>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((layer_norm_grad_kernel<E, T, U, TEAMS, false>), grid, block, 0, s, a);
+  with_drop(a, [&](auto drop) {
+    hipLaunchKernelGGL((layer_norm_grad_kernel<E, T, U, TEAMS, drop.value>), grid, block, 0, s, a);
+  });
 }
 
 template <typename E>
@@ -299,10 +316,9 @@ hipError_t grad(GradArgs<E>& a, const NormBackwardPlan& pl, E* dw, E* db, hipStr
       if (e != hipSuccess) return e;
     }
     const dim3 grid(groups * a.parts);
-    if (a.d.threshold)
-      hipLaunchKernelGGL((layer_norm_grad_parts_kernel<E, true>), grid, dim3(256), 0, s, a);
-    else
-      hipLaunchKernelGGL((layer_norm_grad_parts_kernel<E, false>), grid, dim3(256), 0, s, a);
+    with_drop(a, [&](auto drop) {
+      hipLaunchKernelGGL((layer_norm_grad_parts_kernel<E, drop.value>), grid, dim3(256), 0, s, a);
+    });
   } else if (pl.row.threads == 8) {
     launch_grad<E, 8, 1>(a, groups, s);
   } else if (pl.row.threads == 16) {

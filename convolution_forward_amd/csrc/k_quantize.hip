@@ -52,6 +52,12 @@ __device__ __forceinline__ unsigned row_max(unsigned v, unsigned* lds) {
 struct __attribute__((packed, aligned(1))) EightBytes {
   unsigned lo, hi;
 };
+struct __attribute__((packed, aligned(1))) FourBytes {
+  unsigned v;
+};
+struct __attribute__((packed, aligned(1))) TwoBytes {
+  unsigned short v;
+};
 
 template <int T, int U>
 __device__ __forceinline__ void store_quantized(signed char* q, int n, int run0, float inv,
@@ -70,10 +76,12 @@ __device__ __forceinline__ void store_quantized(signed char* q, int n, int run0,
     }
     if (run < whole) {
       *reinterpret_cast<EightBytes*>(q + run * 8) = {w[0], w[1]};
-    } else if (run == whole) {
-#pragma unroll
-      for (int e = 0; e < 7; ++e)
-        if (e < (n & 7)) q[run * 8 + e] = (signed char)(w[e >> 2] >> (8 * (e & 3)));
+    } else if (run == whole) {  // the pieces of a partial run
+      const int left = n & 7;
+      signed char* p = q + run * 8;
+      if (left & 4) reinterpret_cast<FourBytes*>(p)->v = w[0];
+      if (left & 2) reinterpret_cast<TwoBytes*>(p + (left & 4))->v = (unsigned short)w[1];
+      if (left & 1) p[left & 6] = (signed char)(w[1] >> 16);
     }
   }
 }

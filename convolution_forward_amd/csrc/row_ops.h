@@ -115,9 +115,15 @@ __device__ __forceinline__ bool drop_keeps(const DropBits& b, int e, unsigned th
   return u >= threshold;
 }
 
+// left: elements of the row from the run on; below 8 they lie in a partial run's slots.
 __device__ __forceinline__ void drop8(const DropArgs& a, DropCounter c, unsigned run, unsigned row,
-                                      float (&v)[8]) {
-  const DropBits b = drop_bits(a, c, run, row);
+                                      int left, float (&v)[8]) {
+  DropBits b = drop_bits(a, c, run, row);
+  if (left < 8) {
+    const unsigned w0 = b.w[0], w1 = b.w[1], w2 = b.w[2], w3 = b.w[3];
+    b.w[2] = left & 4 ? w2 : w0;
+    b.w[3] = left & 4 ? (left & 2 ? w3 : w2) : left & 2 ? w1 : w0;
+  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = drop_keeps(b, e, a.threshold) ? v[e] * a.scale : 0.0f;
 }
@@ -133,6 +139,8 @@ inline DropArgs drop_args(int threshold, uint64_t seed, uint64_t offset, const v
   a.step = static_cast<const unsigned long long*>(step);
   return a;
 }
+
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 // A run of 8 elements in memory as it is held: two pieces of 16 bytes of float32, one of
 // 16 bits, from any element's address on.
@@ -151,8 +159,9 @@ struct __attribute__((packed, aligned(sizeof(E)))) Few {
 };
 
 // The last, partial run of a row, 1 <= left <= 7 elements at p, in pieces of 4, 2 and 1
-// (nothing past the end is read), which are held at elements 0, 4 and 6 of q; those that
-// left does not have stay as they were: zeros.
+// (nothing past the end is touched).  The pieces have slots of their own among a run's 8:
+// 0 .. 3, 4 and 5, and 6; slots without an element hold zeros.  Nothing that is done to a
+// row depends on where in the run an element lies, but for the mask (drop8).
 template <typename E>
 __device__ __forceinline__ void fetch_tail(const E* p, int left, Eight<E>& q) {
   constexpr int W = 16 / (int)sizeof(E);
@@ -166,54 +175,44 @@ __device__ __forceinline__ void fetch_tail(const E* p, int left, Eight<E>& q) {
     q.q[4 / W][4 % W] = f[0];
     q.q[5 / W][5 % W] = f[1];
   }
-  if (left & 1) q.q[6 / W][6 % W] = p[left & 6];
-}
-// The pieces, as floats in v, moved to where they belong; zeros behind them.
-__device__ __forceinline__ void order_tail(int left, float (&v)[8]) {
-  const bool has4 = left & 4, has2 = left & 2;
-  const float d0 = v[4], d1 = v[5], s = v[6];
-  const float rest[4] = {has2 ? d0 : s, has2 ? d1 : 0.0f, has2 ? s : 0.0f, 0.0f};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float q = v[e], behind = rest[e];  // values: a choice of places would need memory
-    v[e] = has4 ? q : behind;
-    v[4 + e] = has4 ? behind : 0.0f;
+  if (left & 1) {
+    if constexpr (sizeof(E) == 2) {  // a word of its own: nothing to join before it is used
+      u32x4 w = __builtin_bit_cast(u32x4, q);
+      w[3] = *reinterpret_cast<const unsigned short*>(p + (left & 6));
+      q = __builtin_bit_cast(Eight<E>, w);
+    } else {
+      q.q[6 / W][6 % W] = p[left & 6];
+    }
   }
 }
-template <typename E>
-__device__ __forceinline__ void load_tail(const E* p, int left, float (&v)[8]) {
-  Eight<E> q{};
-  fetch_tail(p, left, q);
-  unpack(q, v);
-  order_tail(left, v);
+// Whether slot e of a partial run holds an element, and which of the run it is.
+__device__ __forceinline__ bool in_tail(int e, int left) {
+  return e < 4 ? left & 4 : e < 6 ? left & 2 : e == 6 ? left & 1 : false;
+}
+__device__ __forceinline__ int tail_element(int e, int left) {
+  return e < 4 ? e : e < 6 ? (left & 4) + e - 4 : left & 6;
 }
 template <typename E>
 __device__ __forceinline__ void store_tail(E* p, int left, const float (&v)[8]) {
-  const bool has4 = left & 4, has2 = left & 2;
-  if (has4) {
+  if (left & 4) {
     typename Few<E, 4>::vec f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = (E)v[e];
     reinterpret_cast<Few<E, 4>*>(p)->v = f;
   }
-  float r[3];
-#pragma unroll
-  for (int e = 0; e < 3; ++e) {
-    const float near = v[e], far = v[4 + e];  // values: a choice of places would need memory
-    r[e] = has4 ? far : near;
-  }
-  if (has2) {
+  if (left & 2) {
     typename Few<E, 2>::vec f;
-    f[0] = (E)r[0];
-    f[1] = (E)r[1];
+    f[0] = (E)v[4];
+    f[1] = (E)v[5];
     reinterpret_cast<Few<E, 2>*>(p + (left & 4))->v = f;
   }
-  const float first = r[0], last = r[2];
-  if (left & 1) p[left & 6] = (E)(has2 ? last : first);
+  if (left & 1) p[left & 6] = (E)v[6];
 }
 
 // Runs run0, run0 + T, .. of a row of n elements, as they lie in memory: fetched ahead of
-// their use.  Runs past the end stay as they were made: zeros.
+// their use.  Runs past the end stay as they were made: zeros.  (16-bit rows at odd
+// elements are loaded as they lie, which costs: 16384 x 2047 forward 38 us for 30 at even
+// ones, backward 67 for 49.  Aligned words and a lane exchange in their place took 49 and 54.)
 template <typename E, int T, int U>
 struct Runs {
   Eight<E> q[U];
@@ -232,14 +231,9 @@ struct Runs {
         if (run0 + u * T == (n >> 3)) fetch_tail(p + (n & ~7), n & 7, q[u]);
     }
   }
-  __device__ __forceinline__ void get(int n, int run0, float (&v)[U][8]) const {
+  __device__ __forceinline__ void get(float (&v)[U][8]) const {
 #pragma unroll
     for (int u = 0; u < U; ++u) unpack(q[u], v[u]);
-    if (n & 7) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (run0 + u * T == (n >> 3)) order_tail(n & 7, v[u]);
-    }
   }
 };
 template <int T, int U, typename E>
@@ -247,30 +241,18 @@ __device__ __forceinline__ void load_runs(const E* p, int n, int run0, float (&v
   Runs<E, T, U> r;
   r.clear();
   r.fetch(p, n, run0);
-  r.get(n, run0, v);
+  r.get(v);
 }
 template <int T, int U, typename E>
 __device__ __forceinline__ void store_runs(E* p, int n, int run0, const float (&v)[U][8]) {
   const int whole = n >> 3;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int run = run0 + u * T;
-    if (run < whole) store8(p + run * 8, 8, v[u]);
-  }
+  for (int u = 0; u < U; ++u)
+    if (run0 + u * T < whole) store8(p + (run0 + u * T) * 8, 8, v[u]);
   if (n & 7) {
-    if ((whole - run0) % T == 0 && whole >= run0 && whole < run0 + T * U) {
-      float t[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = v[0][e];
-#pragma unroll
-      for (int u = 1; u < U; ++u)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float here = v[u][e], other = t[e];
-          t[e] = run0 + u * T == whole ? here : other;
-        }
-      store_tail(p + whole * 8, n & 7, t);
-    }
+    for (int u = 0; u < U; ++u)
+      if (run0 + u * T == whole) store_tail(p + whole * 8, n & 7, v[u]);
   }
 }
 

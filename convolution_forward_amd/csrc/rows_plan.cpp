@@ -96,7 +96,7 @@ NormBackwardPlan plan_layer_norm_backward(const NormGeo& g) {
     at += ceil_div(g.m * o.row.parts * 8, 256) * 256;
   }
   const int64_t most = o.row.parts ? std::max<int64_t>(1, 4 * kCus / o.row.parts)
-                       : o.row.threads == 1024 ? kCus : 2 * kCus;
+                       : o.row.threads == 1024 ? kCus : o.row.runs == 2 ? 2 * kCus : 4 * kCus;
   o.groups = std::max<int64_t>(1, std::min<int64_t>(most, ceil_div(g.m, o.teams)));
   o.partials = at;
   at += ceil_div(o.groups * 2 * np * 4, 256) * 256;
