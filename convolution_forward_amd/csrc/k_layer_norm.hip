@@ -5,7 +5,7 @@
 // that mean and variance are two sums over registers (the second of squared distances,
 // which does not cancel).  Short rows take 8 to 64 lanes of a wave, several to a
 // workgroup, with no barrier.  Longer rows go in two launches: a mean and a sum of squared distances for
-// each part of 8192 elements, then every part joins those of its row (Chan, Golub and
+// each part of 4096 elements, then every part joins those of its row (Chan, Golub and
 // LeVeque's formula for the variance of joined samples) and normalises.
 #include <algorithm>
 #include <type_traits>
@@ -164,7 +164,7 @@ __global__ __launch_bounds__(T* teams_of(T)) void layer_norm_rows_kernel(const N
   store_row<E, T, U>(a, l, row, t, mean, rstd, v);
 }
 
-constexpr int kPart = 8192;  // elements of a part: 256 threads, 4 runs each
+constexpr int kPartRuns = 2, kPart = 256 * 8 * kPartRuns;  // elements of a part: 256 threads, 2 runs each
 
 // A workgroup takes one part of one row.
 template <typename E, bool DROP>
@@ -174,10 +174,10 @@ __global__ __launch_bounds__(256) void layer_norm_parts_kernel(const NormArgs<E>
   const int local = blockIdx.x / a.nparts, part = blockIdx.x - local * a.nparts;
   const long long row = a.row0 + local;
   const int run0 = part * (kPart / 8) + threadIdx.x, count = min(kPart, a.n - part * kPart);
-  float v[4][8];
-  Loads<E, 256, 4> l;
+  float v[kPartRuns][8];
+  Loads<E, 256, kPartRuns> l;
   l.fetch(a, row, run0, false);
-  join_row<E, 256, 4, DROP>(a, l, c, row, run0, v);
+  join_row<E, 256, kPartRuns, DROP>(a, l, c, row, run0, v);
   const float mean = row_sum<256>(total(v), lds[0]) / (float)count;
   const float q = row_sum<256>(spread<256>(v, run0, a.n, mean), lds[1]);
   if (threadIdx.x == 0) a.parts[row * a.nparts + part] = make_float2(mean, q);
@@ -190,23 +190,24 @@ __global__ __launch_bounds__(256) void layer_norm_joined_kernel(const NormArgs<E
   const int local = blockIdx.x / a.nparts, part = blockIdx.x - local * a.nparts;
   const long long row = a.row0 + local;
   const int run0 = part * (kPart / 8) + threadIdx.x;
-  float v[4][8];
-  Loads<E, 256, 4> l;
+  float v[kPartRuns][8];
+  Loads<E, 256, kPartRuns> l;
   l.fetch(a, row, run0, true);
-  // every wave joins the row's parts (128 at most, two a lane)
+  // every wave joins the row's parts (256 at most, four a lane)
   const float2* p = a.parts + row * a.nparts;
-  float2 q[2];
-  float count[2];
+  float2 q[4];
+  float count[4], s = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < 4; ++k) {
     const int at = lane + 64 * k;
     q[k] = at < a.nparts ? p[at] : make_float2(0.0f, 0.0f);
     count[k] = at < a.nparts ? (float)min(kPart, a.n - at * kPart) : 0.0f;
+    s += count[k] * q[k].x;
   }
-  const float mean = wave_sum(count[0] * q[0].x + count[1] * q[1].x) / (float)a.n;
+  const float mean = wave_sum(s) / (float)a.n;
   float far = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < 4; ++k) {
     const float d = q[k].x - mean;
     far += q[k].y + (count[k] > 0.0f ? count[k] * d * d : 0.0f);
   }
@@ -215,9 +216,9 @@ __global__ __launch_bounds__(256) void layer_norm_joined_kernel(const NormArgs<E
     a.mean[row] = mean;
     a.rstd[row] = rstd;
   }
-  join_row<E, 256, 4, DROP>(a, l, c, row, run0, v);
+  join_row<E, 256, kPartRuns, DROP>(a, l, c, row, run0, v);
   if (a.s) store_runs<256>(a.s + row * a.lds, a.n, run0, v);
-  store_row<E, 256, 4>(a, l, row, run0, mean, rstd, v);
+  store_row<E, 256, kPartRuns>(a, l, row, run0, mean, rstd, v);
 }
 
 // Rows go in launches of fewer than 2^32 work-items.

@@ -75,7 +75,7 @@ NormPlan plan_layer_norm(const NormGeo& g) {
   if (runs <= 4096) {
     o.row = row_plan(runs);
   } else {
-    o.row = {256, 4, ceil_div(runs, 256 * 4)};
+    o.row = {256, 2, ceil_div(runs, 256 * 2)};
     // a mean and a sum of squares for each part of each row
     o.scratch = ceil_div(g.m * o.row.parts * 8, 256) * 256;
   }
