@@ -20,8 +20,9 @@
  * Everything between loads and stores is float32: s is not rounded before it is
  * normalised, the variance is the mean of squared distances from the mean (never a
  * difference of squares), and every output is rounded once.  The backward pass
- * reads s as the forward stored it.  A row with an infinity or a NaN is NaN; a row
- * of equal values is b (NaN with eps = 0).
+ * reads s as the forward stored it.  A row with an infinity or a NaN is NaN; a row of
+ * equal values is b up to the rounding of its mean (times 1 / sqrt(eps); NaN with
+ * eps = 0 and a mean without rounding).
  *
  * Any m >= 0 is valid: with m = 0 the forward writes nothing, the backward writes
  * zeros to dw and db, and operands of m rows may be NULL.  n and the row strides

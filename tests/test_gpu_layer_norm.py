@@ -204,6 +204,25 @@ def test_backward(dtype, m, n):
     close("dx alone", got[0], want[0], err[0], h(dtype), TINY[dtype])
 
 
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("n", [7, 40, 1001, 3000, 9001, 50_003])
+def test_weight_or_bias_alone_from_odd_elements(dtype, n):
+    """w without b and b without w, each from an odd element of a buffer."""
+    m = 5
+    x, dy, w, b = inputs(dtype, m, n)
+    w, b = (torch.cat([t.new_full((1,), float("nan")), t])[1:] for t in (w, b))
+    for one, two in ((w, None), (None, b)):
+        got = run_forward(dtype, x, None, one, two)
+        check_forward(dtype, x, None, one, two, 0.0, got)
+        grads = run_backward(dtype, x, one, got[2], got[3], dy, None, bias=two is not None,
+                             residual=False)
+        want, err = backward64(x, one, got[2], got[3], dy, None, 0.0)
+        close("dx", grads[0], want[0], err[0], h(dtype), TINY[dtype])
+        at = 2 if two is None else 3
+        close("dw or db", grads[at], want[at], err[at], h(dtype), TINY[dtype])
+        assert grads[5 - at] is None
+
+
 @pytest.mark.parametrize("n", [24, 1000, 3000, 9000, 20_000, 40_000])
 def test_each_gradient_alone(n):
     x, dy, w, _ = inputs("f32", 6, n)

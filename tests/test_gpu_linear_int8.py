@@ -305,6 +305,25 @@ def test_plans_agree():
     assert len(names) >= 3, names
 
 
+@pytest.mark.parametrize("m,n,k,plan", [
+    (1, 5, 17, "stream16.r4"), (3, 1293, 17, "stream16.r8"), (1, 2284, 17, "stream16.r16"),
+    (20, 4, 20, "stream32.r4"), (20, 1117, 18, "stream32.r8"), (24, 2585, 17, "stream32.r16"),
+    (25, 4566, 20, "stream32.r32"), (35, 4, 1372, "split"), (1, 4, 4, "tile64x64"),
+    (2497, 2749, 32, "tile128x128"), (2001, 2003, 1001, "tile128x128"),
+    (1691, 4544, 1856, "tile256x128"), (2229, 3712, 1728, "tile256x256"),
+    (2033, 9750, 1552, "cut"), (1900, 9750, 1552, "cut"), (1981, 4350, 1560, "tile256x256.pack"),
+    (1202, 2505, 3846, "tile64x64.pack")])
+def test_every_plan(m, n, k, plan):
+    """Each kernel at sizes that the plan gives it, ends inside its tiles."""
+    x, xs, w, ws, b, r = operands("bf16", m, n, k, seed=k)
+    use = []
+    got = forward("bf16", x, xs, w, ws, b, r, act="relu", res="before", use=use)
+    name = cf.linear_int8_describe_variant(use[0][0], "bf16")
+    assert plan in name, name
+    want, err = forward64(x, xs, w, ws, b, r, "relu", "before")
+    close(name, got, want, err, "bf16")
+
+
 @pytest.mark.parametrize("m,n,k", [(4, 500, 1024), (64, 256, 4096), (50, 100, 1531), (1000, 1000, 777)])
 def test_rerun_graph_and_streams(m, n, k):
     """The whole path, quantization and product: reruns and replays are equal."""
