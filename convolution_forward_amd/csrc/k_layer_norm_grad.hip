@@ -74,7 +74,7 @@ template <typename E, int T, int U, int TEAMS, bool DROP>
 __global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_kernel(const GradArgs<E> a) {
   constexpr int WAVES = waves_of(T);
   __shared__ float2 red[2][TEAMS * WAVES];
-  __shared__ float columns[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? T * 8 : 1];
+  __shared__ alignas(16) float columns[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? T * 8 : 1];
   const int t = threadIdx.x % T, team = team_of<T>();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const DropCounter c = DROP ? drop_counter(a.d) : DropCounter{0, 0};
@@ -155,12 +155,7 @@ __global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_kernel(const GradArg
     // the teams' sums joined in order, T runs at a time
 #pragma unroll
     for (int k = 0; k < 2 * U; ++k) {
-      float* own = &columns[team][t * 8];
-      const int left = a.n - (t + k % U * T) * 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (left >= 8 || in_tail(e, left))
-          own[left >= 8 ? e : tail_element(e, left)] = k < U ? dw[k % U][e] : db[k % U][e];
+      store_columns(&columns[team][t * 8], a.n - (t + k % U * T) * 8, k < U ? dw[k % U] : db[k % U]);
       __syncthreads();
       for (int i = threadIdx.x; i < T * 8; i += T * TEAMS) {
         const int at = k % U * T * 8 + i;
