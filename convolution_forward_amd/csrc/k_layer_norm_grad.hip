@@ -6,8 +6,9 @@
 // and a second kernel adds the partial rows in order.  So no atomics, and dy and s are
 // read once for both the row's gradient and the columns' sums.  A row needs two sums
 // (of g and of g u) before its first gradient: one exchange through LDS and one barrier
-// a row, none where lanes of a wave hold it.  Rows of more than 8192 elements go in parts
-// of 2048, in two launches: the parts' sums, then the gradients.
+// a row, none where lanes of a wave hold it.  Few rows take one launch in which some
+// workgroups sum columns and the others take rows.  Rows of more than 8192 elements go
+// in parts of 2048, in two launches: the parts' sums, then the gradients.
 #include <algorithm>
 #include <type_traits>
 
@@ -29,6 +30,8 @@ struct GradArgs {
   long long lds, lddy, ldds, lddx, lddr;
   long long row0, m;  // row0: first row of this launch (parts' sums)
   int n, np, parts;
+  int cols;           // workgroups at the front that sum columns (one launch)
+  E *dw, *db;         // theirs; either may be null
   float inv_n;
   DropArgs d;
 };
@@ -171,6 +174,122 @@ __global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_kernel(const GradArg
   }
 }
 
+constexpr int kColumns = 32;  // of a workgroup that sums columns
+
+struct ColumnLds {
+  float2 stats[kOnceRows];  // mean and 1 / deviation of every row
+  float sums[2][32][kColumns];
+};
+
+// dw and db of 32 columns over all rows: 8 lanes of 4 columns a row, 32 rows at a time
+// (the first 256 threads), then these in order.  The last piece of a row that has no 4
+// columns left lies further to the left, over its neighbour's.
+template <typename E>
+__device__ __forceinline__ void sum_columns(const GradArgs<E>& a, int threads, ColumnLds& lds) {
+  constexpr int SLOTS = 32, B = 32 / (int)sizeof(E), Q = 4;  // B loads of each in flight
+  const int m = (int)a.m;
+  for (int i = threadIdx.x; i < m; i += threads) lds.stats[i] = make_float2(a.mean[i], a.rstd[i]);
+  const int lane = threadIdx.x & 7, slot = threadIdx.x >> 3, first = blockIdx.x * kColumns;
+  const int want = first + lane * 4, at = a.n < 4 ? 0 : want < a.n - 4 ? want : a.n - 4;
+  float dw[4] = {0, 0, 0, 0}, db[4] = {0, 0, 0, 0};
+  __syncthreads();
+  if (slot < SLOTS) {
+    for (int base = 0; base < m; base += SLOTS * B) {
+      Few<E, 4> s[B], dy[B];
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        if (base + k / Q * Q * SLOTS >= m) break;  // the same in all threads
+        const int row = base + k * SLOTS + slot;
+        const long long i = row < m ? row : m - 1;
+        const E *ps = a.s + i * a.lds + at, *pd = a.dy + i * a.lddy + at;
+        if (a.n < 4) {
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            if (e < a.n) {
+              s[k].v[e] = ps[e];
+              dy[k].v[e] = pd[e];
+            }
+        } else {
+          s[k] = *reinterpret_cast<const Few<E, 4>*>(ps);
+          dy[k] = *reinterpret_cast<const Few<E, 4>*>(pd);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        if (base + k / Q * Q * SLOTS >= m) break;
+        const int row = base + k * SLOTS + slot;
+        const float2 q = lds.stats[row < m ? row : m - 1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float u = ((float)s[k].v[e] - q.x) * q.y, g = (float)dy[k].v[e];
+          dw[e] = row < m ? fmaf(g, u, dw[e]) : dw[e];
+          db[e] += row < m ? g : 0.0f;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (at + e >= want && at + e < a.n) {
+        lds.sums[0][slot][at + e - first] = dw[e];
+        lds.sums[1][slot][at + e - first] = db[e];
+      }
+  }
+  __syncthreads();
+  const int which = threadIdx.x / kColumns, c = threadIdx.x % kColumns;
+  E* out = which == 0 ? a.dw : a.db;
+  if (which < 2 && first + c < a.n && out) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) t += lds.sums[which][i][c];
+    out[first + c] = (E)t;
+  }
+}
+
+// Few rows: one launch, a row a team, and dw and db by workgroups of their own that read
+// s and dy once more.  These come first and take longest: a unit gets a line of memory
+// in about 4 ns, two lines a row (777 x 1001 float16: 8.5 us, 9.3 in two launches; 64 x 4096
+// 3.2 us, 8.1).  More loads in flight (24 for 16 of 16 bits) changed nothing.
+template <typename E, int T, int U, int TEAMS, bool DROP>
+__global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_once_kernel(const GradArgs<E> a) {
+  __shared__ ColumnLds lds;
+  if ((int)blockIdx.x < a.cols) {
+    sum_columns(a, T * TEAMS, lds);
+    return;
+  }
+  const int t = threadIdx.x % T;
+  const long long row = (long long)(blockIdx.x - a.cols) * TEAMS + team_of<T>();
+  if (row >= a.m) return;  // whole teams; a row of more than a wave has the workgroup to itself
+  const DropCounter c = DROP ? drop_counter(a.d) : DropCounter{0, 0};
+  Runs<E, T, U> s, dy, ds;
+  s.clear();
+  dy.clear();
+  ds.clear();
+  s.fetch(a.s + row * a.lds, a.n, t);
+  dy.fetch(a.dy + row * a.lddy, a.n, t);
+  if (a.ds) ds.fetch(a.ds + row * a.ldds, a.n, t);
+  float u[U][8], g[U][8], w[U][8], along = 0.0f, level = 0.0f;
+#pragma unroll
+  for (int k = 0; k < U; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[k][e] = 1.0f;
+  if (a.w) load_runs<T>(a.w, a.n, t, w);
+  const float mean = a.mean[row], rstd = a.rstd[row];
+  s.get(u);
+  dy.get(g);
+#pragma unroll
+  for (int k = 0; k < U; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      u[k][e] = (u[k][e] - mean) * rstd;
+      g[k][e] *= w[k][e];
+      along = fmaf(g[k][e], u[k][e], along);
+      level += g[k][e];
+    }
+  along = row_sum<T>(along, lds.sums[0][0]);
+  level = row_sum<T>(level, lds.sums[1][0]);
+  finish_row<E, T, U, DROP>(a, c, row, t, rstd, along * a.inv_n, level * a.inv_n, u, g, ds);
+}
+
 constexpr int kPartRuns = 256;  // runs of a part, a thread each
 
 // Sums of g u and g of one part of one row.
@@ -246,24 +365,25 @@ __global__ __launch_bounds__(256) void layer_norm_grad_parts_kernel(const GradAr
   store_columns(p + a.np, left, db);
 }
 
-// Adds the groups' partial rows: 64 columns of dw or db a workgroup, 64 rows at a time
-// (16 lanes of 4 columns a row), then the 64 sums in order.
+// Adds the groups' partial rows: 32 columns of dw or db a workgroup (a line of memory; a
+// unit takes lines at a rate of its own, so few columns to a workgroup), 128 rows at a
+// time, 8 lanes of 4 columns a row, then the 128 sums in order.
 template <typename E>
 __global__ __launch_bounds__(1024) void layer_norm_grad_join_kernel(const float* partials, E* dw,
                                                                     E* db, int groups, int n,
                                                                     int np) {
-  __shared__ float lds[64][64 + 4];
-  const int slot = threadIdx.x >> 4, col = (threadIdx.x & 15) * 4, at = blockIdx.x * 64 + col;
-  const float* p = partials + (blockIdx.y ? np : 0) + at;
+  constexpr int SLOTS = 128, B = 8;
+  __shared__ float lds[SLOTS][kColumns + 4], part[8][kColumns];
+  const int slot = threadIdx.x >> 3, col = (threadIdx.x & 7) * 4, first = blockIdx.x * kColumns;
+  const float* p = partials + (blockIdx.y ? np : 0) + first + col;
   lin::f32x4 s = {0, 0, 0, 0};
-  if (at < np) {
-    constexpr int B = 8;
-    for (int i = slot; i < groups; i += 64 * B) {
+  if (first + col < np) {
+    for (int i = slot; i < groups; i += SLOTS * B) {
       lin::f32x4 q[B];
 #pragma unroll
       for (int k = 0; k < B; ++k)
-        q[k] = i + 64 * k < groups
-                   ? *reinterpret_cast<const lin::f32x4*>(p + (long long)(i + 64 * k) * 2 * np)
+        q[k] = i + SLOTS * k < groups
+                   ? *reinterpret_cast<const lin::f32x4*>(p + (long long)(i + SLOTS * k) * 2 * np)
                    : lin::f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < B; ++k) s += q[k];
@@ -272,13 +392,20 @@ __global__ __launch_bounds__(1024) void layer_norm_grad_join_kernel(const float*
 #pragma unroll
   for (int e = 0; e < 4; ++e) lds[slot][col + e] = s[e];
   __syncthreads();
-  if (threadIdx.x < 64) {
-    const int c = blockIdx.x * 64 + threadIdx.x;
+  const int c = threadIdx.x % kColumns, q = threadIdx.x / kColumns;
+  if (q < 8) {
     float t = 0.0f;
-#pragma unroll 8
-    for (int i = 0; i < 64; ++i) t += lds[i][threadIdx.x];
-    E* out = blockIdx.y ? db : dw;
-    if (c < n && out) out[c] = (E)t;
+#pragma unroll
+    for (int i = 0; i < SLOTS / 8; ++i) t += lds[q * (SLOTS / 8) + i][c];
+    part[q][c] = t;
+  }
+  __syncthreads();
+  E* out = blockIdx.y ? db : dw;
+  if (q == 0 && first + c < n && out) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += part[i][c];
+    out[first + c] = (E)t;
   }
 }
 
@@ -290,16 +417,32 @@ void with_drop(const GradArgs<E>& a, F f) {
 }
 
 template <typename E, int T, int U>
-void launch_grad(const GradArgs<E>& a, unsigned groups, hipStream_t s) {
+void launch_grad(const GradArgs<E>& a, const NormBackwardPlan& pl, bool in_place, hipStream_t s) {
   constexpr int TEAMS = teams_of(T);
-  const dim3 grid(groups), block(T * TEAMS);
+  const dim3 block(T * TEAMS);
   with_drop(a, [&](auto drop) {
-    hipLaunchKernelGGL((layer_norm_grad_kernel<E, T, U, TEAMS, drop.value>), grid, block, 0, s, a);
+    if (!pl.once) {
+      const dim3 grid((unsigned)pl.groups);
+      hipLaunchKernelGGL((layer_norm_grad_kernel<E, T, U, TEAMS, drop.value>), grid, block, 0, s, a);
+      return;
+    }
+    GradArgs<E> q = a;
+    q.cols = a.dw || a.db ? (a.n + kColumns - 1) / kColumns : 0;
+    unsigned rows = a.dx || a.dr ? (unsigned)pl.groups : 0;
+    auto launch = [&](unsigned grid) {
+      hipLaunchKernelGGL((layer_norm_grad_once_kernel<E, T, U, TEAMS, drop.value>), dim3(grid), block,
+                         0, s, q);
+    };
+    if (in_place && q.cols && rows) {  // the columns' sums before the rows overwrite dy
+      launch(q.cols);
+      q.cols = 0;
+    }
+    launch(q.cols + rows);
   });
 }
 
 template <typename E>
-hipError_t grad(GradArgs<E>& a, const NormBackwardPlan& pl, E* dw, E* db, hipStream_t s) {
+hipError_t grad(GradArgs<E>& a, const NormBackwardPlan& pl, bool in_place, hipStream_t s) {
   const unsigned groups = (unsigned)pl.groups;
   if (pl.row.parts) {
     const long long most = 0xff000000LL / 256 / a.parts;  // fewer than 2^32 work-items a launch
@@ -315,24 +458,24 @@ hipError_t grad(GradArgs<E>& a, const NormBackwardPlan& pl, E* dw, E* db, hipStr
       hipLaunchKernelGGL((layer_norm_grad_parts_kernel<E, drop.value>), grid, dim3(256), 0, s, a);
     });
   } else if (pl.row.threads == 8) {
-    launch_grad<E, 8, 1>(a, groups, s);
+    launch_grad<E, 8, 1>(a, pl, in_place, s);
   } else if (pl.row.threads == 16) {
-    launch_grad<E, 16, 1>(a, groups, s);
+    launch_grad<E, 16, 1>(a, pl, in_place, s);
   } else if (pl.row.threads == 32) {
-    launch_grad<E, 32, 1>(a, groups, s);
+    launch_grad<E, 32, 1>(a, pl, in_place, s);
   } else if (pl.row.threads == 64) {
-    if (pl.row.runs == 1) launch_grad<E, 64, 1>(a, groups, s);
-    else launch_grad<E, 64, 2>(a, groups, s);
+    if (pl.row.runs == 1) launch_grad<E, 64, 1>(a, pl, in_place, s);
+    else launch_grad<E, 64, 2>(a, pl, in_place, s);
   } else if (pl.row.threads == 256) {
-    if (pl.row.runs == 1) launch_grad<E, 256, 1>(a, groups, s);
-    else launch_grad<E, 256, 2>(a, groups, s);
+    if (pl.row.runs == 1) launch_grad<E, 256, 1>(a, pl, in_place, s);
+    else launch_grad<E, 256, 2>(a, pl, in_place, s);
   } else {
-    launch_grad<E, 1024, 1>(a, groups, s);
+    launch_grad<E, 1024, 1>(a, pl, in_place, s);
   }
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.partials) return e;
-  hipLaunchKernelGGL((layer_norm_grad_join_kernel<E>), dim3((a.np + 63) / 64, 2), dim3(1024), 0, s,
-                     a.partials, dw, db, (int)groups, a.n, a.np);
+  if (e != hipSuccess || pl.once || !a.partials) return e;
+  hipLaunchKernelGGL((layer_norm_grad_join_kernel<E>), dim3((a.np + kColumns - 1) / kColumns, 2),
+                     dim3(1024), 0, s, a.partials, a.dw, a.db, (int)groups, a.n, a.np);
   return hipGetLastError();
 }
 
@@ -350,6 +493,8 @@ int run(const layer_norm_problem* p, const NormGeo& g, const NormBackwardPlan& p
   a.dx = elements<E>(dx, p->dx_off);
   a.dr = elements<E>(dr, p->dr_off);
   char* sc = static_cast<char*>(scratch);
+  a.dw = elements<E>(dw, p->dw_off);
+  a.db = elements<E>(db, p->db_off);
   a.partials = dw || db ? reinterpret_cast<float*>(sc + pl.partials) : nullptr;
   a.sums = reinterpret_cast<float2*>(sc + pl.sums);
   a.lds = g.lds; a.lddy = g.ldy; a.ldds = g.ldds; a.lddx = g.lddx; a.lddr = g.lddr;
@@ -359,8 +504,8 @@ int run(const layer_norm_problem* p, const NormGeo& g, const NormBackwardPlan& p
   a.parts = (int)pl.row.parts;
   a.inv_n = 1.0f / (float)g.n;
   a.d = drop_args(drop_threshold(p->drop), p->seed, p->offset, step);
-  const hipError_t e = grad<E>(a, pl, elements<E>(dw, p->dw_off), elements<E>(db, p->db_off),
-                               static_cast<hipStream_t>(stream));
+  const bool in_place = (dx && a.dx == a.dy) || (dr && a.dr == a.dy);
+  const hipError_t e = grad<E>(a, pl, in_place, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? CONV_OK : CONV_ERR_DEVICE;
 }
 

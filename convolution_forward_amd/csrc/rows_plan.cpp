@@ -89,14 +89,28 @@ NormBackwardPlan plan_layer_norm_backward(const NormGeo& g) {
   if (runs <= 1024) {
     o.row = row_plan(runs);
     o.teams = o.row.threads >= 256 ? 1 : 256 / o.row.threads;
+    // One launch reads s and dy twice, its column sums by few workgroups at the rate of a
+    // unit: float16 512 x 4096 8 us for 18, 1024 x 2048 11 for 18, 777 x 1001 8.5 for 9.3
+    // (a call 8.5 for 11), 1024 x 63 7.8 for 6.5 (a call 8 for 11), 2048 x 1001 19 for 14;
+    // 512 x 8192 15 for 20, 777 x 8192 24 for 20.
+    o.once = g.m <= (o.row.threads == 1024 ? kOnceRows / 2 : kOnceRows);
+    if (o.once) {
+      o.groups = ceil_div(g.m, o.teams);
+      return o;
+    }
   } else {
     o.row = {256, 1, ceil_div(runs, 256)};
     o.teams = 1;
     o.sums = at;
     at += ceil_div(g.m * o.row.parts * 8, 256) * 256;
   }
-  const int64_t most = o.row.parts ? std::max<int64_t>(1, 4 * kCus / o.row.parts)
-                       : o.row.threads == 1024 ? kCus : o.row.runs == 2 ? 2 * kCus : 4 * kCus;
+  // Every group writes a partial row and the join reads it, too few leave loads unhidden:
+  // eight rows each, within 512 groups and what the registers let run at once (float16
+  // 2048 x 2048: 512 groups 17 us, 1024 20; 16384 x 1001: 1024 or 512 40, 256 54;
+  // 8192 x 2048: 1024 35, 512 37).
+  int64_t most = o.row.parts ? std::max<int64_t>(1, 4 * kCus / o.row.parts)
+                 : o.row.threads == 1024 ? kCus : o.row.runs == 2 ? 2 * kCus : 4 * kCus;
+  if (!o.row.parts) most = std::min(most, std::max<int64_t>(2 * kCus, ceil_div(g.m, 8 * o.teams)));
   o.groups = std::max<int64_t>(1, std::min<int64_t>(most, ceil_div(g.m, o.teams)));
   o.partials = at;
   at += ceil_div(o.groups * 2 * np * 4, 256) * 256;
@@ -297,8 +311,10 @@ int layer_norm_backward_describe_variant(const layer_norm_problem* p, int dtype,
   const int st = layer_norm_validate(p, dtype, &g);
   if (st) return st;
   char row[40], text[80];
-  row_name(plan_layer_norm_backward(g).row, row, sizeof row);
-  snprintf(text, sizeof text, "layer_norm_backward.%s.%s", float_dtype_name(dtype), row);
+  const NormBackwardPlan plan = plan_layer_norm_backward(g);
+  row_name(plan.row, row, sizeof row);
+  snprintf(text, sizeof text, "layer_norm_backward.%s.%s%s", float_dtype_name(dtype), row,
+           plan.once ? ".once" : "");
   return put_name(text, buf, len);
 }
 

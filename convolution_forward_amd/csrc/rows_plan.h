@@ -30,10 +30,15 @@ struct NormPlan {
   int64_t scratch;
 };
 
+// Rows up to which the backward pass can be one launch.
+constexpr int kOnceRows = 1024;
+
 // Backward: `groups` workgroups, each with a partial row of dw and of db; `teams`
-// rows at a time in a workgroup.
+// rows at a time in a workgroup.  once: `groups` workgroups of a row a team, in one
+// launch with others that sum columns; no scratch.
 struct NormBackwardPlan {
   RowPlan row;
+  bool once;
   int teams;
   int64_t groups;     // workgroups along the rows
   int64_t sums;       // byte offsets: row sums (split), partial rows of dw and db

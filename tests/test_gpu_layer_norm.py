@@ -204,6 +204,40 @@ def test_backward(dtype, m, n):
     close("dx alone", got[0], want[0], err[0], h(dtype), TINY[dtype])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m,n", [(1024, 3), (1023, 5), (897, 66), (769, 130), (770, 1001),
+                                 (513, 2047), (1024, 4096), (512, 8190)])
+def test_backward_in_one_launch(dtype, m, n):
+    """Rows up to the limit of one launch, with columns left over; the same over dy."""
+    assert cf.layer_norm_backward_describe_variant(cf.make_layer_norm_problem(m, n), dtype).endswith(".once")
+    backward_of_many_rows(dtype, m, n)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m,n", [(1025, 9), (20_000, 50), (1100, 100), (9000, 250), (2100, 500),
+                                 (5003, 1001), (1025, 2048), (1500, 2047), (2600, 4090), (513, 5000),
+                                 (800, 8192), (40, 20_001), (1100, 8193)])
+def test_backward_of_several_rows_a_group(dtype, m, n):
+    """Rows beyond that limit: partial rows of dw and db, joined; the same over dy."""
+    assert "once" not in cf.layer_norm_backward_describe_variant(cf.make_layer_norm_problem(m, n), dtype)
+    backward_of_many_rows(dtype, m, n)
+
+
+def backward_of_many_rows(dtype, m, n):
+    x, dy, w, b = inputs(dtype, m, n, seed=m + n)
+    ds = inputs(dtype, m, n, seed=5)[0]
+    f = x.float()
+    mean = f.mean(1)
+    rstd = ((f - mean[:, None]) ** 2).mean(1).add(1e-5).rsqrt()
+    got = run_backward(dtype, x, w, mean, rstd, dy, ds, drop=0.3)
+    want, err = backward64(x, w, mean, rstd, dy, ds, 0.3)
+    for name, a, v, e in zip(("dx", "dr", "dw", "db"), got, want, err):
+        close(name, a, v, e, h(dtype), TINY[dtype])
+    over, other = dy.clone(), ds.clone()
+    again = run_backward(dtype, x, w, mean, rstd, over, other, drop=0.3, dx=over, dr=other)
+    assert all(torch.equal(p, q) for p, q in zip(got, again))
+
+
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
 @pytest.mark.parametrize("n", [7, 40, 1001, 3000, 9001, 50_003])
 def test_weight_or_bias_alone_from_odd_elements(dtype, n):

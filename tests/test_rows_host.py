@@ -220,6 +220,9 @@ def test_overlaps():
     assert norm_back(p, dx=at(4)) == norm_back(p, dx=at(5)) == norm_back(p, dr=at(5)) == cf.CONV_OK
     assert norm_back(p, dx=at(4), dr=at(4)) == norm_back(p, dx=at(0)) == OVERLAP
     assert norm_back(p, dw=at(1)) == norm_back(p, dw=at(10)) == norm_back(p, db=at(2)) == OVERLAP
+    assert cf.layer_norm_backward_scratch_size(p, "f16") == 0
+    assert norm_back(p, scratch=None, scratch_bytes=0) == cf.CONV_OK
+    p = cf.make_layer_norm_problem(2000, 40, residual=True, drop=0.1)
     n = cf.layer_norm_backward_scratch_size(p, "f16")
     assert norm_back(p, scratch=at(4) - 256, scratch_bytes=n) == OVERLAP
     assert norm_back(p, scratch_bytes=n - 1) == SCRATCH
