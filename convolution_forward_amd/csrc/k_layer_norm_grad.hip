@@ -8,7 +8,8 @@
 // (of g and of g u) before its first gradient: one exchange through LDS and one barrier
 // a row, none where lanes of a wave hold it.  Few rows take one launch in which some
 // workgroups sum columns and the others take rows.  Rows of more than 8192 elements go
-// in parts of 2048, in two launches: the parts' sums, then the gradients.
+// in parts of 2048, in two launches: the parts' sums (and, of few rows, the columns'),
+// then the gradients.
 #include <algorithm>
 #include <type_traits>
 
@@ -292,11 +293,16 @@ __global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_once_kernel(const Gr
 
 constexpr int kPartRuns = 256;  // runs of a part, a thread each
 
-// Sums of g u and g of one part of one row.
+// Sums of g u and g of one part of one row; of few rows, beside them, dw and db.
 template <typename E>
 __global__ __launch_bounds__(256) void layer_norm_grad_sums_kernel(const GradArgs<E> a) {
-  __shared__ float lds[2][4];
-  const int local = blockIdx.x / a.parts, part = blockIdx.x - local * a.parts;
+  __shared__ ColumnLds columns;
+  if ((int)blockIdx.x < a.cols) {
+    sum_columns(a, 256, columns);
+    return;
+  }
+  float (*lds)[kColumns] = columns.sums[0];
+  const int id = blockIdx.x - a.cols, local = id / a.parts, part = id - local * a.parts;
   const long long row = a.row0 + local;
   const int run0 = part * kPartRuns + threadIdx.x;
   float u[1][8], g[1][8], along = 0.0f, level = 0.0f;
@@ -416,6 +422,12 @@ void with_drop(const GradArgs<E>& a, F f) {
   else f(std::false_type());
 }
 
+// Workgroups that sum columns.
+template <typename E>
+int columns_of(const GradArgs<E>& a) {
+  return a.dw || a.db ? (a.n + kColumns - 1) / kColumns : 0;
+}
+
 template <typename E, int T, int U>
 void launch_grad(const GradArgs<E>& a, const NormBackwardPlan& pl, bool in_place, hipStream_t s) {
   constexpr int TEAMS = teams_of(T);
@@ -427,7 +439,7 @@ void launch_grad(const GradArgs<E>& a, const NormBackwardPlan& pl, bool in_place
       return;
     }
     GradArgs<E> q = a;
-    q.cols = a.dw || a.db ? (a.n + kColumns - 1) / kColumns : 0;
+    q.cols = columns_of(a);
     unsigned rows = a.dx || a.dr ? (unsigned)pl.groups : 0;
     auto launch = [&](unsigned grid) {
       hipLaunchKernelGGL((layer_norm_grad_once_kernel<E, T, U, TEAMS, drop.value>), dim3(grid), block,
@@ -442,9 +454,25 @@ void launch_grad(const GradArgs<E>& a, const NormBackwardPlan& pl, bool in_place
 }
 
 template <typename E>
+void launch_parts(const GradArgs<E>& a, unsigned groups, hipStream_t s) {
+  with_drop(a, [&](auto drop) {
+    hipLaunchKernelGGL((layer_norm_grad_parts_kernel<E, drop.value>), dim3(groups * a.parts), dim3(256), 0,
+                       s, a);
+  });
+}
+
+template <typename E>
 hipError_t grad(GradArgs<E>& a, const NormBackwardPlan& pl, bool in_place, hipStream_t s) {
   const unsigned groups = (unsigned)pl.groups;
-  if (pl.row.parts) {
+  if (pl.row.parts && pl.once) {
+    a.cols = columns_of(a);
+    const bool rows = a.dx || a.dr;
+    const dim3 grid((unsigned)(a.cols + (rows ? a.m * a.parts : 0)));
+    hipLaunchKernelGGL((layer_norm_grad_sums_kernel<E>), grid, dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !rows) return e;
+    launch_parts(a, groups, s);
+  } else if (pl.row.parts) {
     const long long most = 0xff000000LL / 256 / a.parts;  // fewer than 2^32 work-items a launch
     for (long long at = 0; at < a.m; at += most) {
       a.row0 = at;
@@ -453,10 +481,7 @@ hipError_t grad(GradArgs<E>& a, const NormBackwardPlan& pl, bool in_place, hipSt
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    const dim3 grid(groups * a.parts);
-    with_drop(a, [&](auto drop) {
-      hipLaunchKernelGGL((layer_norm_grad_parts_kernel<E, drop.value>), grid, dim3(256), 0, s, a);
-    });
+    launch_parts(a, groups, s);
   } else if (pl.row.threads == 8) {
     launch_grad<E, 8, 1>(a, pl, in_place, s);
   } else if (pl.row.threads == 16) {
@@ -495,7 +520,7 @@ int run(const layer_norm_problem* p, const NormGeo& g, const NormBackwardPlan& p
   char* sc = static_cast<char*>(scratch);
   a.dw = elements<E>(dw, p->dw_off);
   a.db = elements<E>(db, p->db_off);
-  a.partials = dw || db ? reinterpret_cast<float*>(sc + pl.partials) : nullptr;
+  a.partials = (dw || db) && !pl.once ? reinterpret_cast<float*>(sc + pl.partials) : nullptr;
   a.sums = reinterpret_cast<float2*>(sc + pl.sums);
   a.lds = g.lds; a.lddy = g.ldy; a.ldds = g.ldds; a.lddx = g.lddx; a.lddr = g.lddr;
   a.m = g.m;

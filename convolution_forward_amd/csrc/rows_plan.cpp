@@ -89,20 +89,22 @@ NormBackwardPlan plan_layer_norm_backward(const NormGeo& g) {
   if (runs <= 1024) {
     o.row = row_plan(runs);
     o.teams = o.row.threads >= 256 ? 1 : 256 / o.row.threads;
-    // One launch reads s and dy twice, its column sums by few workgroups at the rate of a
-    // unit: float16 512 x 4096 8 us for 18, 1024 x 2048 11 for 18, 777 x 1001 8.5 for 9.3
-    // (a call 8.5 for 11), 1024 x 63 7.8 for 6.5 (a call 8 for 11), 2048 x 1001 19 for 14;
-    // 512 x 8192 15 for 20, 777 x 8192 24 for 20.
-    o.once = g.m <= (o.row.threads == 1024 ? kOnceRows / 2 : kOnceRows);
-    if (o.once) {
-      o.groups = ceil_div(g.m, o.teams);
-      return o;
-    }
   } else {
     o.row = {256, 1, ceil_div(runs, 256)};
     o.teams = 1;
     o.sums = at;
     at += ceil_div(g.m * o.row.parts * 8, 256) * 256;
+  }
+  // Workgroups that sum columns read s and dy once more, each at the rate of a unit, but
+  // spare the partial rows and a launch.  float16, us for those of partial rows: 512 x 4096
+  // 8 for 18, 1024 x 4096 13 for 20, 1024 x 2048 11 for 18, 777 x 1001 8.5 for 9.3 (a call
+  // 8.5 for 11), 1024 x 63 7.8 for 6.5 (a call 8 for 11), 2048 x 1001 19 for 14; 512 x 8192
+  // 15 for 20, 777 x 8192 24 for 20; 32 x 50176 11 for 23, 128 x 32768 17 for 24, 512 x
+  // 16384 29 for 26.
+  o.once = g.m <= kOnceRows && g.m * g.n <= 1 << 22;
+  if (o.once && !o.row.parts) {
+    o.groups = ceil_div(g.m, o.teams);
+    return o;
   }
   // Every group writes a partial row and the join reads it, too few leave loads unhidden:
   // eight rows each, within 512 groups and what the registers let run at once (float16
@@ -113,7 +115,7 @@ NormBackwardPlan plan_layer_norm_backward(const NormGeo& g) {
   if (!o.row.parts) most = std::min(most, std::max<int64_t>(2 * kCus, ceil_div(g.m, 8 * o.teams)));
   o.groups = std::max<int64_t>(1, std::min<int64_t>(most, ceil_div(g.m, o.teams)));
   o.partials = at;
-  at += ceil_div(o.groups * 2 * np * 4, 256) * 256;
+  if (!o.once) at += ceil_div(o.groups * 2 * np * 4, 256) * 256;
   o.scratch = at;
   return o;
 }

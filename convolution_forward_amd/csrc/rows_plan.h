@@ -30,12 +30,13 @@ struct NormPlan {
   int64_t scratch;
 };
 
-// Rows up to which the backward pass can be one launch.
+// Rows up to which dw and db can be summed by workgroups of their own, all rows each.
 constexpr int kOnceRows = 1024;
 
 // Backward: `groups` workgroups, each with a partial row of dw and of db; `teams`
-// rows at a time in a workgroup.  once: `groups` workgroups of a row a team, in one
-// launch with others that sum columns; no scratch.
+// rows at a time in a workgroup.  once: dw and db by
+// workgroups of their own and no partial rows; whole rows (`groups` workgroups of a row
+// a team) then go in the same launch and need no scratch.
 struct NormBackwardPlan {
   RowPlan row;
   bool once;

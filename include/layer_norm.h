@@ -67,7 +67,7 @@ int layer_norm_backward_scratch_size(const layer_norm_problem* p, int dtype, uin
 
 /* Name of the kernel plan, e.g. "layer_norm.bf16.rows256x2" (rows held by 256 threads,
  * up to 2 runs of 8 elements each), "layer_norm.f32.split13" (rows cut into 13 parts),
- * "layer_norm_backward.f16.rows64x2.once" (rows and columns in one launch).
+ * "layer_norm_backward.f16.rows64x2.once" (dw and db beside the rows, in one pass).
  * CONV_ERR_ARG when len is too small, or the validation status of the problem. */
 int layer_norm_describe_variant(const layer_norm_problem* p, int dtype, char* buf, uint64_t len);
 int layer_norm_backward_describe_variant(const layer_norm_problem* p, int dtype, char* buf,

@@ -206,17 +206,19 @@ def test_backward(dtype, m, n):
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("m,n", [(1024, 3), (1023, 5), (897, 66), (769, 130), (770, 1001),
-                                 (513, 2047), (1024, 4096), (512, 8190)])
-def test_backward_in_one_launch(dtype, m, n):
-    """Rows up to the limit of one launch, with columns left over; the same over dy."""
+                                 (513, 2047), (1024, 4096), (512, 8190), (40, 20_001), (300, 8193),
+                                 (3, 100_003)])
+def test_backward_of_few_rows(dtype, m, n):
+    """Rows up to the limit of columns summed beside them, with columns left over; the
+    same over dy."""
     assert cf.layer_norm_backward_describe_variant(cf.make_layer_norm_problem(m, n), dtype).endswith(".once")
     backward_of_many_rows(dtype, m, n)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("m,n", [(1025, 9), (20_000, 50), (1100, 100), (9000, 250), (2100, 500),
-                                 (5003, 1001), (1025, 2048), (1500, 2047), (2600, 4090), (513, 5000),
-                                 (800, 8192), (40, 20_001), (1100, 8193)])
+                                 (5003, 1001), (1025, 2048), (1500, 2047), (2600, 4090), (1030, 5000),
+                                 (800, 8192), (1100, 8193), (600, 20_001)])
 def test_backward_of_several_rows_a_group(dtype, m, n):
     """Rows beyond that limit: partial rows of dw and db, joined; the same over dy."""
     assert "once" not in cf.layer_norm_backward_describe_variant(cf.make_layer_norm_problem(m, n), dtype)
