@@ -88,8 +88,12 @@ __device__ __forceinline__ DropCounter drop_counter(const DropArgs& a) {
   return {(unsigned)c, (unsigned)(c >> 32)};
 }
 
+__device__ __forceinline__ unsigned xor3(unsigned a, unsigned b, unsigned c) {
+  return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
+}
+
 // Philox4x32-10: 8 numbers of 16 bits for run `run` of row `row`.  20 products of 32
-// bits (low and high half from one instruction) and 40 logic operations for 8 elements.
+// bits (low and high half from one instruction) and 20 logic operations for 8 elements.
 struct DropBits {
   unsigned w[4];
 };
@@ -100,9 +104,9 @@ __device__ __forceinline__ DropBits drop_bits(const DropArgs& a, DropCounter c, 
   for (int i = 0; i < 10; ++i) {
     const unsigned long long p = (unsigned long long)x0 * 0xD2511F53u;
     const unsigned long long q = (unsigned long long)x2 * 0xCD9E8D57u;
-    x0 = (unsigned)(q >> 32) ^ x1 ^ k0;
+    x0 = xor3((unsigned)(q >> 32), x1, k0);
     x1 = (unsigned)q;
-    x2 = (unsigned)(p >> 32) ^ x3 ^ k1;
+    x2 = xor3((unsigned)(p >> 32), x3, k1);
     x3 = (unsigned)p;
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;

@@ -53,7 +53,7 @@ typedef struct dropout_problem {
     int32_t reserved;                     /* 0 */
 } dropout_problem;
 
-/* Name of the kernel plan ("dropout.bf16.runs4": 4 runs of 8 elements a thread).
+/* Name of the kernel plan ("dropout.f32.runs2": 2 runs of 8 elements a thread).
  * Shape-only. */
 int dropout_describe_variant(const dropout_problem* p, int dtype, char* buf, uint64_t len);
 

@@ -75,6 +75,17 @@ def test_forward_and_backward(dtype, m, n):
         check(dtype, backward(dtype, x, drop), x, None, keep, drop)
 
 
+@pytest.mark.parametrize("m,n", [(2051, 4097), (4_200_000, 2), (9, 1_000_003)])
+def test_several_runs_a_thread(m, n):
+    """Float32 of 2^20 runs and more."""
+    assert cf.dropout_describe_variant(cf.make_dropout_problem(m, n, 0.1), "f32").endswith("runs2")
+    g = gen(m)
+    x, r = rnd(g, "f32", m, n), rnd(g, "f32", m, n)
+    keep = keep_of(m, n, 0.1)
+    check("f32", forward("f32", x, r, 0.1), x, r, keep, 0.1)
+    check("f32", backward("f32", x, 0.1), x, None, keep, 0.1)
+
+
 @pytest.mark.parametrize("drop", [0.0, 1.0, 2.0 ** -16, 1 - 2.0 ** -16, 2.0 ** -18, 0.9])
 def test_probabilities(drop):
     g = gen(1)
