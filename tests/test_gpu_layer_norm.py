@@ -421,7 +421,8 @@ def test_gradients_against_differences(n):
         assert abs(float((grad.double() * e).sum()) - want) <= 500 * U * size + 1e-7 * abs(want) + 1e-6
 
 
-@pytest.mark.parametrize("m,n", [(70, 600), (9, 4096), (3, 20_000), (4, 50_000)])
+@pytest.mark.parametrize("m,n", [(70, 600), (9, 4096), (3, 20_000), (4, 50_000),
+                                 (1100, 264), (300, 20_000)])
 def test_rerun_graph_and_streams(m, n):
     """Reruns are equal bit for bit; a captured forward and backward, replayed with new
     inputs and a step that moves on, equals the eager calls, also with eager work and a
