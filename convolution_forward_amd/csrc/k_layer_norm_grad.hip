@@ -298,16 +298,19 @@ __global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_once_kernel(const Gr
 
 constexpr int kPartRuns = 256;  // runs of a part, a thread each
 
-// Sums of g u and g of one part of one row; of few rows, beside them, dw and db.
-template <typename E>
+// Sums of g u and g of one part of one row.  FEW rows: dw and db beside them, with the
+// registers and LDS of that (many rows with them: 2048 x 16384 bfloat16 99 us for 96).
+template <typename E, bool FEW>
 __global__ __launch_bounds__(256) void layer_norm_grad_sums_kernel(const GradArgs<E> a) {
-  __shared__ ColumnLds columns;
-  if ((int)blockIdx.x < a.cols) {
-    sum_columns(a, 256, columns);
-    return;
+  if constexpr (FEW) {
+    __shared__ ColumnLds columns;
+    if ((int)blockIdx.x < a.cols) {
+      sum_columns(a, 256, columns);
+      return;
+    }
   }
-  float (*lds)[kColumns] = columns.sums[0];
-  const int id = blockIdx.x - a.cols, local = id / a.parts, part = id - local * a.parts;
+  __shared__ float lds[2][4];
+  const int id = blockIdx.x - (FEW ? a.cols : 0), local = id / a.parts, part = id - local * a.parts;
   const long long row = a.row0 + local;
   const int run0 = part * kPartRuns + threadIdx.x;
   float u[1][8], g[1][8], along = 0.0f, level = 0.0f;
@@ -473,7 +476,7 @@ hipError_t grad(GradArgs<E>& a, const NormBackwardPlan& pl, bool in_place, hipSt
     a.cols = columns_of(a);
     const bool rows = a.dx || a.dr;
     const dim3 grid((unsigned)(a.cols + (rows ? a.m * a.parts : 0)));
-    hipLaunchKernelGGL((layer_norm_grad_sums_kernel<E>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((layer_norm_grad_sums_kernel<E, true>), grid, dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !rows) return e;
     launch_parts(a, groups, s);
@@ -482,7 +485,7 @@ hipError_t grad(GradArgs<E>& a, const NormBackwardPlan& pl, bool in_place, hipSt
     for (long long at = 0; at < a.m; at += most) {
       a.row0 = at;
       const dim3 grid((unsigned)(std::min(most, a.m - at) * a.parts));
-      hipLaunchKernelGGL((layer_norm_grad_sums_kernel<E>), grid, dim3(256), 0, s, a);
+      hipLaunchKernelGGL((layer_norm_grad_sums_kernel<E, false>), grid, dim3(256), 0, s, a);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
