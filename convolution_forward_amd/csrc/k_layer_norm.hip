@@ -229,13 +229,10 @@ __global__ __launch_bounds__(256) void layer_norm_joined_kernel(const NormArgs<E
   store_row<E, 256, kPartRuns>(a, l, row, run0, mean, rstd, v);
 }
 
-// Rows go in launches of fewer than 2^32 work-items.
-constexpr long long kMostItems = 0xff000000LL;
-
-// f(args, rows) for the rows of every launch, `each` work-items a row.
+// f(args, rows) for the rows of every launch, `each` work-items a row, `teams` rows a workgroup.
 template <typename E, typename F>
-hipError_t by_rows(NormArgs<E> a, long long each, F f) {
-  const long long most = kMostItems / each;
+hipError_t by_rows(NormArgs<E> a, long long each, int teams, F f) {
+  const long long most = rows_of_launch(each, teams);
   for (long long at = 0; at < a.m; at += most) {
     a.row0 = at;
     f(a, (unsigned)std::min(most, a.m - at));
@@ -255,7 +252,7 @@ void with_drop(const NormArgs<E>& a, F f) {
 template <typename E, int T, int U>
 hipError_t launch_rows(const NormArgs<E>& args, hipStream_t s) {
   constexpr int TEAMS = teams_of(T);
-  return by_rows(args, T, [&](const NormArgs<E>& a, unsigned rows) {
+  return by_rows(args, T, TEAMS, [&](const NormArgs<E>& a, unsigned rows) {
     const dim3 grid((rows + TEAMS - 1) / TEAMS), block(T * TEAMS);
     with_drop(a, [&](auto drop) {
       hipLaunchKernelGGL((layer_norm_rows_kernel<E, T, U, drop.value>), grid, block, 0, s, a);
@@ -265,14 +262,14 @@ hipError_t launch_rows(const NormArgs<E>& args, hipStream_t s) {
 
 template <typename E>
 hipError_t launch_parts(const NormArgs<E>& args, hipStream_t s) {
-  const hipError_t e = by_rows(args, 256 * args.nparts, [&](const NormArgs<E>& a, unsigned rows) {
+  const hipError_t e = by_rows(args, 256 * args.nparts, 1, [&](const NormArgs<E>& a, unsigned rows) {
     const dim3 grid(rows * a.nparts), block(256);
     with_drop(a, [&](auto drop) {
       hipLaunchKernelGGL((layer_norm_parts_kernel<E, drop.value>), grid, block, 0, s, a);
     });
   });
   if (e != hipSuccess) return e;
-  return by_rows(args, 256 * args.nparts, [&](const NormArgs<E>& a, unsigned rows) {
+  return by_rows(args, 256 * args.nparts, 1, [&](const NormArgs<E>& a, unsigned rows) {
     const dim3 grid(rows * a.nparts), block(256);
     with_drop(a, [&](auto drop) {
       hipLaunchKernelGGL((layer_norm_joined_kernel<E, drop.value>), grid, block, 0, s, a);

@@ -499,7 +499,7 @@ hipError_t grad(GradArgs<E>& a, const NormBackwardPlan& pl, bool in_place, hipSt
     if (e != hipSuccess || !rows) return e;
     launch_parts(a, groups, s);
   } else if (pl.row.parts) {
-    const long long most = 0xff000000LL / 256 / a.parts;  // fewer than 2^32 work-items a launch
+    const long long most = rows_of_launch(256 * a.parts, 1);
     for (long long at = 0; at < a.m; at += most) {
       a.row0 = at;
       const dim3 grid((unsigned)(std::min(most, a.m - at) * a.parts));

@@ -145,7 +145,7 @@ __global__ __launch_bounds__(T* teams_of(T)) void quantize_kernel(const QuantArg
 template <typename E, int T, int U, bool LONG>
 hipError_t launch(QuantArgs<E> a, hipStream_t s) {
   constexpr int TEAMS = teams_of(T);
-  const long long most = 0xff000000LL / T;  // fewer than 2^32 work-items a launch
+  const long long most = rows_of_launch(T, TEAMS);
   for (long long at = 0; at < a.m; at += most) {
     a.row0 = at;
     const long long rows = std::min(most, a.m - at);

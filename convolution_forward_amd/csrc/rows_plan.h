@@ -59,6 +59,14 @@ struct QuantGeo {
   RowPlan row;  // parts > 0: the row is read twice
 };
 
+// Rows of one launch of a row kernel: fewer than 2^32 work-items, `items` a row, in whole
+// workgroups of `teams` rows.  A kernel knows the last row of the call, not that of its launch:
+// a last workgroup with room left would take rows of the next launch, which would then
+// be worked on twice, outputs over inputs as well.
+constexpr int64_t rows_of_launch(int64_t items, int64_t teams) {
+  return 0xff000000LL / items / teams * teams;
+}
+
 // Drop threshold of 16 random bits.
 int drop_threshold(float p);
 
