@@ -11,10 +11,12 @@
  *                  activation, y = act(z); or z without r, y = fl( act(z) + r )
  *
  * A row whose largest |x| is below 2^-100 has scale 0 and q 0 (fl(127 / a) may not be
- * finite there); a row with an infinity or a NaN has scale NaN and q 0, so that its
- * outputs are NaN.  The sum over k is exact (int32), rounded once to float32; the
- * product of the two scales, the product with the sum and every step after it are
- * float32, and y is rounded once to its type.
+ * finite there); a row with an infinity or a NaN has scale NaN and q 0, so that z of
+ * that row is NaN, and y with it but for relu: as in linear.h, relu(NaN) is 0, so such a
+ * token comes out as zeros (or as r, with the residual after), and only its scale tells.
+ * The sum over k is exact (int32), rounded once to float32; the product of the two scales,
+ * the product with the sum and every step after it are float32, and y is rounded once to
+ * its type.
  *
  * Layouts (row-major; rows ld elements apart, ld = 0 meaning dense):
  *   quantize_rows  x [m, n] of the call's element type, q [m, n] int8, scale [m] float32
