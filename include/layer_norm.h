@@ -22,7 +22,9 @@
  * difference of squares), and every output is rounded once.  The backward pass
  * reads s as the forward stored it.  A row with an infinity or a NaN is NaN; a row of
  * equal values is b up to the rounding of its mean (times 1 / sqrt(eps); NaN with
- * eps = 0 and a mean without rounding).
+ * eps = 0 and a mean without rounding).  The sums have float32's range: a row whose
+ * sum passes it is NaN, one whose sum of squared distances does (all of them 2^64 /
+ * sqrt(n), say) has rstd 0 and is b.
  *
  * Any m >= 0 is valid: with m = 0 the forward writes nothing, the backward writes
  * zeros to dw and db, and operands of m rows may be NULL.  n and the row strides
