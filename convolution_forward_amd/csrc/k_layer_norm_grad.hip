@@ -12,9 +12,11 @@
 // then the gradients.
 //
 // bfloat16 8192 x 4096 with dropout, residual and ds: 72 us (4.6 TB/s), of which the join
-// 5; without them 47.  The loop is bound by memory and by what two workgroups of 140
-// registers a thread keep in flight on a unit.  In parts, 2048 x 16384: 96 us (one
-// workgroup of 1024 threads by 2 runs spilled: 193).
+// 5; without them 46.  The loop is bound by memory, and two workgroups on a unit ask for
+// about as much of it as there is: the 16-bit kernels' 140 to 150 registers allow a third,
+// but 768 groups, with half as many partial rows again, take 75 and 49 us (8192 x 3000: 60
+// and 39 for 61 and 42).  float32's 204 to 212 registers allow two.  In parts, 2048 x 16384:
+// 95 us (one workgroup of 1024 threads by 2 runs spilled: 193).
 #include <algorithm>
 #include <type_traits>
 
@@ -271,8 +273,10 @@ __device__ __forceinline__ void sum_columns(const GradArgs<E>& a, int threads, C
 
 // Few rows: one launch, a row a team, and dw and db by workgroups of their own that read
 // s and dy once more.  These come first and take longest: a unit gets a line of memory
-// in about 4 ns, two lines a row (777 x 1001 float16: 8.5 us, 9.3 in two launches; 64 x 4096
-// 3.2 us, 8.1).  More loads in flight (24 for 16 of 16 bits) changed nothing.
+// in about 4 ns, two lines a row (float16 777 x 1001: kernels 8.5 us, as long as the two
+// launches', a call 9.1 for 11.8; 64 x 4096 kernels 2.8 us for 7.2).  More loads in flight (24
+// for 16 of 16 bits) changed nothing.  The sums' exchange at the end has several slots of
+// a wave in the same banks, once a workgroup (192 cycles of conflicts).
 template <typename E, int T, int U, int TEAMS, bool DROP>
 __global__ __launch_bounds__(T* TEAMS) void layer_norm_grad_once_kernel(const GradArgs<E> a) {
   __shared__ ColumnLds lds;

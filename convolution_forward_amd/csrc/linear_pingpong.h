@@ -352,9 +352,11 @@ __global__ __launch_bounds__(512) void linear_pingpong_kernel(const ProductArgs 
   K::run(a, xcd_logical(blockIdx.x, gridDim.x), smem);
 }
 
-// Tiles of 256 x 256, the last of them cut in two: where fewer than half of the units
+// Tiles of 256 x 256, the last of them cut in two: where at most half of the units
 // would have a tile in the last round, twice as many have half a one.  8192 x 11008 x
-// 4096 of 8 bits, 5.4 rounds: 322 us for 340.
+// 4096 of 8 bits, 5.4 rounds: 322 us for 340.  Of 16-bit outputs the 256 x 256 tile of 8-bit
+// operands takes 255 registers and keeps two more in memory: written once behind
+// the loop, read in the rounds of an epilogue that stores part of a tile.
 template <typename E, typename O>
 __global__ __launch_bounds__(512) void linear_cut_kernel(const ProductArgs a, int whole) {
   using Whole = lin::PingPong<E, false, false, 256, false, false, O>;

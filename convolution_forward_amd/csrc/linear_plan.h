@@ -99,8 +99,8 @@ struct PairPlan {
   double time;         // estimated, us
   ProductPlan dx, dw;  // of each alone; for TILE_64 in that launch
 };
-// 8-bit products: tiles of 256 x 256 of the last round that are cut in two (0: none).  Fewer
-// than half of the units would have one in it (8192 x 11008 x 4096: 322 us for 340).
+// 8-bit products: tiles of 256 x 256 of the last round that are cut in two (0: none).  At most
+// half of the units would have one in it (8192 x 11008 x 4096: 322 us for 340).
 inline int64_t cut_tiles(int64_t tiles) {
   const int64_t rest = tiles % 256;
   return tiles > 256 && rest <= 128 ? rest : 0;

@@ -189,12 +189,9 @@ __device__ __forceinline__ void fetch_tail(const E* p, int left, Eight<E>& q) {
     }
   }
 }
-// Whether slot e of a partial run holds an element, and which of the run it is.
+// Whether slot e of a partial run holds an element.
 __device__ __forceinline__ bool in_tail(int e, int left) {
   return e < 4 ? left & 4 : e < 6 ? left & 2 : e == 6 ? left & 1 : false;
-}
-__device__ __forceinline__ int tail_element(int e, int left) {
-  return e < 4 ? e : e < 6 ? (left & 4) + e - 4 : left & 6;
 }
 template <typename E>
 __device__ __forceinline__ void store_tail(E* p, int left, const float (&v)[8]) {
@@ -215,8 +212,9 @@ __device__ __forceinline__ void store_tail(E* p, int left, const float (&v)[8]) 
 
 // Runs run0, run0 + T, .. of a row of n elements, as they lie in memory: fetched ahead of
 // their use.  Runs past the end stay as they were made: zeros.  (16-bit rows at odd
-// elements are loaded as they lie, which costs: 16384 x 2047 forward 38 us for 30 at even
-// ones, backward 67 for 49.  Aligned words and a lane exchange in their place took 49 and 54.)
+// elements are loaded as they lie, which costs: bfloat16 16384 x 2047 forward 39 us, backward
+// 68, where 2046 takes 30 and 48, 2048 27 and 47.  Aligned words and a lane exchange in their
+// place took 49 and 54.)
 template <typename E, int T, int U>
 struct Runs {
   Eight<E> q[U];

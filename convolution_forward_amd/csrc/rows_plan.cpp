@@ -22,7 +22,10 @@ bool off8(const void* p) { return (uintptr_t)p % 8 != 0; }
 // Threads that hold a row of up to 32768 elements, one run of 8 each where that does
 // not take too many: more runs a thread cost registers, and with them loads in flight
 // (bf16 16384 x 2048: 64 threads of 4 runs 63 us, 256 of 1 53; 4096 x 8192: 256 of 4 63,
-// 1024 of 1 54).
+// 1024 of 1 54).  A row that does not fill its threads leaves some without loads, which
+// weighs most just above 4096 (widths of 33.5 million elements in all, no dropout or residual:
+// bfloat16 forward 5.2 TB/s at 4096, 3.1 at 4104, 3.5 at 5120, 4.2 at 7168, 4.4 at 8192; backward
+// 4.4, 3.8, 4.1, 4.4, 4.4; float32 forward 5.1, 4.4, 4.6, 4.8, 5.0, backward 4.8 to 5.2 throughout).
 RowPlan row_plan(int64_t runs) {
   if (runs <= 8) return {8, 1, 0};
   if (runs <= 16) return {16, 1, 0};
@@ -96,11 +99,14 @@ NormBackwardPlan plan_layer_norm_backward(const NormGeo& g) {
     at += ceil_div(g.m * o.row.parts * 8, 256) * 256;
   }
   // Workgroups that sum columns read s and dy once more, each at the rate of a unit, but
-  // spare the partial rows and a launch.  float16, us for those of partial rows: 512 x 4096
-  // 8 for 18, 1024 x 4096 13 for 20, 1024 x 2048 11 for 18, 777 x 1001 8.5 for 9.3 (a call
-  // 8.5 for 11), 1024 x 63 7.8 for 6.5 (a call 8 for 11), 2048 x 1001 19 for 14; 512 x 8192
-  // 15 for 20, 777 x 8192 24 for 20; 32 x 50176 11 for 23, 128 x 32768 17 for 24, 512 x
-  // 16384 29 for 26.
+  // spare the partial rows and a launch.  Kernels, us for those of partial rows, float16
+  // and float32: 512 x 4096 7.8 for 17 and 8.9 for 18, 1024 x 4096 14 for 19 and 15 for 18, 1024 x
+  // 2048 11 for 13 and 12 for 14, 512 x 8192 14 for 18 and 18 for 18, 32 x 50176 11 for 23 and
+  // 13 for 23, 256 x 16384 16 for 22 and 19 for 23.  Narrow rows near the limit lose some of
+  // the kernels' time, 777 x 1001 8.5 for 8.5 and 9.5 for 9.0, 1024 x 1000 9.8 for 8.8 and 11 for
+  // 9.2, 1000 x 240 7.0 for 5.6 and 6.9 for 5.7, and gain a launch where calls are not replayed
+  // from a graph (float16 777 x 1001 9.1 for 11.8, 1024 x 63 8 for 11).  Beyond the limits,
+  // float16: 2048 x 1001 19 for 14, 777 x 8192 24 for 20, 512 x 16384 29 for 26.
   o.once = g.m <= kOnceRows && g.m * g.n <= 1 << 22;
   if (o.once && !o.row.parts) {
     o.groups = ceil_div(g.m, o.teams);
